@@ -13,6 +13,7 @@ no GPU is present, calls fail loudly.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -41,6 +42,18 @@ class MapDesc(ctypes.Structure):
     _fields_ = [("d", ctypes.c_int64), ("d_out", ctypes.c_int64), ("k", ctypes.c_int64),
                 ("dtype", ctypes.c_int), ("W", ctypes.c_void_p), ("V", ctypes.c_void_p),
                 ("M", ctypes.c_void_p), ("gram", ctypes.c_void_p)]
+
+
+class CacheDesc(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int64), ("n_heads", ctypes.c_int64),
+                ("head_dim", ctypes.c_int64), ("dtype", ctypes.c_int), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("K", ctypes.c_void_p),
+                ("V", ctypes.c_void_p)]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int), ("eps", ctypes.c_float), ("weight", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p)]
 
 
 _lib = None
@@ -78,6 +91,12 @@ def lib() -> ctypes.CDLL:
         "gsi_basis_coherence": [vp, vp, i64, i64, vp, vp, vp],
         "gsi_basis_export": [vp, i64, i64, vp, ctypes.c_int, vp],
         "gsi_residual_check": [P(MapDesc), vp, i64, vp, vp, vp, vp, vp, sz, vp],
+        "gsi_paged_plan": [vp, vp, i64, vp, i64, vp, i64, vp, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp],
+        "gsi_cache_append": [P(CacheDesc), vp, ctypes.c_int, i64, vp, i64, i64, vp, vp],
+        "gsi_paged_attention": [P(CacheDesc), vp, i64, i64, i64, vp, vp, vp, i64, i64, i64, f32, ctypes.c_int, i64, vp,
+                                vp, sz, vp],
+        "gsi_norm_residual": [vp, ctypes.c_int, vp, ctypes.c_int, i64, i64, f32, P(NormDesc), vp, i64, vp, P(NormDesc),
+                              vp, vp, ctypes.c_int, vp],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -89,6 +108,8 @@ def lib() -> ctypes.CDLL:
     L.gsi_residual_check_work_bytes.restype = sz
     L.gsi_basis_step_work_bytes.argtypes = [i64, i64, i64]
     L.gsi_basis_step_work_bytes.restype = sz
+    L.gsi_paged_attention_workspace_size.argtypes = [P(CacheDesc), i64]
+    L.gsi_paged_attention_workspace_size.restype = sz
     L.gsi_last_error.argtypes = []
     L.gsi_last_error.restype = ctypes.c_char_p
     L.gsi_debug_fail_after.argtypes = [ctypes.c_int]
@@ -126,6 +147,11 @@ def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _raw_stream(stream, t):
+    """The stream's handle as a number (the current stream of t's device by default)."""
+    return stream.cuda_stream if stream is not None else torch.cuda.current_stream(t.device).cuda_stream
 
 
 def _dtype_code(dt: torch.dtype) -> int:
@@ -421,3 +447,241 @@ def stack_raw(args, n, T, eps, workspace, stream=None, mode: str = "auto"):
     """gsi_stack_ex on prepared ctypes arrays (no per-call Python allocation)."""
     _check(lib().gsi_stack_ex(args[0], n, args[1], T, float(eps), args[2], args[3],
                               _ptr(workspace), workspace.numel(), STACK_MODES[mode], _stream(stream)))
+
+
+# ---------------------------------------------------------------- serving operators
+# What stands between the gated maps of a decoder layer: pages and slots of a
+# step's tokens, the paged key/value cache, attention over it, and the norms
+# with gate and residual.  Outputs and workspaces may be passed in (a serving
+# loop keeps them); what is not passed is allocated by PyTorch on `stream`.
+
+PLAN_BAD_LENGTH, PLAN_TABLE_FULL, PLAN_NO_PAGES, PLAN_TOO_MANY_TOKENS = 1, 2, 4, 8
+NORMS = {"none": 0, "rms": 1, "layer": 2}
+
+
+def _on_stream(stream):
+    """Allocations inside belong to the stream that uses them."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _ints(name, t, n, dtype=torch.int32):
+    """A contiguous integer CUDA tensor of n elements."""
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of {n} {dtype}, not {tuple(t.shape)} {t.dtype}")
+
+
+def _like(name, t, shape, dtype):
+    """A contiguous CUDA tensor of this shape and type."""
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or t.shape != shape:
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of {tuple(shape)} {dtype}, "
+                         f"not {tuple(t.shape)} {t.dtype}")
+
+
+@dataclass
+class PagedCache:
+    """Keys and values in pages: two (pages, heads, page_size, head_dim) tensors
+    of one dtype (float32 or bfloat16) and one layout.  Only head_dim has to be
+    contiguous: a (pages, page_size, heads, head_dim) buffer is passed as its
+    permuted view."""
+    K: torch.Tensor
+    V: torch.Tensor
+
+    @classmethod
+    def empty(cls, n_pages: int, n_heads: int, page_size: int, head_dim: int, dtype=torch.bfloat16, device="cuda"):
+        return cls(*(torch.empty(n_pages, n_heads, page_size, head_dim, dtype=dtype, device=device) for _ in range(2)))
+
+    def desc(self) -> CacheDesc:
+        K, V = self.K, self.V
+        st = K.stride()
+        if K.dim() != 4 or K.shape != V.shape or st != V.stride() or K.dtype is not V.dtype:
+            raise ValueError("K and V must be two (pages, heads, page_size, head_dim) tensors of one dtype and layout")
+        if not K.is_cuda or not V.is_cuda or st[3] != 1:
+            raise ValueError("K and V must be CUDA tensors with contiguous head_dim")
+        n, h, p, d = K.shape
+        return CacheDesc(n, p, h, d, _dtype_code(K.dtype), st[0], st[1], st[2], K.data_ptr(), V.data_ptr())
+
+
+@dataclass
+class PagedPlan:
+    """One step's plan (device tensors): q_start (requests + 1), kv_len (requests),
+    slots (int64), token_req and positions (one a token), n_free and status (1)."""
+    q_start: torch.Tensor
+    kv_len: torch.Tensor
+    slots: torch.Tensor
+    token_req: torch.Tensor
+    positions: torch.Tensor
+    n_free: torch.Tensor
+    status: torch.Tensor
+
+    @classmethod
+    def empty(cls, n_requests: int, n_tokens: int, device="cuda"):
+        i32 = dict(dtype=torch.int32, device=device)
+        return cls(torch.empty(n_requests + 1, **i32), torch.empty(n_requests, **i32),
+                   torch.empty(n_tokens, dtype=torch.int64, device=device), torch.empty(n_tokens, **i32),
+                   torch.empty(n_tokens, **i32), torch.empty(1, **i32), torch.empty(1, **i32))
+
+
+def paged_plan(cached: torch.Tensor, fresh: torch.Tensor, table: torch.Tensor, free_pages: torch.Tensor,
+               n_free: torch.Tensor, page_size: int, n_tokens: int = None, plan: PagedPlan = None,
+               stream=None) -> PagedPlan:
+    """Pages and slots of a step in which request r, with cached[r] tokens in the
+    pages of table[r], appends fresh[r] tokens (int32 tensors).  The pages come
+    off the end of free_pages[:n_free]; the table's new entries are written in
+    place.  n_tokens: the capacity of the token arrays (the new tokens' number,
+    or more, the rest padded with -1).  plan.status is 0, or PLAN_ bits and
+    nothing planned; it stays on the device (check it where the step's tokens
+    are read back)."""
+    R = cached.numel()
+    if plan is None:
+        if n_tokens is None:
+            raise ValueError("n_tokens or a plan to write is needed")
+        with _on_stream(stream):
+            plan = PagedPlan.empty(R, n_tokens, cached.device)
+    N = plan.slots.numel()
+    if n_tokens is not None and n_tokens != N:
+        raise ValueError(f"plan holds {N} tokens, not {n_tokens}")
+    if table.dim() != 2 or table.shape[0] != R:
+        raise ValueError(f"table must be ({R}, pages), not {tuple(table.shape)}")
+    width = table.shape[1]
+    _ints("cached", cached, R)
+    _ints("fresh", fresh, R)
+    _ints("table", table, R * width)
+    _ints("free_pages", free_pages, free_pages.numel())
+    _ints("n_free", n_free, 1)
+    _ints("plan.q_start", plan.q_start, R + 1)
+    _ints("plan.kv_len", plan.kv_len, R)
+    _ints("plan.slots", plan.slots, N, torch.int64)
+    _ints("plan.token_req", plan.token_req, N)
+    _ints("plan.positions", plan.positions, N)
+    _ints("plan.n_free", plan.n_free, 1)
+    _ints("plan.status", plan.status, 1)
+    _check(lib().gsi_paged_plan(cached.data_ptr(), fresh.data_ptr(), R, table.data_ptr(), width, free_pages.data_ptr(),
+                                free_pages.numel(), n_free.data_ptr(), page_size, N, plan.q_start.data_ptr(),
+                                plan.kv_len.data_ptr(), plan.slots.data_ptr(), plan.token_req.data_ptr(),
+                                plan.positions.data_ptr(), plan.n_free.data_ptr(), plan.status.data_ptr(),
+                                _raw_stream(stream, cached)))
+    return plan
+
+
+def cache_append(cache: PagedCache, rows: torch.Tensor, slots: torch.Tensor, n_q_heads: int, Q=None, stream=None):
+    """The rows of a qkv map (T x (n_q_heads + 2 heads) head_dim, float32 or
+    bfloat16, rows contiguous): keys and values into the cache at `slots`
+    (negative: padding), queries to Q (T, n_q_heads, head_dim), returned."""
+    c = cache.desc()
+    T = slots.numel()
+    if rows.dim() != 2 or not rows.is_cuda or rows.shape[0] != T or \
+            rows.shape[1] != (n_q_heads + 2 * c.n_heads) * c.head_dim or (rows.stride(1) != 1 and T):
+        raise ValueError(f"rows must be CUDA rows of ({T}, {(n_q_heads + 2 * c.n_heads) * c.head_dim}), "
+                         f"not {tuple(rows.shape)}")
+    _ints("slots", slots, T, torch.int64)
+    if Q is None:
+        with _on_stream(stream):
+            Q = torch.empty(T, n_q_heads, c.head_dim, dtype=cache.K.dtype, device=rows.device)
+    else:
+        _like("Q", Q, (T, n_q_heads, c.head_dim), cache.K.dtype)
+    _check(lib().gsi_cache_append(ctypes.byref(c), rows.data_ptr(), _dtype_code(rows.dtype), rows.stride(0),
+                                  slots.data_ptr(), T, n_q_heads, Q.data_ptr(), _raw_stream(stream, rows)))
+    return Q
+
+
+def paged_attention_workspace_size(cache: PagedCache, n_q_heads: int) -> int:
+    c = cache.desc()
+    n = int(lib().gsi_paged_attention_workspace_size(ctypes.byref(c), n_q_heads))
+    if n == 0:
+        raise GsiError(1, lib().gsi_last_error().decode() or "no attention of this shape")
+    return n
+
+
+def paged_attention(cache: PagedCache, Q: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor,
+                    table: torch.Tensor, max_q: int = None, scale: float = None, causal: bool = True, window: int = 0,
+                    out=None, workspace=None, stream=None):
+    """Attention of every request's new tokens Q (N, heads, head_dim; rows of the
+    cache's dtype, any stride between tokens) over its cached keys, as planned
+    by paged_plan; returns out (N, heads, head_dim).  causal: the new tokens are
+    the last ones of the request's kv_len keys; window > 0: a token sees only
+    that many keys, its own the last.  causal=False: every key (cross attention
+    to cached states).  A row that sees no key gives zeros; rows of no request
+    are not written.  max_q: a bound on a request's new tokens, for the choice
+    of kernel.  scale defaults to head_dim ** -0.5."""
+    c = cache.desc()
+    if Q.dim() != 3 or not Q.is_cuda or Q.dtype is not cache.K.dtype or Q.shape[2] != c.head_dim:
+        raise ValueError(f"Q must be a (tokens, heads, {c.head_dim}) CUDA tensor of {cache.K.dtype}, "
+                         f"not {tuple(Q.shape)} {Q.dtype}")
+    N, H, D = Q.shape
+    st = Q.stride()
+    if N and (st[2] != 1 or (H > 1 and st[1] != D)):
+        raise ValueError("the heads of a token of Q must be contiguous")
+    R = kv_len.numel()
+    if table.dim() != 2 or table.shape[0] != R:
+        raise ValueError(f"table must be ({R}, pages), not {tuple(table.shape)}")
+    width = table.shape[1]
+    _ints("table", table, R * width)
+    _ints("q_start", q_start, R + 1)
+    _ints("kv_len", kv_len, R)
+    if out is None:
+        with _on_stream(stream):
+            out = torch.empty(N, H, D, dtype=Q.dtype, device=Q.device)
+    else:
+        _like("out", out, Q.shape, Q.dtype)
+    if workspace is None:
+        with _on_stream(stream):
+            workspace = new_workspace(paged_attention_workspace_size(cache, H), Q.device, stream)
+    _check(lib().gsi_paged_attention(ctypes.byref(c), Q.data_ptr(), st[0], N, H, q_start.data_ptr(), kv_len.data_ptr(),
+                                     table.data_ptr(), width, R, N if max_q is None else max_q,
+                                     D ** -0.5 if scale is None else scale, 1 if causal else 0, window, out.data_ptr(),
+                                     workspace.data_ptr(), workspace.numel(), _raw_stream(stream, Q)))
+    return out
+
+
+@dataclass
+class Norm:
+    """A norm over a row: kind "rms", "layer" or "none", float32 weight and bias (or None)."""
+    kind: str
+    weight: torch.Tensor = None
+    bias: torch.Tensor = None
+    eps: float = 1e-5
+
+    def desc(self, d: int) -> NormDesc:
+        w, b = self.weight, self.bias
+        if w is not None:
+            _like("norm weight", w, (d,), torch.float32)
+        if b is not None:
+            _like("norm bias", b, (d,), torch.float32)
+        return NormDesc(NORMS[self.kind], self.eps, None if w is None else w.data_ptr(),
+                        None if b is None else b.data_ptr())
+
+
+def norm_residual(h: torch.Tensor, y: torch.Tensor = None, post: Norm = None, pre: Norm = None, gate=None,
+                  gate_index=None, alpha: float = 1.0, h_out=None, x=None, x_dtype=torch.bfloat16, stream=None):
+    """The end of one block and the beginning of the next, in one pass over T x d
+    rows: h_out = alpha h + gate post(y), x = pre(h_out); returns (h_out, x).
+    h, y, x: float32 or bfloat16.  gate: float32, (d,) for every token or
+    (n, d) with gate_index (T int32) naming each token's row (a plan's
+    token_req, for a gate per request).  h_out may be h."""
+    T, d = h.shape
+    _like("h", h, (T, d), h.dtype)
+    if y is not None:
+        _like("y", y, (T, d), y.dtype)
+    rows = 0
+    if gate is not None:
+        rows = gate.numel() // d
+        _like("gate", gate, gate.shape[:-1] + (d,), torch.float32)
+        if gate_index is not None:
+            _ints("gate_index", gate_index, T)
+        elif rows != 1:
+            raise ValueError("a gate of several rows needs gate_index")
+    with _on_stream(stream):
+        if h_out is None:
+            h_out = torch.empty_like(h)
+        if x is None:
+            x = torch.empty(T, d, dtype=x_dtype, device=h.device)
+    _like("h_out", h_out, (T, d), h.dtype)
+    _like("x", x, (T, d), x.dtype)
+    _check(lib().gsi_norm_residual(h.data_ptr(), _dtype_code(h.dtype), None if y is None else y.data_ptr(),
+                                   0 if y is None else _dtype_code(y.dtype), T, d, alpha,
+                                   None if post is None else ctypes.byref(post.desc(d)),
+                                   None if gate is None else gate.data_ptr(), rows,
+                                   None if gate_index is None else gate_index.data_ptr(),
+                                   None if pre is None else ctypes.byref(pre.desc(d)), h_out.data_ptr(), x.data_ptr(),
+                                   _dtype_code(x.dtype), _raw_stream(stream, h)))
+    return h_out, x

@@ -41,7 +41,7 @@ static gsi_status ok() {
 }
 
 // Host-side fault injection: when armed with n, the n-th launch step fails.
-static bool injected_failure() {
+bool injected_failure() {
   int n = g_fail_after.load();
   if (n <= 0) return false;
   if (g_fail_after.fetch_sub(1) == 1) return true;

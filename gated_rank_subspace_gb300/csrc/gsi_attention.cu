@@ -1,0 +1,105 @@
+// Attention of new tokens over a paged key/value cache: dispatch, and the
+// plain kernel.
+
+#include "gsi_common.cuh"
+#include "gsi_kernels.h"
+
+namespace gsi {
+
+// The plain kernel, one warp a (token, head): the running maximum m and sum l
+// of a softmax and its weighted sum o over the row's keys, one pass,
+//   m' = max(m, s), l' = l e^(m - m') + e^(s - m'), o' = o e^(m - m') + e^(s - m') v,
+// 32 keys at a time (a lane scores one key; the weighted sum has the lanes on
+// the head's columns).
+constexpr int kPlainWarps = 4;
+
+template <class T>
+__global__ void __launch_bounds__(kPlainWarps * 32) attn_plain_kernel(AttnArgs a) {
+  __shared__ float s_q[kPlainWarps][256];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t w = int64_t(blockIdx.x) * kPlainWarps + warp;
+  const int hq = a.hkv * a.group;
+  const int64_t tok = w / hq;
+  const int head = int(w - tok * hq);
+  if (tok >= a.N) return;
+  // its request: the last one that begins at or before the token
+  int lo = 0, hi = a.n_req;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldcg(a.q_start + mid) <= tok) lo = mid; else hi = mid;
+  }
+  const int r = lo;
+  const int64_t q0 = __ldcg(a.q_start + r), q1 = __ldcg(a.q_start + r + 1);
+  if (tok < q0 || tok >= q1) return;
+  const int64_t most = a.width << a.page_shift;
+  const int64_t len = min(max(int64_t(__ldcg(a.kv_len + r)), int64_t(0)), most);
+  const int64_t lim = a.causal ? max(int64_t(0), len - (q1 - tok) + 1) : len;
+  const int64_t first = a.window > 0 ? max(int64_t(0), lim - a.window) : 0;
+  for (int c = lane; c < a.dim; c += 32) s_q[warp][c] = T::load1_cg(a.Q, tok * a.q_stride + int64_t(head) * a.dim + c) * a.scale;
+  __syncwarp();
+  const int kvh = head / a.group;
+  float m = -INFINITY, l = 0.f, o[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] = 0.f;
+  for (int64_t j0 = first; j0 < lim; j0 += 32) {
+    const int64_t j = j0 + lane;
+    float s = -INFINITY;
+    int64_t at = -1;
+    if (j < lim) {
+      const int64_t pg = __ldcg(a.table + r * a.width + (j >> a.page_shift));
+      s = 0.f;
+      if (pg >= 0 && pg < a.n_pages) {
+        at = pg * a.page_stride + kvh * a.head_stride + (j & ((1 << a.page_shift) - 1)) * a.token_stride;
+        for (int c = 0; c < a.dim; ++c) s = fmaf(s_q[warp][c], T::load1_cg(a.K, at + c), s);
+      }
+    }
+    float mx = s;
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+    mx = fmaxf(mx, m);
+    const float p = j < lim ? (s == -INFINITY ? 0.f : expf(s - mx)) : 0.f;
+    const float f = m == -INFINITY ? 0.f : expf(m - mx);
+    m = mx;
+    l = l * f + warp_sum(p);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] *= f;
+    const int n = int(min(int64_t(32), lim - j0));
+    for (int k = 0; k < n; ++k) {
+      const float pk = __shfl_sync(0xffffffffu, p, k);
+      const int64_t ak = __shfl_sync(0xffffffffu, (long long)at, k);
+      if (ak >= 0)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int c = lane + 32 * i;
+          if (c < a.dim) o[i] = fmaf(pk, T::load1_cg(a.V, ak + c), o[i]);
+        }
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int c = lane + 32 * i;
+    if (c < a.dim) T::store1(a.O, (tok * hq + head) * a.dim + c, o[i] * inv);
+  }
+}
+
+size_t attention_work_bytes(gsi_dtype dt, int dim, int group) { return sizeof(Ctrl); }
+
+cudaError_t launch_paged_attention(const AttnArgs& a, gsi_dtype dt, int64_t max_q, cudaStream_t s) {
+  const int64_t rows = int64_t(a.N) * a.hkv * a.group;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(unsigned((rows + kPlainWarps - 1) / kPlainWarps));
+  cfg.blockDim = dim3(kPlainWarps * 32);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return dt == GSI_F32 ? cudaLaunchKernelEx(&cfg, attn_plain_kernel<F32>, a)
+                       : cudaLaunchKernelEx(&cfg, attn_plain_kernel<BF16>, a);
+}
+
+}  // namespace gsi

@@ -225,6 +225,8 @@ cudaError_t launch_gram(const void* V, float* gram, int64_t d, int64_t k, gsi_dt
 
 // Sets the calling thread's gsi_last_error() message and returns s.
 gsi_status record_error(gsi_status s, const char* msg);
+// Host-side fault injection (gsi_debug_fail_after): true when this launch step is the one that fails.
+bool injected_failure();
 
 cudaError_t launch_gate(const GateArgs& a, const GatePlan& p, gsi_dtype dt, cudaStream_t s,
                         bool pdl);
@@ -251,5 +253,82 @@ cudaError_t launch_residual_check(const void* X, const void* V, const float* G, 
                                   cudaStream_t s);
 cudaError_t launch_image(const void* W, const void* V, void* M, float* gram, int64_t d,
                          int64_t d_out, int64_t k, gsi_dtype dt, cudaStream_t s);
+
+
+// Serving operators (see gsi_paged.cu, gsi_norm.cu, gsi_attention.cu).
+struct PlanArgs {
+  const int32_t* cached;
+  const int32_t* fresh;
+  int n_req;
+  int32_t* table;
+  int64_t width;
+  const int32_t* free_pages;
+  int64_t capacity;
+  const int32_t* n_free;
+  int page_shift;
+  int n_tokens;
+  int32_t* q_start;
+  int32_t* kv_len;
+  int64_t* slots;
+  int32_t* token_req;
+  int32_t* positions;
+  int32_t* n_free_out;
+  int32_t* status;
+};
+cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t s);
+
+struct AppendArgs {
+  const void* X;       // T x (hq + 2 hkv) * dim rows
+  int64_t row_stride;
+  const int64_t* slots;
+  int T, hq, hkv, dim, page_shift;
+  int64_t n_slots;     // n_pages * page_size
+  int64_t page_stride, head_stride, token_stride;
+  void* K;
+  void* V;
+  void* Q;             // or null
+};
+cudaError_t launch_cache_append(const AppendArgs& a, gsi_dtype xdt, gsi_dtype cdt, cudaStream_t s);
+
+struct AttnArgs {
+  const void* K;
+  const void* V;
+  int64_t page_stride, head_stride, token_stride;
+  int64_t n_pages;
+  int page_shift, hkv, group, dim;
+  const void* Q;
+  int64_t q_stride;
+  void* O;             // N x (hkv * group) x dim
+  int N;
+  const int32_t* q_start;
+  const int32_t* kv_len;
+  const int32_t* table;
+  int64_t width;
+  int n_req;
+  float scale;
+  int causal, window;
+  void* work;
+};
+cudaError_t launch_paged_attention(const AttnArgs& a, gsi_dtype dt, int64_t max_q, cudaStream_t s);
+size_t attention_work_bytes(gsi_dtype dt, int dim, int group);
+
+struct NormArgs {
+  const void* H;
+  const void* Y;       // or null
+  int T, d;
+  float alpha;
+  int post, pre;       // gsi_norm_kind
+  float post_eps, pre_eps;
+  const float* post_w;
+  const float* post_b;
+  const float* pre_w;
+  const float* pre_b;
+  const float* gate;
+  int gate_rows;
+  const int32_t* gate_index;
+  void* H_out;
+  void* X;
+};
+cudaError_t launch_norm_residual(const NormArgs& a, gsi_dtype hdt, gsi_dtype ydt, gsi_dtype xdt, cudaStream_t s);
 
 }  // namespace gsi

@@ -342,6 +342,135 @@ size_t gsi_linear_noalloc_max_bytes(void);
  * the next call.  Allocates nothing. */
 gsi_status gsi_linear_noalloc_status(uint32_t* code, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Serving operators: what stands between the gated maps of a decoder layer.
+ * No counterpart in the paper, which accelerates the maps and leaves
+ * attention as it is (§2.4); a model served through gsi_linear needs, between
+ * its qkv and out maps, a paged key/value cache and the attention over it,
+ * and between its blocks the norms, gate and residual.  A step of a server:
+ *   gsi_paged_plan       pages and slots of the step's new tokens
+ *   per layer: gsi_linear (qkv), gsi_cache_append, gsi_paged_attention,
+ *              gsi_linear (out), gsi_norm_residual, gsi_linear (up) ...
+ * The conventions above hold (asynchronous on `stream`, nothing allocated,
+ * argument errors synchronous, no host synchronisation: lengths, tables and
+ * slots stay on the device and calls may be captured into a CUDA graph).
+ * Arrays of 32- and 64-bit integers need only their natural alignment. */
+
+/* A paged key/value cache.  K and V hold n_pages pages of page_size tokens;
+ * the head_dim values of token o of page p under head h are contiguous at
+ * element p * page_stride + h * head_stride + o * token_stride of either.
+ * page_size is a power of two from 16 to 256; head_dim is at most 256;
+ * head_dim and the strides are multiples of 16 bytes; the strides are
+ * non-negative.  GSI_ERR_UNSUPPORTED otherwise. */
+typedef struct gsi_cache_desc {
+  int64_t n_pages;
+  int64_t page_size;
+  int64_t n_heads;  /* key/value heads */
+  int64_t head_dim;
+  gsi_dtype dtype;
+  int64_t page_stride, head_stride, token_stride; /* elements */
+  void* K;
+  void* V;
+} gsi_cache_desc;
+
+/* Bits of the status that gsi_paged_plan writes (0: the plan was made). */
+#define GSI_PLAN_BAD_LENGTH 1  /* a negative length, or lengths beyond 2^31 */
+#define GSI_PLAN_TABLE_FULL 2  /* a request needs more pages than table_width */
+#define GSI_PLAN_NO_PAGES 4    /* fewer free pages than needed (or n_free outside 0 .. capacity) */
+#define GSI_PLAN_TOO_MANY_TOKENS 8 /* more new tokens than n_tokens */
+
+/* Block tables and slot maps of one step, from the requests' lengths.
+ * Request r holds cached[r] tokens in the pages table[r][0 ..
+ * ceil(cached[r] / page_size)) and appends fresh[r] more.  The free pages are
+ * the stack free_pages[0 .. *n_free), taken from its end in the order of the
+ * requests and of their pages; the table entries of the pages taken are
+ * written, and
+ *   q_start (n_req + 1)  the first new token of each request, and their sum
+ *   kv_len (n_req)       cached + fresh
+ *   slots (n_tokens)     page * page_size + offset of every new token
+ *   token_req, positions (n_tokens)  its request, and its place there
+ *   *n_free_out          the free pages that are left.
+ * Tokens from q_start[n_req] on (a fixed n_tokens larger than the step's) get
+ * -1 in slots, token_req and positions, as does the slot of a token whose
+ * page a caller's table entry gives as negative.  The inputs but `table` are
+ * left as they are: a caller that goes on passes kv_len as the next step's
+ * cached and n_free_out as its n_free, and gives a finished request's pages
+ * back by appending them to free_pages.  kv_len must not be cached, nor
+ * n_free_out n_free (GSI_ERR_INVALID_ARG).  A plan that cannot be made is not
+ * made in part: *status receives the GSI_PLAN_ bits, q_start zeros, kv_len
+ * the unchanged cached lengths (negative ones as 0), the token arrays -1,
+ * *n_free_out *n_free, and the table stays.  All pointers are device
+ * pointers; n_req <= 2^20, n_tokens <= 2^24, table_width * page_size < 2^31. */
+gsi_status gsi_paged_plan(const int32_t* cached, const int32_t* fresh, int64_t n_req, int32_t* table,
+                          int64_t table_width, const int32_t* free_pages, int64_t capacity, const int32_t* n_free,
+                          int64_t page_size, int64_t n_tokens, int32_t* q_start, int32_t* kv_len, int64_t* slots,
+                          int32_t* token_req, int32_t* positions, int32_t* n_free_out, int32_t* status, void* stream);
+
+/* The rows of a qkv map (gsi_linear's Y, or any T x (n_q_heads + 2 n_heads) *
+ * head_dim rows of type xdt, row_stride elements apart): the first n_q_heads *
+ * head_dim values of a row are its queries and go to Q (T x n_q_heads x
+ * head_dim, the cache's type; Q may be NULL, then they are left out), the
+ * next n_heads * head_dim its keys and the last its values, which go to the
+ * cache at slots[t].  float32 rows are rounded to nearest even into a bf16
+ * cache.  Tokens whose slot lies outside the cache (negative: padding) leave
+ * the cache as it is; their queries are still written.  Slots are distinct. */
+gsi_status gsi_cache_append(const gsi_cache_desc* cache, const void* X, gsi_dtype xdt, int64_t row_stride,
+                            const int64_t* slots, int64_t T, int64_t n_q_heads, void* Q, void* stream);
+
+/* Attention of the new tokens of every request over its paged keys and
+ * values.  Request r has the tokens q_start[r] .. q_start[r + 1) of Q (its
+ * q_len) and kv_len[r] keys, key j in page table[r][j / page_size].  Query
+ * head h reads key/value head h / (n_q_heads / n_heads).  Token i of a
+ * request sees the keys j in [lo, lim):
+ *   causal:     lim = kv_len - q_len + i + 1 (at least 0), and with
+ *               window > 0 lo = max(0, lim - window);
+ *   not causal: all kv_len keys (window must be 0) -- the cross attention of
+ *               a chunk to states of another length.
+ * O[i] = sum_j p_j v_j with p = softmax(scale * q_i . k_j) over those keys;
+ * a row that sees none gives zeros.  Values outside a row's keys (stale
+ * slots, other tokens, whatever they hold) do not reach it.  Q rows are
+ * q_stride elements apart (n_q_heads x head_dim values each, 16-byte aligned);
+ * O is N x n_q_heads x head_dim, of the cache's type like Q; its rows outside
+ * every request are not written.  q_start must not decrease and stays within
+ * N; kv_len stays within table_width * page_size (a longer one is cut there);
+ * a table entry outside the cache reads as zeros.
+ * Softmax statistics and sums are float32; for GSI_BF16 the weights p enter
+ * the second product as bf16.  max_q is the caller's bound on a request's
+ * new tokens (it chooses the kernel; a wrong one costs time, not results).
+ * workspace: zeroed once (gsi_workspace_init), one stream at a time, at least
+ * gsi_paged_attention_workspace_size bytes. */
+size_t gsi_paged_attention_workspace_size(const gsi_cache_desc* cache, int64_t n_q_heads);
+gsi_status gsi_paged_attention(const gsi_cache_desc* cache, const void* Q, int64_t q_stride, int64_t N,
+                               int64_t n_q_heads, const int32_t* q_start, const int32_t* kv_len,
+                               const int32_t* table, int64_t table_width, int64_t n_req, int64_t max_q, float scale,
+                               int causal, int64_t window, void* O, void* workspace, size_t ws_bytes, void* stream);
+
+typedef enum gsi_norm_kind { GSI_NORM_NONE = 0, GSI_NORM_RMS = 1, GSI_NORM_LAYER = 2 } gsi_norm_kind;
+
+/* One norm: RMS, v / sqrt(mean(v^2) + eps), or LAYER, (v - mean) /
+ * sqrt(var + eps) (the biased variance), then times weight, plus bias.
+ * weight and bias: d float32 (device), each may be NULL. */
+typedef struct gsi_norm {
+  gsi_norm_kind kind;
+  float eps;
+  const float* weight;
+  const float* bias;
+} gsi_norm;
+
+/* The end of one block and the beginning of the next:
+ *   h' = alpha * h + gate * post(y),   x = pre(h').
+ * H, Y: T x d (rows of d contiguous values) of hdt and ydt.  Y may be NULL
+ * (h' = alpha * h).  gate: gate_rows x d float32 or NULL (1); token t takes
+ * row gate_index[t], or row 0 where gate_index is NULL (then gate_rows is 1
+ * or more; an index outside 0 .. gate_rows gives a gate of 0).  H_out: T x d
+ * of hdt, or NULL; it may be H.  X: T x d of xdt, or NULL.  pre sees h' in
+ * float32, before it is rounded into hdt.  Sums are float32; LAYER forms the
+ * variance from the centred values.  d is a multiple of 8, at most 16384. */
+gsi_status gsi_norm_residual(const void* H, gsi_dtype hdt, const void* Y, gsi_dtype ydt, int64_t T, int64_t d,
+                             float alpha, const gsi_norm* post, const float* gate, int64_t gate_rows,
+                             const int32_t* gate_index, const gsi_norm* pre, void* H_out, void* X, gsi_dtype xdt,
+                             void* stream);
+
 /* Message for the calling thread's last non-OK status ("" if none). */
 const char* gsi_last_error(void);
 
