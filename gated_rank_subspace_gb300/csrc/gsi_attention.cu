@@ -1,8 +1,7 @@
 // Attention of new tokens over a paged key/value cache: dispatch, and the
 // plain kernel.
 
-#include "gsi_common.cuh"
-#include "gsi_kernels.h"
+#include "gsi_attn.cuh"
 
 namespace gsi {
 
@@ -85,9 +84,57 @@ __global__ void __launch_bounds__(kPlainWarps * 32) attn_plain_kernel(AttnArgs a
   }
 }
 
-size_t attention_work_bytes(gsi_dtype dt, int dim, int group) { return sizeof(Ctrl); }
+// ------------------------------------------------------------------ host side
+typedef CUresult (*AttnEncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static AttnEncodeFn attn_encode_fn() {
+  static const AttnEncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                        cudaSuccess && q == cudaDriverEntryPointSuccess;
+    return ok ? reinterpret_cast<AttnEncodeFn>(p) : nullptr;
+  }();
+  return fn;
+}
+
+cudaError_t attn_page_map(CUtensorMap* m, const AttnArgs& a, const void* base, int box_rows) {
+  const AttnEncodeFn fn = attn_encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint64_t page = cuuint64_t(1) << a.page_shift;
+  cuuint64_t dim[4] = {cuuint64_t(a.dim), page, cuuint64_t(a.hkv), cuuint64_t(a.n_pages)};
+  // the stride of a dimension of one element is never used: any valid one does
+  const int64_t st[3] = {a.token_stride, a.hkv > 1 ? a.head_stride : a.token_stride,
+                         a.n_pages > 1 ? a.page_stride : a.token_stride};
+  cuuint64_t bytes[3];
+  for (int i = 0; i < 3; ++i) bytes[i] = cuuint64_t(st[i]) * 2;
+  if (a.n_pages == 0) {  // nothing is read through it (no request then has a key)
+    base = a.Q;
+    dim[1] = dim[2] = dim[3] = 1;
+  }
+  const cuuint32_t box[4] = {64, cuuint32_t(box_rows), 1, 1}, es[4] = {1, 1, 1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dim, bytes, box, es,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+int attn_sm_count() {
+  static const int n = [] {
+    int dev = 0, v = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return kAttnCtas;
+    return v;
+  }();
+  return n;
+}
+
+size_t attention_work_bytes(gsi_dtype dt, int dim, int group) { return attn_work_bytes(16, dim); }
 
 cudaError_t launch_paged_attention(const AttnArgs& a, gsi_dtype dt, int64_t max_q, cudaStream_t s) {
+  if (dt == GSI_BF16 && max_q * a.group <= 16 && a.group <= 16) return launch_attn_rows16(a, s);
   const int64_t rows = int64_t(a.N) * a.hkv * a.group;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(unsigned((rows + kPlainWarps - 1) / kPlainWarps));

@@ -1,0 +1,295 @@
+// What the attention kernels share: how the work of ragged requests is cut
+// into equal shares, the partial results where a share ends inside a row
+// tile, and the paged tensor maps.
+#pragma once
+
+#include <cuda.h>
+
+#include "gsi_async.cuh"
+#include "gsi_kernels.h"
+
+namespace gsi {
+
+// ------------------------------------------------------------------ work
+// A unit is a block of `ut` consecutive new tokens of one request under one
+// key/value head (their ut * group query rows), over the tiles of `kt` keys
+// that any of its rows sees.  All units' tiles, in the order of requests,
+// heads and token blocks, form one line; CTA b of G takes the tiles
+// [T b / G, T (b + 1) / G) of it.  So the shares are equal to a tile whatever
+// the lengths are, one long request is spread over all CTAs, and neighbours
+// read the same keys.  A unit that sees no key counts as one tile (its rows
+// of zeros have to be written).  Each CTA finds its share from the lengths.
+struct AttnReq {
+  int q0, q_len, len;
+};
+
+__device__ __forceinline__ AttnReq attn_request(const AttnArgs& a, int r) {
+  const int s = __ldcg(a.q_start + r), e = __ldcg(a.q_start + r + 1), n = __ldcg(a.kv_len + r);
+  AttnReq q;
+  q.q0 = min(max(s, 0), a.N);
+  q.q_len = min(max(e, q.q0), a.N) - q.q0;
+  q.len = min(max(n, 0), int(a.width << a.page_shift));
+  return q;
+}
+
+// The keys [lo, lim) that token i of a request sees.
+__device__ __forceinline__ int attn_lim(const AttnArgs& a, const AttnReq& q, int i) {
+  return a.causal ? max(0, q.len - q.q_len + i + 1) : q.len;
+}
+__device__ __forceinline__ int attn_lo(const AttnArgs& a, int lim) {
+  return a.window > 0 && lim > a.window ? lim - a.window : 0;
+}
+
+// First tile and number of tiles of unit u.
+__device__ __forceinline__ void attn_tiles(const AttnArgs& a, const AttnReq& q, int u, int ut, int kt, int& t0, int& n) {
+  const int lim = attn_lim(a, q, min((u + 1) * ut, q.q_len) - 1);
+  t0 = attn_lo(a, attn_lim(a, q, u * ut)) / kt;
+  n = max(0, (lim + kt - 1) / kt - t0);
+}
+
+__device__ __forceinline__ long long attn_head_cost(const AttnArgs& a, const AttnReq& q, int ut, int kt) {
+  long long s = 0;
+  for (int u = 0; u * ut < q.q_len; ++u) {
+    int t0, n;
+    attn_tiles(a, q, u, ut, kt, t0, n);
+    s += max(1, n);
+  }
+  return s;
+}
+
+struct AttnShare {
+  long long total, pos, end;  // tiles of the line: all, and this CTA's
+  long long off;              // pos inside request r
+  int r, grid;                // grid: the CTAs that have a share (all, or as many as there are tiles)
+};
+
+// The share of CTA blockIdx.x; all NT threads of the block.
+template <int NT>
+__device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, int ut, int kt) {
+  __shared__ long long s_sum[NT / 32], s_off;
+  __shared__ int s_r;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int r0 = int((long long)a.n_req * tid / NT), r1 = int((long long)a.n_req * (tid + 1) / NT);
+  long long mine = 0;
+  for (int r = r0; r < r1; ++r) mine += attn_head_cost(a, attn_request(a, r), ut, kt) * a.hkv;
+  long long inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) s_sum[warp] = inc;
+  __syncthreads();
+  long long before = inc - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < warp) before += s_sum[w];
+    total += s_sum[w];
+  }
+  AttnShare s;
+  s.total = total;
+  s.grid = int(total < (long long)gridDim.x ? total : (long long)gridDim.x);
+  s.pos = s.end = 0;
+  if (int(blockIdx.x) < s.grid) {
+    s.pos = total * blockIdx.x / s.grid;
+    s.end = total * (blockIdx.x + 1) / s.grid;
+    if (before <= s.pos && s.pos < before + mine) {
+      long long at = s.pos - before;
+      for (int r = r0; r < r1; ++r) {
+        const long long c = attn_head_cost(a, attn_request(a, r), ut, kt) * a.hkv;
+        if (at < c) {
+          s_r = r;
+          s_off = at;
+          break;
+        }
+        at -= c;
+      }
+    }
+  }
+  __syncthreads();
+  s.r = s_r;
+  s.off = s_off;
+  return s;
+}
+
+// One part of a unit: its tiles [a, b) of n.
+struct AttnSeg {
+  AttnReq q;
+  int r, h, u;
+  int t0, n, a, b;
+  long long first, last;  // the unit's place on the line
+};
+
+// Walks a share segment by segment; every role of a CTA walks it alike.
+struct AttnWalk {
+  AttnShare s;
+  int ut, kt;
+  AttnReq q;
+  long long per_head;
+  int r, h, u;
+  long long off;  // tiles of unit u that lie before pos
+
+  __device__ __forceinline__ void enter(const AttnArgs& a, long long at) {
+    q = attn_request(a, r);
+    per_head = attn_head_cost(a, q, ut, kt);
+    h = int(at / max(per_head, 1ll));
+    off = at - h * per_head;
+    for (u = 0;; ++u) {
+      int t0, n;
+      attn_tiles(a, q, u, ut, kt, t0, n);
+      if (off < max(1, n)) break;
+      off -= max(1, n);
+    }
+  }
+  __device__ __forceinline__ void begin(const AttnArgs& a, const AttnShare& share, int ut_, int kt_) {
+    s = share;
+    ut = ut_;
+    kt = kt_;
+    r = s.r;
+    if (s.pos < s.end) enter(a, s.off);
+  }
+  __device__ __forceinline__ bool next(const AttnArgs& a, AttnSeg& g) {
+    if (s.pos >= s.end) return false;
+    attn_tiles(a, q, u, ut, kt, g.t0, g.n);
+    const long long cost = max(1, g.n);
+    const long long take = cost - off < s.end - s.pos ? cost - off : s.end - s.pos;
+    g.q = q;
+    g.r = r;
+    g.h = h;
+    g.u = u;
+    g.first = s.pos - off;
+    g.last = g.first + cost;
+    g.a = int(off);
+    g.b = g.n == 0 ? 0 : int(off + take);
+    s.pos += take;
+    off += take;
+    if (off == cost && s.pos < s.end) {
+      off = 0;
+      if ((u + 1) * ut < q.q_len) {
+        ++u;
+      } else if (h + 1 < a.hkv) {
+        u = 0;
+        ++h;
+      } else {
+        do ++r; while (attn_request(a, r).q_len == 0);  // there is a next one: the share goes on
+        enter(a, 0);
+      }
+    }
+    return true;
+  }
+  // The CTA whose share holds tile x of the line.
+  __device__ __forceinline__ int owner(long long x) const { return int(((x + 1) * s.grid - 1) / s.total); }
+};
+
+// ------------------------------------------------------------------ partial results
+// A unit that is cut has its parts in the shares of consecutive CTAs.  Each
+// leaves its rows' running maximum m, sum l and unnormalised output o in the
+// workspace; the CTA that finds itself the last to arrive at the unit's
+// counter joins all parts in the order of the line (so the result does not
+// depend on who came last) and sets the counter back to zero.  Nobody waits.
+// At most two units of a share are cut: one that an earlier CTA began (slot
+// 2 b) and one that a later CTA ends (slot 2 b + 1).
+constexpr int kAttnCtas = 152;  // CTAs of a launch, at most: one an SM
+constexpr size_t kAttnCounterBytes = 1024;
+static_assert(kAttnCtas * 4 <= int(kAttnCounterBytes), "a counter a CTA");
+
+__host__ __device__ constexpr size_t attn_slot_floats(int rows, int dim) { return size_t(rows) * (dim + 2); }
+inline size_t attn_work_bytes(int rows, int dim) {
+  return (sizeof(Ctrl) + kAttnCounterBytes + 2 * kAttnCtas * attn_slot_floats(rows, dim) * 4 + 255) / 256 * 256;
+}
+__device__ __forceinline__ uint32_t* attn_err(const AttnArgs& a) { return &static_cast<Ctrl*>(a.work)->err; }
+__device__ __forceinline__ unsigned* attn_counter(const AttnArgs& a, int cta) {
+  return reinterpret_cast<unsigned*>(static_cast<char*>(a.work) + sizeof(Ctrl)) + cta;
+}
+__device__ __forceinline__ float* attn_slot(const AttnArgs& a, int slot, int rows) {
+  return reinterpret_cast<float*>(static_cast<char*>(a.work) + sizeof(Ctrl) + kAttnCounterBytes) +
+         slot * attn_slot_floats(rows, a.dim);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// exp2(m - to) for running maxima, where -inf stands for "no key yet".
+__device__ __forceinline__ float attn_scale(float m, float to) { return m == -INFINITY ? 0.f : ex2(m - to); }
+
+// Address of the output row of query row `row` (token-major, head-minor) of a unit.
+__device__ __forceinline__ int64_t attn_out_row(const AttnArgs& a, const AttnSeg& g, int ut, int row) {
+  const int tok = row / a.group;
+  return (int64_t(g.q.q0 + g.u * ut + tok) * a.hkv + g.h) * a.group + (row - tok * a.group);
+}
+
+// Joins the parts b0 .. b1 of a unit's rows and writes them; threads tid of nt.
+template <class T>
+__device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnSeg& g, int b0, int b1, int n_rows, int slot_rows,
+                                          int ut, int tid, int nt) {
+  const int vec = a.dim / 8;
+  for (int e = tid; e < n_rows * vec; e += nt) {
+    const int row = e / vec, c = (e - row * vec) * 8;
+    float m = -INFINITY, l = 0.f, o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = 0.f;
+#pragma unroll 4
+    for (int b = b0; b <= b1; ++b) {
+      const float* p = attn_slot(a, 2 * b + (b == b0), slot_rows);
+      const float mp = __ldcg(p + row), lp = __ldcg(p + slot_rows + row);
+      const float4* po = reinterpret_cast<const float4*>(p + 2 * slot_rows + size_t(row) * a.dim + c);
+      const float4 x = __ldcg(po), y = __ldcg(po + 1);
+      const float mm = fmaxf(m, mp), f = attn_scale(m, mm), fp = attn_scale(mp, mm);
+      m = mm;
+      l = l * f + lp * fp;
+      const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = fmaf(v[i], fp, o[i] * f);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t at = attn_out_row(a, g, ut, row) * a.dim + c;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) T::store1(a.O, at + i, o[i] * inv);
+  }
+}
+
+// The values that a masked tile hides from some rows are multiplied by
+// weights of zero, which hides numbers but not infinities and NaN.  The
+// kernels therefore take non-finite values out of such tiles, and where one
+// was found (`found`) this adds it to the rows that do see its key: the sum
+// with it is what the definition gives.  Tiles [t0 + a, t0 + b) of kt keys;
+// the value of column c for a row that sees [lo, lim).
+template <class T>
+__device__ __noinline__ float attn_nonfinite(const AttnArgs& a, const AttnSeg& g, int kt, int lo, int lim, int lo_all,
+                                             int lim_all, int c, float o) {
+  for (int t = g.t0 + g.a; t < g.t0 + g.b; ++t) {
+    if (t * kt >= lo_all && (t + 1) * kt <= lim_all) continue;  // every row sees this tile: nothing was taken out
+    for (int j = max(t * kt, lo); j < min((t + 1) * kt, lim); ++j) {
+      const int64_t pg = __ldcg(a.table + int64_t(g.r) * a.width + (j >> a.page_shift));
+      if (pg < 0 || pg >= a.n_pages) continue;
+      const float v = T::load1_cg(a.V, pg * a.page_stride + g.h * a.head_stride +
+                                           int64_t(j & ((1 << a.page_shift) - 1)) * a.token_stride + c);
+      if (!(fabsf(v) < INFINITY)) o += v;
+    }
+  }
+  return o;
+}
+
+// ------------------------------------------------------------------ paged tensor maps
+// Box loads of a paged operand: coordinates (column, token of the page, head, page).
+__device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap* map, uint32_t bar, int col, int tok, int head,
+                                              int page) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+          dst),
+      "l"(map), "r"(col), "r"(tok), "r"(head), "r"(page), "r"(bar)
+      : "memory");
+}
+
+// Maps of K and V with boxes of 64 columns x box_rows tokens (128-byte
+// swizzle; columns beyond head_dim and pages outside the cache read as zeros).
+cudaError_t attn_page_map(CUtensorMap* m, const AttnArgs& a, const void* base, int box_rows);
+
+// SMs of the current device.
+int attn_sm_count();
+
+cudaError_t launch_attn_rows16(const AttnArgs& a, cudaStream_t s);
+
+}  // namespace gsi

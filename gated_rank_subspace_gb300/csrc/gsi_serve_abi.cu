@@ -237,7 +237,7 @@ gsi_status gsi_paged_attention(const gsi_cache_desc* cache, const void* Q, int64
   a.q_start = q_start;
   a.kv_len = kv_len;
   a.table = table;
-  a.width = table_width;
+  a.width = cache->n_pages ? table_width : 0;  // an empty cache holds no keys
   a.n_req = int(n_req);
   a.scale = scale;
   a.causal = causal != 0;

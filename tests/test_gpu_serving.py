@@ -8,8 +8,9 @@ Tolerances, from the arithmetic the kernels do:
     e A.  float32: scores of magnitude <= ~20 from up to 256 products, rounded
     at 2^-24 each in random directions (sqrt(256) * 2^-24 * 20 = 2e-5), the
     exponential's few ulps and the sum's rounding: e = 1e-4 covers them five
-    times.  bf16 maps: weights rounded to bf16 (2^-9), and the result rounded
-    once (2^-9 |o|): 2^-8 A + 1e-4 A;
+    times.  bf16 maps: weights rounded to bf16, whose 8 significant bits make
+    that a relative error of up to 2^-8, and the result rounded once (up to
+    2^-8 |o|): 2^-8 A + 2^-8 |o| + 1e-4 A;
   * norm: sums of up to 16384 squares in a tree of short chains (relative
     error under 40 * 2^-24 = 2.4e-6), centred values and products: 2e-5 (1 +
     |value|) for rows of magnitude ~1 whose mean is at most a few standard
@@ -193,7 +194,8 @@ def attention_case(gsi, dt, hq, hkv, D, page, lens, causal=True, window=0, seed=
     assert (o[~rows] == 7.0).all(), "rows of no request were written"
     fin = np.isfinite(O[rows])
     assert np.array_equal(o[rows][~fin], O[rows][~fin], equal_nan=True), "NaN or infinities unlike the definition's"
-    err, tol = np.abs(o[rows][fin] - O[rows][fin]), ((1e-4 if dt == F else 2**-8 + 1e-4) * A)[rows][fin]
+    o, O_, A = o[rows][fin], O[rows][fin], A[rows][fin]
+    err, tol = np.abs(o - O_), 1e-4 * A + (0 if dt == F else 2**-8 * (A + np.abs(O_)))
     if err.size:
         assert (err <= tol).all(), f"{float((err / np.maximum(tol, 1e-30)).max())} times the tolerance"
     return out, O
