@@ -121,6 +121,19 @@ cudaError_t attn_page_map(CUtensorMap* m, const AttnArgs& a, const void* base, i
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+cudaError_t attn_query_map(CUtensorMap* m, const AttnArgs& a, int box_heads, int box_tokens) {
+  const AttnEncodeFn fn = attn_encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint64_t dim[3] = {cuuint64_t(a.dim), cuuint64_t(a.hkv) * a.group, cuuint64_t(a.N)};
+  const int64_t row = a.N > 1 ? a.q_stride : int64_t(a.dim) * a.hkv * a.group;
+  const cuuint64_t bytes[2] = {cuuint64_t(a.dim) * 2, cuuint64_t(row) * 2};
+  const cuuint32_t box[3] = {64, cuuint32_t(box_heads), cuuint32_t(box_tokens)}, es[3] = {1, 1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.Q), dim, bytes, box, es,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 int attn_sm_count() {
   static const int n = [] {
     int dev = 0, v = 0;
@@ -131,10 +144,10 @@ int attn_sm_count() {
   return n;
 }
 
-size_t attention_work_bytes(gsi_dtype dt, int dim, int group) { return attn_work_bytes(16, dim); }
+size_t attention_work_bytes(gsi_dtype dt, int dim, int group) { return dt == GSI_BF16 ? attn_tiles_work_bytes(dim) : sizeof(Ctrl); }
 
 cudaError_t launch_paged_attention(const AttnArgs& a, gsi_dtype dt, int64_t max_q, cudaStream_t s) {
-  if (dt == GSI_BF16 && max_q * a.group <= 16 && a.group <= 16) return launch_attn_rows16(a, s);
+  if (dt == GSI_BF16) return max_q * a.group <= 16 ? launch_attn_rows16(a, s) : launch_attn_tiles(a, s);
   const int64_t rows = int64_t(a.N) * a.hkv * a.group;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(unsigned((rows + kPlainWarps - 1) / kPlainWarps));

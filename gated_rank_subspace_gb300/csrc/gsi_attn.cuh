@@ -190,20 +190,28 @@ struct AttnWalk {
 // At most two units of a share are cut: one that an earlier CTA began (slot
 // 2 b) and one that a later CTA ends (slot 2 b + 1).
 constexpr int kAttnCtas = 152;  // CTAs of a launch, at most: one an SM
-constexpr size_t kAttnCounterBytes = 1024;
-static_assert(kAttnCtas * 4 <= int(kAttnCounterBytes), "a counter a CTA");
+constexpr size_t kAttnCounterBytes = 2048;
+static_assert(kAttnCtas * 2 * 4 <= int(kAttnCounterBytes), "two counters (row tiles) a CTA");
 
 __host__ __device__ constexpr size_t attn_slot_floats(int rows, int dim) { return size_t(rows) * (dim + 2); }
 inline size_t attn_work_bytes(int rows, int dim) {
   return (sizeof(Ctrl) + kAttnCounterBytes + 2 * kAttnCtas * attn_slot_floats(rows, dim) * 4 + 255) / 256 * 256;
 }
 __device__ __forceinline__ uint32_t* attn_err(const AttnArgs& a) { return &static_cast<Ctrl*>(a.work)->err; }
-__device__ __forceinline__ unsigned* attn_counter(const AttnArgs& a, int cta) {
-  return reinterpret_cast<unsigned*>(static_cast<char*>(a.work) + sizeof(Ctrl)) + cta;
+__device__ __forceinline__ unsigned* attn_counter(const AttnArgs& a, int cta, int tile) {
+  return reinterpret_cast<unsigned*>(static_cast<char*>(a.work) + sizeof(Ctrl)) + 2 * cta + tile;
 }
-__device__ __forceinline__ float* attn_slot(const AttnArgs& a, int slot, int rows) {
+// The part of row tile `tile` (of `tiles` of a unit, `rows` rows each) in a
+// slot: m[rows], l[rows], then o in 16-byte pieces -- a row's pieces side by
+// side (kRowMajor), or one piece of every row side by side, which is how
+// threads that own a row each store them in whole lines.
+__device__ __forceinline__ float* attn_part(const AttnArgs& a, int slot, int tiles, int tile, int rows) {
   return reinterpret_cast<float*>(static_cast<char*>(a.work) + sizeof(Ctrl) + kAttnCounterBytes) +
-         slot * attn_slot_floats(rows, a.dim);
+         (size_t(slot) * tiles + tile) * attn_slot_floats(rows, a.dim);
+}
+template <bool kRowMajor>
+__device__ __forceinline__ float4* attn_piece(float* part, int rows, int dim, int row, int c) {
+  return reinterpret_cast<float4*>(part + 2 * rows) + (kRowMajor ? row * (dim / 4) + c / 4 : (c / 4) * rows + row);
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -214,28 +222,46 @@ __device__ __forceinline__ float ex2(float x) {
 // exp2(m - to) for running maxima, where -inf stands for "no key yet".
 __device__ __forceinline__ float attn_scale(float m, float to) { return m == -INFINITY ? 0.f : ex2(m - to); }
 
-// Address of the output row of query row `row` (token-major, head-minor) of a unit.
-__device__ __forceinline__ int64_t attn_out_row(const AttnArgs& a, const AttnSeg& g, int ut, int row) {
+// Number of the output row of query row `row` (token-major, head-minor) of a
+// row tile that begins with token tok0 of the request.
+__device__ __forceinline__ int64_t attn_out_row(const AttnArgs& a, const AttnSeg& g, int tok0, int row) {
   const int tok = row / a.group;
-  return (int64_t(g.q.q0 + g.u * ut + tok) * a.hkv + g.h) * a.group + (row - tok * a.group);
+  return (int64_t(g.q.q0 + tok0 + tok) * a.hkv + g.h) * a.group + (row - tok * a.group);
 }
 
-// Joins the parts b0 .. b1 of a unit's rows and writes them; threads tid of nt.
+__device__ __forceinline__ uint32_t attn_pack(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// Eight finished values of an output row.
 template <class T>
-__device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnSeg& g, int b0, int b1, int n_rows, int slot_rows,
-                                          int ut, int tid, int nt) {
+__device__ __forceinline__ void attn_store8(const AttnArgs& a, int64_t at, const float (&v)[8]) {
+  if constexpr (T::kBytes == 2) {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.O) + at) =
+        make_uint4(attn_pack(v[0], v[1]), attn_pack(v[2], v[3]), attn_pack(v[4], v[5]), attn_pack(v[6], v[7]));
+  } else {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.O) + at);
+    p[0] = make_float4(v[0], v[1], v[2], v[3]);
+    p[1] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+// Joins the parts b0 .. b1 of a row tile and writes its rows; threads tid of nt.
+template <class T, bool kRowMajor>
+__device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnSeg& g, int b0, int b1, int tiles, int tile,
+                                          int rows, int n_rows, int tok0, int tid, int nt) {
   const int vec = a.dim / 8;
   for (int e = tid; e < n_rows * vec; e += nt) {
-    const int row = e / vec, c = (e - row * vec) * 8;
+    const int row = kRowMajor ? e / vec : e % n_rows, c = (kRowMajor ? e % vec : e / n_rows) * 8;
     float m = -INFINITY, l = 0.f, o[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] = 0.f;
 #pragma unroll 4
     for (int b = b0; b <= b1; ++b) {
-      const float* p = attn_slot(a, 2 * b + (b == b0), slot_rows);
-      const float mp = __ldcg(p + row), lp = __ldcg(p + slot_rows + row);
-      const float4* po = reinterpret_cast<const float4*>(p + 2 * slot_rows + size_t(row) * a.dim + c);
-      const float4 x = __ldcg(po), y = __ldcg(po + 1);
+      float* p = attn_part(a, 2 * b + (b == b0), tiles, tile, rows);
+      const float mp = __ldcg(p + row), lp = __ldcg(p + rows + row);
+      const float4 x = __ldcg(attn_piece<kRowMajor>(p, rows, a.dim, row, c));
+      const float4 y = __ldcg(attn_piece<kRowMajor>(p, rows, a.dim, row, c + 4));
       const float mm = fmaxf(m, mp), f = attn_scale(m, mm), fp = attn_scale(mp, mm);
       m = mm;
       l = l * f + lp * fp;
@@ -244,9 +270,9 @@ __device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnSeg& g, i
       for (int i = 0; i < 8; ++i) o[i] = fmaf(v[i], fp, o[i] * f);
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int64_t at = attn_out_row(a, g, ut, row) * a.dim + c;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) T::store1(a.O, at + i, o[i] * inv);
+    for (int i = 0; i < 8; ++i) o[i] *= inv;
+    attn_store8<T>(a, attn_out_row(a, g, tok0, row) * a.dim + c, o);
   }
 }
 
@@ -290,6 +316,11 @@ cudaError_t attn_page_map(CUtensorMap* m, const AttnArgs& a, const void* base, i
 // SMs of the current device.
 int attn_sm_count();
 
+// Map of the query rows: (column, head, token) boxes of 64 x box_heads x box_tokens.
+cudaError_t attn_query_map(CUtensorMap* m, const AttnArgs& a, int box_heads, int box_tokens);
+
 cudaError_t launch_attn_rows16(const AttnArgs& a, cudaStream_t s);
+cudaError_t launch_attn_tiles(const AttnArgs& a, cudaStream_t s);
+size_t attn_tiles_work_bytes(int dim);
 
 }  // namespace gsi

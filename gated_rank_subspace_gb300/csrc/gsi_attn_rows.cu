@@ -43,10 +43,6 @@ __device__ __forceinline__ void rows_mma(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t rows_pack(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
 // The compute warps only.
 __device__ __forceinline__ void rows_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kRowsWarps * 32) : "memory"); }
 
@@ -133,7 +129,6 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
 
   // ---- compute warps
   const float sl = a.scale * 1.4426950408889634f;  // scores in powers of two
-  const int hq = a.hkv * a.group;
   const int r0 = lane >> 2, c0 = (lane & 3) * 2;
   bool ok = true;
   while (walk.next(a, g)) {  // after a wait that gave up too: the warps meet at barriers
@@ -228,8 +223,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         }
       }
       // the weights enter the second product as bf16: 2^-9 of each, what their own rounding to the cache's type costs
-      const uint32_t p[4] = {rows_pack(sc[0][0], sc[0][1]), rows_pack(sc[0][2], sc[0][3]), rows_pack(sc[1][0], sc[1][1]),
-                             rows_pack(sc[1][2], sc[1][3])};
+      const uint32_t p[4] = {attn_pack(sc[0][0], sc[0][1]), attn_pack(sc[0][2], sc[0][3]), attn_pack(sc[1][0], sc[1][1]),
+                             attn_pack(sc[1][2], sc[1][3])};
       {
         const int vr = warp * 16 + (lane & 15);
         const uint32_t base = vb + vr * 128;
@@ -291,7 +286,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     }
     const bool whole = g.a == 0 && g.b == g.n;
     const int b0 = walk.owner(g.first), b1 = walk.owner(g.last - 1);
-    float* slot = attn_slot(a, 2 * int(blockIdx.x) + (int(blockIdx.x) == b0), 16);
+    float* part = attn_part(a, 2 * int(blockIdx.x) + (int(blockIdx.x) == b0), 1, 0, 16);
     const int vec = a.dim / 8;
     for (int e = tid; e < n_rows * vec; e += kRowsWarps * 32) {
       const int row = e / vec, c = (e - row * vec) * 8;
@@ -310,19 +305,15 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       }
       if (whole) {
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        uint4 w;
-        w.x = rows_pack(v[0] * inv, v[1] * inv);
-        w.y = rows_pack(v[2] * inv, v[3] * inv);
-        w.z = rows_pack(v[4] * inv, v[5] * inv);
-        w.w = rows_pack(v[6] * inv, v[7] * inv);
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.O) + attn_out_row(a, g, ut, row) * a.dim + c) = w;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) v[x] *= inv;
+        attn_store8<BF16>(a, attn_out_row(a, g, tok0, row) * a.dim + c, v);
       } else {
-        float4* dst = reinterpret_cast<float4*>(slot + 32 + size_t(row) * a.dim + c);
-        dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-        dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+        *attn_piece<true>(part, 16, a.dim, row, c) = make_float4(v[0], v[1], v[2], v[3]);
+        *attn_piece<true>(part, 16, a.dim, row, c + 4) = make_float4(v[4], v[5], v[6], v[7]);
         if (c == 0) {
-          slot[row] = mx;
-          slot[16 + row] = sum;
+          part[row] = mx;
+          part[16 + row] = sum;
         }
       }
     }
@@ -331,14 +322,14 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       rows_sync();
       if (tid == 0) {
         const unsigned n = unsigned(b1 - b0 + 1);
-        const bool last = atomicAdd(attn_counter(a, b0), 1u) == n - 1;
-        if (last) *attn_counter(a, b0) = 0;
+        const bool last = atomicAdd(attn_counter(a, b0, 0), 1u) == n - 1;
+        if (last) *attn_counter(a, b0, 0) = 0;
         s_flag[0] = last;
       }
       rows_sync();
       if (s_flag[0]) {
         __threadfence();
-        attn_join<BF16>(a, g, b0, b1, n_rows, 16, ut, tid, kRowsWarps * 32);
+        attn_join<BF16, true>(a, g, b0, b1, 1, 0, 16, n_rows, tok0, tid, kRowsWarps * 32);
       }
     }
     if (tid == 0) s_flag[1] = 0;

@@ -1,0 +1,659 @@
+// Attention of many query rows (prompts, chunks, grouped heads): row tiles of
+// 128 on the tensor cores (tcgen05, TMEM), sm_103a.
+
+#include "gsi_attn.cuh"
+
+namespace gsi {
+
+// A unit is NQ row tiles of 128 query rows (floor(128 / G) tokens of the G
+// heads that share a key/value head), over tiles of 128 keys:
+//   S = Q K^T (tcgen05, both operands in shared memory, S in TMEM)
+//   p = 2^(S c - m), l += sum p, per row; where m grows by more than 2^8 the
+//       output so far is scaled to the new m (below that the larger weights
+//       stay within bf16 and float32 range and the scaling is saved)
+//   O += P V (P bf16 in TMEM over the columns of S, V in shared memory)
+// Roles: one thread issues every product; a copy warp fills a ring of 16 KB
+// slots by TMA (a K slot is 64 columns of the tile's 128 keys, a V slot all
+// columns of some keys), in the order in which the products use them; a
+// warpgroup a row tile owns the softmax (a thread a row, so neither maximum
+// nor sum needs an exchange); two warps clean the masked tiles' V (below).
+// Up to 128 columns NQ = 2: the products of one row tile run while the other
+// one's softmax does, and each key is read from L2 once for 256 rows.  Above,
+// the output of one tile takes half of TMEM, and two S buffers of one row tile
+// alternate instead.
+//
+// Masked tiles: S is masked in registers; a weight of 0 hides a number of V
+// but not an infinity or NaN, nor the ring's stale bytes where no page was
+// copied, so those values are set to zero in shared memory before the product
+// and the non-finite ones that a row does see are added at its end.
+constexpr int kTileKeys = 128;
+constexpr int kSlotBytes = 16384;
+
+template <int NS>
+struct TilesCfg {
+  static constexpr int kNQ = NS <= 2 ? 2 : 1;
+  static constexpr int kVK = NS == 1 ? 128 : NS == 2 ? 64 : 32;  // keys of a V slot
+  static constexpr int kNV = kTileKeys / kVK;
+  static constexpr int kSoftWarps = 4 * kNQ;
+  static constexpr int kThreads = 32 * (kSoftWarps + 4);
+  static constexpr int kQBytes = kNQ * NS * kSlotBytes;
+  static constexpr int kSlots = (232448 - 2048 - kQBytes) / kSlotBytes;
+  static constexpr size_t kSmem = 1024 + size_t(kQBytes) + size_t(kSlots) * kSlotBytes + 1024;
+  static constexpr int kOCol = 256;  // TMEM: S buffers at 0 and 128, O from here
+  static_assert(kNV * kVK == kTileKeys && NS * 128 * kVK <= kSlotBytes, "V slots");
+  static_assert(kOCol + kNQ * NS * 64 <= 512, "TMEM columns");
+};
+
+struct TilesBars {
+  uint64_t full[12], empty[12];
+  uint64_t dirty, clean;  // a masked tile's V is there; it is cleaned
+  uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
+  uint64_t q_full, done;
+  uint32_t tmem;
+  int found[8];  // per segment (mod 8): its number + 1 where a non-finite value was taken out
+  int last[2];
+};
+static_assert(sizeof(TilesBars) <= 1024, "barriers");
+
+// ------------------------------------------------------------------ tcgen05
+__device__ __forceinline__ void tl_mma_ss(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(ad), "l"(bd), "r"(idesc), "r"(uint32_t(acc))
+      : "memory");
+}
+__device__ __forceinline__ void tl_mma_ts(uint32_t d, uint32_t at, uint64_t bd, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+      "r"(at), "l"(bd), "r"(idesc), "r"(uint32_t(acc))
+      : "memory");
+}
+__device__ __forceinline__ void tl_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(sa(bar)) : "memory");
+}
+__device__ __forceinline__ void tl_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tl_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tl_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tl_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+#define GSI_R8(r, i) "=r"((r)[(i)]), "=r"((r)[(i) + 1]), "=r"((r)[(i) + 2]), "=r"((r)[(i) + 3]), "=r"((r)[(i) + 4]), \
+                     "=r"((r)[(i) + 5]), "=r"((r)[(i) + 6]), "=r"((r)[(i) + 7])
+#define GSI_W8(r, i) "r"((r)[(i)]), "r"((r)[(i) + 1]), "r"((r)[(i) + 2]), "r"((r)[(i) + 3]), "r"((r)[(i) + 4]), \
+                     "r"((r)[(i) + 5]), "r"((r)[(i) + 6]), "r"((r)[(i) + 7])
+// 32 columns of this warp's 32 lanes (no wait).
+__device__ __forceinline__ void tl_ld32(uint32_t t, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, "
+      "[%32];"
+      : GSI_R8(r, 0), GSI_R8(r, 8), GSI_R8(r, 16), GSI_R8(r, 24)
+      : "r"(t));
+}
+__device__ __forceinline__ void tl_st32(uint32_t t, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+      ::"r"(t), GSI_W8(r, 0), GSI_W8(r, 8), GSI_W8(r, 16), GSI_W8(r, 24)
+      : "memory");
+}
+
+// Shared-memory operand descriptors, 128-byte swizzle (version 1).  K-major
+// (Q, K: rows of 64 columns): 8-row groups 1024 bytes apart.  MN-major (V: a
+// row is a key, its 64 columns run along N): 8-key groups 1024 bytes apart,
+// the next 64 columns `slab` bytes on.
+__device__ __forceinline__ uint64_t tl_desc(uint32_t addr, uint32_t slab) {
+  return uint64_t((addr & 0x3ffffu) >> 4) | (uint64_t(slab >> 4) << 16) | (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) |
+         (uint64_t(2) << 61);
+}
+// kind::f16, A and B bf16, D float32; b_mn: B is MN-major.
+__host__ __device__ constexpr uint32_t tl_idesc(int n, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(b_mn) << 16) | (uint32_t(n >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+}
+
+__device__ __forceinline__ void tl_load_query(uint32_t dst, const CUtensorMap* map, uint32_t bar, int col, int head, int tok) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(col), "r"(head), "r"(tok), "r"(bar)
+      : "memory");
+}
+
+// What every role derives from a segment: the row tiles' tokens and key ranges.
+template <int NQ>
+struct TilesSeg {
+  int tok0[NQ], n_tok[NQ];  // tokens of each row tile
+  int ja[NQ], jb[NQ];       // the segment's tiles (of the unit) that some row of it sees
+  int lo_all, lim_all;      // keys that some row of the unit sees
+  int lo_max, lim_min;      // keys that every row of the unit sees lie in [lo_max, lim_min)
+  __device__ __forceinline__ void set(const AttnArgs& a, const AttnSeg& g, int tpt) {
+    const int u0 = g.u * NQ * tpt, u1 = min(u0 + NQ * tpt, g.q.q_len);
+    lim_min = attn_lim(a, g.q, u0);
+    lim_all = attn_lim(a, g.q, u1 - 1);
+    lo_all = attn_lo(a, lim_min);
+    lo_max = attn_lo(a, lim_all);
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      tok0[q] = u0 + q * tpt;
+      n_tok[q] = max(0, min(tpt, u1 - tok0[q]));
+      ja[q] = jb[q] = g.a;
+      if (n_tok[q] > 0 && g.b > g.a) {
+        const int lim = attn_lim(a, g.q, tok0[q] + n_tok[q] - 1), lo = attn_lo(a, attn_lim(a, g.q, tok0[q]));
+        ja[q] = max(g.a, lo / kTileKeys - g.t0);
+        jb[q] = min(g.b, (lim + kTileKeys - 1) / kTileKeys - g.t0);
+        if (jb[q] <= ja[q]) ja[q] = jb[q] = g.a;
+      }
+    }
+  }
+  __device__ __forceinline__ bool sees(int q, int j) const { return j >= ja[q] && j < jb[q]; }
+  // some row does not see some key of tile t
+  __device__ __forceinline__ bool masked(int t) const { return t * kTileKeys < lo_max || (t + 1) * kTileKeys > lim_min; }
+};
+
+template <int NS>
+__global__ void __launch_bounds__(TilesCfg<NS>::kThreads, 1)
+    attn_tiles_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                      const __grid_constant__ CUtensorMap mv, const __grid_constant__ AttnArgs a) {
+  using C = TilesCfg<NS>;
+  constexpr int NQ = C::kNQ, NV = C::kNV, VK = C::kVK, SLOTS = C::kSlots;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* s_q = base;
+  uint8_t* ring = base + C::kQBytes;
+  TilesBars& bars = *reinterpret_cast<TilesBars*>(ring + SLOTS * kSlotBytes);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_launch_dependents();
+  if (tid == 0) {
+    for (int s = 0; s < SLOTS; ++s) {
+      bar_init(&bars.full[s], 1);
+      bar_init(&bars.empty[s], 1);
+    }
+    bar_init(&bars.dirty, 1);
+    bar_init(&bars.clean, 2);
+    for (int q = 0; q < 2; ++q) {
+      bar_init(&bars.s_full[q], 1);
+      bar_init(&bars.p_full[q], 4);
+      bar_init(&bars.pv_done[q], 1);
+      bar_init(&bars.o_free[q], 4);
+    }
+    bar_init(&bars.q_full, 1);
+    bar_init(&bars.done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&mq) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&mk) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&mv) : "memory");
+    for (int i = 0; i < 8; ++i) bars.found[i] = 0;
+  }
+  if (warp == C::kSoftWarps) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sa(&bars.tmem)), "r"(512u) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tl_fence_before();
+  pdl_wait();
+  const int tpt = 128 / a.group, ut = NQ * tpt;
+  const AttnShare share = attn_share<C::kThreads>(a, ut, kTileKeys);  // its block barriers publish the ones above
+  tl_fence_after();
+  const uint32_t tmem = bars.tmem;
+  AttnWalk walk;
+  walk.begin(a, share, ut, kTileKeys);
+  uint32_t* err = attn_err(a);
+  AttnSeg g;
+  TilesSeg<NQ> t;
+  bool ok = true;
+
+  if (warp >= C::kSoftWarps) {
+    if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == C::kSoftWarps) {
+      // ---- the products (one thread)
+      if (lane == 0) {
+        constexpr uint32_t id_qk = tl_idesc(kTileKeys, false), id_pv = tl_idesc(NS * 64, true);
+        int p = 0;                 // ring slots used
+        int n_masked = 0;          // masked tiles so far
+        int n_q = 0, n_s[2] = {0, 0}, n_o[2] = {0, 0}, tile_no = 0;
+        auto load_q = [&]() {
+          t.set(a, g, tpt);
+          if (g.b == g.a) return;
+          int tiles = 0;
+          for (int q = 0; q < NQ; ++q) tiles += t.n_tok[q] > 0;
+          bar_expect_tx(&bars.q_full, uint32_t(tiles * NS * tpt * a.group) * 128);
+          for (int q = 0; q < tiles; ++q)
+            for (int s = 0; s < NS; ++s)
+              tl_load_query(sa(s_q + (q * NS + s) * kSlotBytes), &mq, sa(&bars.q_full), s * 64, g.h * a.group,
+                            g.q.q0 + t.tok0[q]);
+        };
+        auto wait_slots = [&](int first, int n, bool masked) {
+          for (int i = first; ok && i < first + n; ++i)
+            ok = bar_wait(&bars.full[i % SLOTS], uint32_t(i / SLOTS) & 1u, err);
+          if (masked && ok) {
+            bar_arrive(&bars.dirty);
+            ok = bar_wait(&bars.clean, uint32_t(n_masked++) & 1u, err);
+          }
+          tl_fence_after();
+        };
+        auto release = [&](int first, int n) {
+          for (int i = first; i < first + n; ++i) tl_commit(&bars.empty[i % SLOTS]);
+        };
+        auto qk = [&](int q, int buf, int slot) {
+#pragma unroll
+          for (int s = 0; s < NS; ++s) {
+            const uint64_t ad = tl_desc(sa(s_q + (q * NS + s) * kSlotBytes), 0);
+            const uint64_t bd = tl_desc(sa(ring + ((slot + s) % SLOTS) * kSlotBytes), 0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              tl_mma_ss(tmem + buf * 128, ad + uint64_t(2 * k), bd + uint64_t(2 * k), id_qk, (s | k) != 0);
+          }
+          tl_commit(&bars.s_full[buf]);
+        };
+        auto pv = [&](int q, int buf, int slot, bool first) {
+#pragma unroll
+          for (int k = 0; k < kTileKeys / 16; ++k) {
+            const uint64_t bd = tl_desc(sa(ring + ((slot + k * 16 / VK) % SLOTS) * kSlotBytes) + (k * 16 % VK) * 128, VK * 128);
+            tl_mma_ts(tmem + C::kOCol + q * 128, tmem + buf * 128 + k * 8, bd, id_pv, !(first && k == 0));
+          }
+          tl_commit(&bars.pv_done[q]);
+        };
+        bool have = walk.next(a, g);
+        if (have) load_q();
+        while (ok && have) {
+          if (g.b > g.a) {
+            ok = bar_wait(&bars.q_full, uint32_t(n_q++) & 1u, err);
+            tl_fence_after();
+            if constexpr (NQ == 2) {
+              if (ok) wait_slots(p, NS, false);
+              if (ok) {
+                for (int q = 0; q < 2; ++q)
+                  if (t.sees(q, g.a)) qk(q, q, p);
+                release(p, NS);
+              }
+              for (int j = g.a; ok && j < g.b; ++j) {
+                const int vs = p + NS, ks = vs + NV;
+                bool v_in = false, k_in = false;
+                for (int q = 0; q < 2 && ok; ++q) {
+                  if (t.sees(q, j)) {
+                    if (!v_in) wait_slots(vs, NV, t.masked(g.t0 + j));
+                    v_in = true;
+                    const bool first = j == t.ja[q];
+                    if (ok && first && n_o[q] > 0) ok = bar_wait(&bars.o_free[q], uint32_t(n_o[q] - 1) & 1u, err);
+                    n_o[q] += first;
+                    if (ok) ok = bar_wait(&bars.p_full[q], uint32_t(n_s[q]++) & 1u, err);
+                    tl_fence_after();
+                    if (ok) pv(q, q, vs, first);
+                  }
+                  if (ok && j + 1 < g.b && t.sees(q, j + 1)) {
+                    if (!k_in) wait_slots(ks, NS, false);
+                    k_in = true;
+                    if (ok) qk(q, q, ks);
+                  }
+                }
+                // a slot is given back only after its copy has landed
+                if (ok && !v_in) wait_slots(vs, NV, t.masked(g.t0 + j));
+                if (ok && !k_in && j + 1 < g.b) wait_slots(ks, NS, false);
+                if (!ok) break;
+                release(vs, NV);
+                if (j + 1 < g.b) release(ks, NS);
+                p = ks;
+              }
+            } else {
+              if (ok) wait_slots(p, NS, false);
+              if (ok) {
+                qk(0, tile_no & 1, p);
+                release(p, NS);
+              }
+              p += NS;
+              for (int j = g.a; ok && j < g.b; ++j, ++tile_no) {
+                if (j + 1 < g.b) {
+                  wait_slots(p, NS, false);
+                  if (!ok) break;
+                  qk(0, (tile_no + 1) & 1, p);
+                  release(p, NS);
+                  p += NS;
+                }
+                wait_slots(p, NV, t.masked(g.t0 + j));
+                const bool first = j == g.a;
+                if (ok && first && n_o[0] > 0) ok = bar_wait(&bars.o_free[0], uint32_t(n_o[0] - 1) & 1u, err);
+                n_o[0] += first;
+                if (ok) ok = bar_wait(&bars.p_full[tile_no & 1], uint32_t(tile_no >> 1) & 1u, err);
+                tl_fence_after();
+                if (!ok) break;
+                pv(0, tile_no & 1, p, first);
+                release(p, NV);
+                p += NV;
+              }
+            }
+          }
+          // every S of this segment has been read, so Q may be replaced
+          have = walk.next(a, g);
+          if (ok && have) load_q();
+        }
+        tl_commit(&bars.done);
+        bar_wait(&bars.done, 0, err, ok ? kSpinCycles : kSpinCyclesAfterError);
+        if (!ok && n_q >= 0) bar_wait(&bars.q_full, uint32_t(n_q) & 1u, err, kSpinCyclesAfterError);
+      }
+      __syncwarp();
+    } else if (warp == C::kSoftWarps + 1) {
+      // ---- copies: lane l issues box l of a slot (at most 8)
+      const int page = 1 << a.page_shift;
+      const int bk = min(page, kTileKeys), bv = min(page, VK);
+      int p = 0;
+      // the copy of one slot: K columns of slab `part`, or V keys of group `part`; pid: lane i has the tile's page i
+      auto slot_copy = [&](bool is_v, int part, int key0, int pid) {
+        const int s = p % SLOTS;
+        const int rows = is_v ? bv : bk, per = (is_v ? VK : kTileKeys) / rows;  // boxes of 64 columns
+        const int b = lane % per, slab = is_v ? lane / per : part;
+        const int row0 = (is_v ? part * VK : 0) + b * rows;  // in the tile
+        const bool mine = lane < (is_v ? NS * per : per) && key0 + row0 < t.lim_all && key0 + row0 + rows > t.lo_all;
+        const int id = __shfl_sync(0xffffffffu, pid, page >= kTileKeys ? 0 : row0 >> a.page_shift);
+        if (p >= SLOTS) ok = __all_sync(0xffffffffu, bar_wait(&bars.empty[s], uint32_t(p / SLOTS - 1) & 1u, err));
+        if (!ok) return;
+        const uint32_t bytes = uint32_t(rows) * 128;
+        const int n = __popc(__ballot_sync(0xffffffffu, mine));
+        if (lane == 0) bar_expect_tx(&bars.full[s], uint32_t(n) * bytes);
+        __syncwarp();
+        if (mine)
+          tma_load_page(sa(ring + s * kSlotBytes) + (is_v ? slab * VK * 128 : 0) + b * bytes, is_v ? &mv : &mk,
+                        sa(&bars.full[s]), slab * 64, (key0 + row0) & (page - 1), g.h, id);
+        ++p;
+      };
+      while (ok && walk.next(a, g)) {
+        t.set(a, g, tpt);
+        const int32_t* row = a.table + int64_t(g.r) * a.width;
+        auto page_of = [&](int j) {  // lane i: page i of tile j (0 where no row sees it)
+          const int k = (g.t0 + j) * kTileKeys + lane * page;
+          return j < g.b && lane * page < kTileKeys && k < t.lim_all && k + page > t.lo_all ? __ldcg(row + (k >> a.page_shift)) : 0;
+        };
+        int pid = page_of(g.a);
+        if constexpr (NQ == 2) {
+          for (int j = g.a; ok && j < g.b; ++j) {
+            const int next = page_of(j + 1);
+            const int key0 = (g.t0 + j) * kTileKeys;
+            for (int i = 0; ok && i < NS; ++i) slot_copy(false, i, key0, pid);
+            for (int i = 0; ok && i < NV; ++i) slot_copy(true, i, key0, pid);
+            pid = next;
+          }
+        } else {
+          const int k0 = (g.t0 + g.a) * kTileKeys;
+          if (g.b > g.a)
+            for (int i = 0; ok && i < NS; ++i) slot_copy(false, i, k0, pid);
+          for (int j = g.a; ok && j < g.b; ++j) {
+            const int next = page_of(j + 1);
+            const int key0 = (g.t0 + j) * kTileKeys;
+            if (j + 1 < g.b)
+              for (int i = 0; ok && i < NS; ++i) slot_copy(false, i, key0 + kTileKeys, next);
+            for (int i = 0; ok && i < NV; ++i) slot_copy(true, i, key0, pid);
+            pid = next;
+          }
+        }
+      }
+      // the copies in flight land before the CTA leaves
+      for (int j = max(p - SLOTS, 0); j < p; ++j)
+        bar_wait(&bars.full[j % SLOTS], uint32_t(j / SLOTS) & 1u, err, ok ? kSpinCycles : kSpinCyclesAfterError);
+    } else {
+      // ---- masked tiles' V: what lies outside the unit's keys, or is not finite, becomes zero
+      const int ct = tid - 32 * (C::kSoftWarps + 2);  // 0 .. 63
+      int p = 0, seg = 0, n_masked = 0;
+      while (ok && walk.next(a, g)) {
+        t.set(a, g, tpt);
+        for (int j = g.a; ok && j < g.b; ++j) {
+          // the V slots of tile j, in the order of the copies
+          int vs;
+          if constexpr (NQ == 2) {
+            vs = p + (j - g.a) * (NS + NV) + NS;
+          } else {
+            vs = p + NS + (j - g.a) * (NS + NV) + (j + 1 < g.b ? NS : 0);
+          }
+          if (!t.masked(g.t0 + j)) continue;
+          const int key0 = (g.t0 + j) * kTileKeys;
+          bool found = false;
+          ok = __all_sync(0xffffffffu, bar_wait(&bars.dirty, uint32_t(n_masked++) & 1u, err));
+          if (!ok) break;
+          for (int v = 0; v < NV; ++v) {
+            const int s = (vs + v) % SLOTS;
+            uint8_t* sl = ring + s * kSlotBytes;
+            for (int e = ct; e < NS * VK * 8; e += 64) {  // 16-byte pieces; a row is 128 bytes of a slab
+              const int key = key0 + v * VK + (e >> 3) % VK;
+              uint4* x = reinterpret_cast<uint4*>(sl) + e;
+              if (key < t.lo_all || key >= t.lim_all) {
+                *x = make_uint4(0, 0, 0, 0);
+              } else {
+                uint4 y = *x;
+                uint32_t* w = reinterpret_cast<uint32_t*>(&y);
+                bool bad = false;
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                  if ((w[z] & 0x7f80u) == 0x7f80u) w[z] &= 0xffff0000u, bad = true;
+                  if ((w[z] & 0x7f800000u) == 0x7f800000u) w[z] &= 0xffffu, bad = true;
+                }
+                if (bad) {
+                  *x = y;
+                  found = true;
+                }
+              }
+            }
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // these writes, before the product reads
+          if (found) bars.found[seg & 7] = seg + 1;
+          __syncwarp();
+          if (lane == 0) bar_arrive(&bars.clean);
+        }
+        p += (g.b - g.a) * (NS + NV);
+        ++seg;
+      }
+    }
+  } else {
+    // ---- softmax: a warpgroup a row tile, a thread a row
+    if constexpr (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int q = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+    const float c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f);  // powers of two; a scale of 0 still masks
+    const bool neg = a.scale < 0.f;
+    const uint32_t o_at = tmem + lanes + C::kOCol + q * 128;
+    int ks = 0, seg = 0;
+    while (walk.next(a, g)) {  // after a wait that gave up too: the warps of a row tile meet at barriers
+      t.set(a, g, tpt);
+      const int this_seg = seg++;
+      const int tok0 = q == 0 ? t.tok0[0] : t.tok0[NQ - 1], n_tok = q == 0 ? t.n_tok[0] : t.n_tok[NQ - 1];
+      const int ja = q == 0 ? t.ja[0] : t.ja[NQ - 1], jb = q == 0 ? t.jb[0] : t.jb[NQ - 1];
+      if (n_tok == 0) continue;
+      const int n_rows = n_tok * a.group;
+      const int my_tok = tok0 + min(row / a.group, n_tok - 1);
+      const int lim = attn_lim(a, g.q, my_tok), lo = attn_lo(a, lim);
+      const int lim_min = attn_lim(a, g.q, tok0), lo_max = attn_lo(a, attn_lim(a, g.q, tok0 + n_tok - 1));
+      float m = -INFINITY, l = 0.f;  // m in units of S; weights are 2^(c (S - m))
+      for (int j = ja; j < jb; ++j, ++ks) {
+        const int buf = NQ == 2 ? q : ks & 1;
+        const uint32_t s_at = tmem + lanes + buf * 128;
+        ok = ok && __all_sync(0xffffffffu, bar_wait(&bars.s_full[buf], uint32_t(NQ == 2 ? ks : ks >> 1) & 1u, err));
+        if (!ok) continue;
+        tl_fence_after();
+        uint32_t sr[128];
+        float* s = reinterpret_cast<float*>(sr);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tl_ld32(s_at + 32 * i, sr + 32 * i);
+        tl_wait_ld();
+        const int tile = (g.t0 + j) * kTileKeys;
+        if (neg) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i) s[i] = -s[i];
+        }
+        if (tile < lo_max || tile + kTileKeys > lim_min) {
+          const int from = lo - tile, to = lim - tile;
+#pragma unroll
+          for (int i = 0; i < 128; ++i) s[i] = i >= from && i < to ? s[i] : -INFINITY;
+        }
+        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int i = 4; i < 128; i += 4)
+#pragma unroll
+          for (int z = 0; z < 4; ++z) mx[z] = fmaxf(mx[z], s[i + z]);
+        const float m_new = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), m);
+        // (m_new - m is NaN where both are infinite: nothing to scale)
+        if (__any_sync(0xffffffffu, (m_new - m) * c > 8.f)) {
+          const float f = m == -INFINITY ? 0.f : ex2((m - m_new) * c);
+          m = m_new;
+          l *= f;
+          if (j > ja) {
+            ok = __all_sync(0xffffffffu, bar_wait(&bars.pv_done[q], uint32_t(ks - 1) & 1u, err));
+            if (!ok) continue;
+            tl_fence_after();
+#pragma unroll 1
+            for (int i = 0; i < NS * 2; ++i) {
+              uint32_t r[32];
+              tl_ld32(o_at + 32 * i, r);
+              tl_wait_ld();
+#pragma unroll
+              for (int z = 0; z < 32; ++z) r[z] = __float_as_uint(__uint_as_float(r[z]) * f);
+              tl_st32(o_at + 32 * i, r);
+            }
+          }
+        }
+        float mc = m == -INFINITY ? 0.f : m * c;
+        // S c - m c as one fused product is off by up to |m c| 2^-24, at large scores more than S itself is where the
+        // scores are alike: subtract first there
+        if (__any_sync(0xffffffffu, fabsf(mc) > 256.f)) {
+          const float d = mc == 0.f ? 0.f : m;
+#pragma unroll
+          for (int i = 0; i < 128; ++i) s[i] -= d;
+          mc = 0.f;
+        }
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t pr[64];
+#pragma unroll
+        for (int i = 0; i < 128; i += 2) {
+          const float x = ex2(fmaf(s[i], c, -mc)), y = ex2(fmaf(s[i + 1], c, -mc));
+          sum[i & 2] += x;
+          sum[(i & 2) + 1] += y;
+          // the weights enter the second product as bf16 (2^-8 of each at most, like the cache's own rounding)
+          pr[i / 2] = attn_pack(x, y);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tl_st32(s_at, pr);
+        tl_st32(s_at + 32, pr + 32);
+        tl_wait_st();
+        tl_fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bars.p_full[buf]);
+      }
+
+      // ---- the segment's end: the rows are finished, or left as a part
+      const bool some = jb > ja;
+      if (some && ok) {
+        // with two S buffers only the product before the last but one is known to be done here: a parity wait must
+        // not skip a phase
+        if (NQ == 1 && ks > 1) bar_wait(&bars.pv_done[q], uint32_t(ks - 2) & 1u, err);
+        ok = __all_sync(0xffffffffu, bar_wait(&bars.pv_done[q], uint32_t(ks - 1) & 1u, err));
+        tl_fence_after();
+      }
+      const bool whole = g.a == 0 && g.b == g.n;
+      const bool any = some && *reinterpret_cast<volatile int*>(&bars.found[this_seg & 7]) == this_seg + 1;
+      const int b0 = walk.owner(g.first), b1 = walk.owner(g.last - 1);
+      float* part = attn_part(a, 2 * int(blockIdx.x) + (int(blockIdx.x) == b0), NQ, q, 128);
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const int64_t out = row < n_rows ? attn_out_row(a, g, tok0, row) * a.dim : 0;
+#pragma unroll 1
+      for (int i = 0; i < NS * 2; ++i) {
+        uint32_t r[32];
+        __syncwarp();
+        if (some && ok) {
+          tl_ld32(o_at + 32 * i, r);
+          tl_wait_ld();
+        } else {
+#pragma unroll
+          for (int z = 0; z < 32; ++z) r[z] = 0;
+        }
+        if (row < n_rows) {
+#pragma unroll
+          for (int z = 0; z < 32; z += 8) {
+            const int col = 32 * i + z;
+            if (col >= a.dim) break;
+            float v[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) v[x] = __uint_as_float(r[z + x]);
+            if (any)
+#pragma unroll 1
+              for (int x = 0; x < 8; ++x)
+                v[x] = attn_nonfinite<BF16>(a, g, kTileKeys, lo, lim, t.lo_max, t.lim_min, col + x, v[x]);
+            if (whole) {
+#pragma unroll
+              for (int x = 0; x < 8; ++x) v[x] *= inv;
+              attn_store8<BF16>(a, out + col, v);
+            } else {
+              *attn_piece<false>(part, 128, a.dim, row, col) = make_float4(v[0], v[1], v[2], v[3]);
+              *attn_piece<false>(part, 128, a.dim, row, col + 4) = make_float4(v[4], v[5], v[6], v[7]);
+            }
+          }
+        }
+      }
+      if (some) {
+        tl_fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bars.o_free[q]);
+      }
+      if (!whole) {
+        if (row < n_rows) {
+          part[row] = m == -INFINITY ? m : m * c;
+          part[128 + row] = l;
+        }
+        __threadfence();
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory");
+        if ((warp & 3) == 0 && lane == 0) {
+          const unsigned n = unsigned(b1 - b0 + 1);
+          const bool last = atomicAdd(attn_counter(a, b0, q), 1u) == n - 1;
+          if (last) *attn_counter(a, b0, q) = 0;
+          bars.last[q] = last;
+        }
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory");
+        if (*reinterpret_cast<volatile int*>(&bars.last[q])) {
+          __threadfence();
+          attn_join<BF16, false>(a, g, b0, b1, NQ, q, 128, n_rows, tok0, row, 128);
+        }
+      }
+    }
+  }
+  tl_fence_before();
+  __syncthreads();
+  if (warp == C::kSoftWarps)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+}
+
+template <int NS>
+static cudaError_t launch_tiles(const AttnArgs& a, cudaStream_t s) {
+  using C = TilesCfg<NS>;
+  static_assert(C::kSmem <= 232448 && C::kSlots <= 12, "shared memory of an SM");
+  const int page = 1 << a.page_shift;
+  CUtensorMap mq, mk, mv;
+  cudaError_t e = attn_query_map(&mq, a, a.group, 128 / a.group);
+  if (e == cudaSuccess) e = attn_page_map(&mk, a, a.K, page < kTileKeys ? page : kTileKeys);
+  if (e == cudaSuccess) e = attn_page_map(&mv, a, a.V, page < C::kVK ? page : C::kVK);
+  if (e != cudaSuccess) return e;
+  static bool set = false;  // a function attribute, the same for every call
+  if (!set) {
+    e = cudaFuncSetAttribute(attn_tiles_kernel<NS>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::kSmem));
+    if (e != cudaSuccess) return e;
+    set = true;
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(min(attn_sm_count(), kAttnCtas));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_tiles_kernel<NS>, mq, mk, mv, a);
+}
+
+cudaError_t launch_attn_tiles(const AttnArgs& a, cudaStream_t s) {
+  switch ((a.dim + 63) / 64) {
+    case 1: return launch_tiles<1>(a, s);
+    case 2: return launch_tiles<2>(a, s);
+    case 3: return launch_tiles<3>(a, s);
+    default: return launch_tiles<4>(a, s);
+  }
+}
+
+size_t attn_tiles_work_bytes(int dim) { return attn_work_bytes(dim <= 128 ? 256 : 128, dim); }
+
+}  // namespace gsi

@@ -248,6 +248,16 @@ def test_attention_long(gsi, dt, D, lens):
     attention_case(gsi, dt, 2, 1, D, 64, lens)
 
 
+@pytest.mark.parametrize("dt,hq,hkv,D,page,lens,window", [
+    (BF, 16, 16, 128, 16, [(700, 3000), (60, 2000)], 0), (BF, 16, 8, 64, 64, [(600, 600), (513, 2000)], 0),
+    (BF, 12, 12, 256, 32, [(400, 2300), (130, 131)], 0), (BF, 8, 8, 192, 128, [(500, 1500)], 0),
+    (BF, 16, 16, 128, 16, [(900, 1900)], 300), (BF, 8, 8, 256, 64, [(700, 1900)], 200), (BF, 24, 8, 80, 32, [(300, 4000)], 0),
+    (BF, 16, 16, 128, 16, [(1, 9000), (1, 3001)], 0), (BF, 16, 2, 256, 64, [(1, 9000), (2, 8000)] * 3, 0),
+    (BF, 8, 8, 64, 32, [(1, 20000), (0, 9), (1, 1)], 0), (F, 8, 8, 64, 16, [(150, 1500), (1, 4000)], 0)])
+def test_attention_many_tiles_a_cta(gsi, dt, hq, hkv, D, page, lens, window):
+    attention_case(gsi, dt, hq, hkv, D, page, lens, window=window)
+
+
 @pytest.mark.parametrize("dt", [BF, F])
 @pytest.mark.parametrize("lens", [[(1, 40), (1, 200)], [(140, 300)], [(6, 9)]], ids=str)
 def test_attention_table_entries_outside_the_cache(gsi, dt, lens):
