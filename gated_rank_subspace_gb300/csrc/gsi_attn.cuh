@@ -57,16 +57,32 @@ __device__ __forceinline__ long long attn_head_cost(const AttnArgs& a, const Att
   return s;
 }
 
+// A cut within `snap` tiles of a unit's end is moved there: the share grows or
+// shrinks by less than the part of a unit would cost to write and join.
 struct AttnShare {
   long long total, pos, end;  // tiles of the line: all, and this CTA's
   long long off;              // pos inside request r
-  int r, grid;                // grid: the CTAs that have a share (all, or as many as there are tiles)
+  int r, grid, snap;          // grid: the CTAs that have a share (all, or as many as there are tiles)
 };
+
+// The cut at place `at` of request r, moved to the end of its unit where that is near.
+__device__ __forceinline__ long long attn_snap(const AttnArgs& a, const AttnReq& q, long long at, int ut, int kt, int snap) {
+  if (snap == 0) return at;
+  const long long per = attn_head_cost(a, q, ut, kt);
+  long long rem = at % per;
+  for (int u = 0;; ++u) {
+    int t0, n;
+    attn_tiles(a, q, u, ut, kt, t0, n);
+    const int c = max(1, n);
+    if (rem < c) return rem <= snap ? at - rem : c - rem <= snap ? at + c - rem : at;
+    rem -= c;
+  }
+}
 
 // The share of CTA blockIdx.x; all NT threads of the block.
 template <int NT>
-__device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, int ut, int kt) {
-  __shared__ long long s_sum[NT / 32], s_off;
+__device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, int ut, int kt, int snap) {
+  __shared__ long long s_sum[NT / 32], s_off, s_cut[2];
   __shared__ int s_r;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r0 = int((long long)a.n_req * tid / NT), r1 = int((long long)a.n_req * (tid + 1) / NT);
@@ -89,24 +105,35 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, int ut, int k
   AttnShare s;
   s.total = total;
   s.grid = int(total < (long long)gridDim.x ? total : (long long)gridDim.x);
+  s.snap = total >= (long long)s.grid * 4 * snap ? snap : 0;  // small shares are cut where they fall
   s.pos = s.end = 0;
   if (int(blockIdx.x) < s.grid) {
-    s.pos = total * blockIdx.x / s.grid;
-    s.end = total * (blockIdx.x + 1) / s.grid;
-    if (before <= s.pos && s.pos < before + mine) {
-      long long at = s.pos - before;
-      for (int r = r0; r < r1; ++r) {
-        const long long c = attn_head_cost(a, attn_request(a, r), ut, kt) * a.hkv;
-        if (at < c) {
-          s_r = r;
-          s_off = at;
-          break;
+    const long long cut[2] = {total * blockIdx.x / s.grid, total * (blockIdx.x + 1) / s.grid};
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (before <= cut[i] && cut[i] < before + mine) {
+        long long at = cut[i] - before;
+        for (int r = r0; r < r1; ++r) {
+          const AttnReq q = attn_request(a, r);
+          const long long c = attn_head_cost(a, q, ut, kt) * a.hkv;
+          if (at < c) {
+            const long long to = attn_snap(a, q, at, ut, kt, s.snap);
+            s_cut[i] = cut[i] + to - at;
+            if (i == 0) {
+              s_r = r;
+              s_off = to;
+            }
+            break;
+          }
+          at -= c;
         }
-        at -= c;
       }
-    }
   }
   __syncthreads();
+  if (int(blockIdx.x) < s.grid) {
+    s.pos = s_cut[0];
+    s.end = int(blockIdx.x) + 1 == s.grid ? total : s_cut[1];
+  }
   s.r = s_r;
   s.off = s_off;
   return s;
@@ -130,9 +157,13 @@ struct AttnWalk {
   long long off;  // tiles of unit u that lie before pos
 
   __device__ __forceinline__ void enter(const AttnArgs& a, long long at) {
-    q = attn_request(a, r);
-    per_head = attn_head_cost(a, q, ut, kt);
-    h = int(at / max(per_head, 1ll));
+    for (;; ++r) {  // the first request that goes on beyond `at`: there is one, the share does
+      q = attn_request(a, r);
+      per_head = attn_head_cost(a, q, ut, kt);
+      if (at < per_head * a.hkv) break;
+      at -= per_head * a.hkv;
+    }
+    h = int(at / per_head);
     off = at - h * per_head;
     for (u = 0;; ++u) {
       int t0, n;
@@ -171,14 +202,18 @@ struct AttnWalk {
         u = 0;
         ++h;
       } else {
-        do ++r; while (attn_request(a, r).q_len == 0);  // there is a next one: the share goes on
+        ++r;
         enter(a, 0);
       }
     }
     return true;
   }
-  // The CTA whose share holds tile x of the line.
-  __device__ __forceinline__ int owner(long long x) const { return int(((x + 1) * s.grid - 1) / s.total); }
+  // The CTAs that hold parts of a unit: the cuts inside it, beyond what is moved to its ends, are those of the CTAs
+  // b0 + 1 .. b1 (none: b0 >= b1).
+  __device__ __forceinline__ void parts(const AttnSeg& g, int& b0, int& b1) const {
+    b0 = int(((g.first + s.snap + 1) * s.grid + s.total - 1) / s.total) - 1;
+    b1 = int(((g.last - s.snap) * s.grid - 1) / s.total);
+  }
 };
 
 // ------------------------------------------------------------------ partial results
@@ -246,33 +281,60 @@ __device__ __forceinline__ void attn_store8(const AttnArgs& a, int64_t at, const
   }
 }
 
-// Joins the parts b0 .. b1 of a row tile and writes its rows; threads tid of nt.
-template <class T, bool kRowMajor>
+// Folds the parts from .. to of a row tile whose first part is b0's into the
+// state (m, l, o[CW], from column c) of one row.  All loads of a part are in
+// flight together.  Starting from the first part's own values or from nothing
+// gives the same bits.
+template <bool kRowMajor, int CW>
+__device__ __forceinline__ void attn_fold(const AttnArgs& a, int from, int to, int b0, int tiles, int tile, int rows,
+                                          int row, int c, float& m, float& l, float (&o)[CW]) {
+#pragma unroll(CW <= 8 ? 4 : 1)
+  for (int b = from; b <= to; ++b) {
+    float* p = attn_part(a, 2 * b + (b == b0), tiles, tile, rows);
+    const float mp = __ldcg(p + row), lp = __ldcg(p + rows + row);
+    float4 v[CW / 4];
+#pragma unroll
+    for (int i = 0; i < CW / 4; ++i)
+      v[i] = c + 4 * i < a.dim ? __ldcg(attn_piece<kRowMajor>(p, rows, a.dim, row, c + 4 * i)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float mm = fmaxf(m, mp), f = attn_scale(m, mm), fp = attn_scale(mp, mm);
+    m = mm;
+    l = l * f + lp * fp;
+#pragma unroll
+    for (int i = 0; i < CW / 4; ++i) {
+      o[4 * i] = fmaf(v[i].x, fp, o[4 * i] * f);
+      o[4 * i + 1] = fmaf(v[i].y, fp, o[4 * i + 1] * f);
+      o[4 * i + 2] = fmaf(v[i].z, fp, o[4 * i + 2] * f);
+      o[4 * i + 3] = fmaf(v[i].w, fp, o[4 * i + 3] * f);
+    }
+  }
+}
+
+// Writes CW columns from c of a finished row: o / l.
+template <class T, int CW>
+__device__ __forceinline__ void attn_finish(const AttnArgs& a, int64_t at, int c, float l, const float (&o)[CW]) {
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int i = 0; i < CW; i += 8) {
+    float w[8];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) w[x] = o[i + x] * inv;
+    if (c + i < a.dim) attn_store8<T>(a, at + i, w);
+  }
+}
+
+// Joins all parts of a row tile and writes its rows; threads tid of nt.
+template <class T, bool kRowMajor, int CW>
 __device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnSeg& g, int b0, int b1, int tiles, int tile,
                                           int rows, int n_rows, int tok0, int tid, int nt) {
-  const int vec = a.dim / 8;
-  for (int e = tid; e < n_rows * vec; e += nt) {
-    const int row = kRowMajor ? e / vec : e % n_rows, c = (kRowMajor ? e % vec : e / n_rows) * 8;
-    float m = -INFINITY, l = 0.f, o[8];
+  const int per = (a.dim + CW - 1) / CW;
+  for (int e = tid; e < (kRowMajor ? n_rows : rows) * per; e += nt) {
+    const int row = kRowMajor ? e / per : e % rows, c = (kRowMajor ? e % per : e / rows) * CW;
+    if (row >= n_rows) continue;
+    float m = -INFINITY, l = 0.f, o[CW];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = 0.f;
-#pragma unroll 4
-    for (int b = b0; b <= b1; ++b) {
-      float* p = attn_part(a, 2 * b + (b == b0), tiles, tile, rows);
-      const float mp = __ldcg(p + row), lp = __ldcg(p + rows + row);
-      const float4 x = __ldcg(attn_piece<kRowMajor>(p, rows, a.dim, row, c));
-      const float4 y = __ldcg(attn_piece<kRowMajor>(p, rows, a.dim, row, c + 4));
-      const float mm = fmaxf(m, mp), f = attn_scale(m, mm), fp = attn_scale(mp, mm);
-      m = mm;
-      l = l * f + lp * fp;
-      const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = fmaf(v[i], fp, o[i] * f);
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] *= inv;
-    attn_store8<T>(a, attn_out_row(a, g, tok0, row) * a.dim + c, o);
+    for (int i = 0; i < CW; ++i) o[i] = 0.f;
+    attn_fold<kRowMajor, CW>(a, b0, b1, b0, tiles, tile, rows, row, c, m, l, o);
+    attn_finish<T, CW>(a, attn_out_row(a, g, tok0, row) * a.dim + c, c, l, o);
   }
 }
 

@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   }
   pdl_wait();
   const int ut = 16 / a.group;
-  const AttnShare share = attn_share<kRowsThreads>(a, ut, kRowsKt);  // also publishes the barriers to the block
+  const AttnShare share = attn_share<kRowsThreads>(a, ut, kRowsKt, 0);  // also publishes the barriers to the block
   AttnWalk walk;
   walk.begin(a, share, ut, kRowsKt);
   uint32_t* err = attn_err(a);
@@ -285,7 +285,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       rows_sync();
     }
     const bool whole = g.a == 0 && g.b == g.n;
-    const int b0 = walk.owner(g.first), b1 = walk.owner(g.last - 1);
+    int b0, b1;
+    walk.parts(g, b0, b1);
     float* part = attn_part(a, 2 * int(blockIdx.x) + (int(blockIdx.x) == b0), 1, 0, 16);
     const int vec = a.dim / 8;
     for (int e = tid; e < n_rows * vec; e += kRowsWarps * 32) {
@@ -329,7 +330,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       rows_sync();
       if (s_flag[0]) {
         __threadfence();
-        attn_join<BF16, true>(a, g, b0, b1, 1, 0, 16, n_rows, tok0, tid, kRowsWarps * 32);
+        attn_join<BF16, true, 8>(a, g, b0, b1, 1, 0, 16, n_rows, tok0, tid, kRowsWarps * 32);
       }
     }
     if (tid == 0) s_flag[1] = 0;

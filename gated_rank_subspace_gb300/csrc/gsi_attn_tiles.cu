@@ -12,9 +12,9 @@ namespace gsi {
 //       output so far is scaled to the new m (below that the larger weights
 //       stay within bf16 and float32 range and the scaling is saved)
 //   O += P V (P bf16 in TMEM over the columns of S, V in shared memory)
-// Roles: one thread issues every product; a copy warp fills a ring of 16 KB
-// slots by TMA (a K slot is 64 columns of the tile's 128 keys, a V slot all
-// columns of some keys), in the order in which the products use them; a
+// Roles: one thread issues every product; a copy warp fills a ring of 32 KB
+// stages by TMA (a K stage is 128 columns of the tile's 128 keys, a V stage all
+// columns of 64 or 128 keys), in the order in which the products use them; a
 // warpgroup a row tile owns the softmax (a thread a row, so neither maximum
 // nor sum needs an exchange); two warps clean the masked tiles' V (below).
 // Up to 128 columns NQ = 2: the products of one row tile run while the other
@@ -27,33 +27,57 @@ namespace gsi {
 // copied, so those values are set to zero in shared memory before the product
 // and the non-finite ones that a row does see are added at its end.
 constexpr int kTileKeys = 128;
-constexpr int kSlotBytes = 16384;
+constexpr int kSlabBytes = 16384;  // 64 columns of 128 rows
+// A cut nearer than this to a unit's end is moved there (tiles; a part of a unit costs about as much to write and join).
+constexpr int kTileSnap = 2;
 
 template <int NS>
 struct TilesCfg {
   static constexpr int kNQ = NS <= 2 ? 2 : 1;
-  static constexpr int kVK = NS == 1 ? 128 : NS == 2 ? 64 : 32;  // keys of a V slot
-  static constexpr int kNV = kTileKeys / kVK;
+  static constexpr int kStage = NS == 1 ? kSlabBytes : 2 * kSlabBytes;
+  static constexpr int kKST = (NS + 1) / 2;             // stages of a K tile: two slabs each
+  static constexpr int kVST = kKST;                     // stages of a V tile
+  static constexpr int kVK = kTileKeys / kVST;          // keys of a V stage
   static constexpr int kSoftWarps = 4 * kNQ;
   static constexpr int kThreads = 32 * (kSoftWarps + 4);
-  static constexpr int kQBytes = kNQ * NS * kSlotBytes;
-  static constexpr int kSlots = (232448 - 2048 - kQBytes) / kSlotBytes;
-  static constexpr size_t kSmem = 1024 + size_t(kQBytes) + size_t(kSlots) * kSlotBytes + 1024;
+  static constexpr int kQBytes = kNQ * NS * kSlabBytes;
+  static constexpr int kStages = (232448 - 2048 - kQBytes) / kStage;
+  static constexpr size_t kSmem = 1024 + size_t(kQBytes) + size_t(kStages) * kStage + 1024;
   static constexpr int kOCol = 256;  // TMEM: S buffers at 0 and 128, O from here
-  static_assert(kNV * kVK == kTileKeys && NS * 128 * kVK <= kSlotBytes, "V slots");
+  static_assert(NS * 128 * kVK <= kStage, "V stages");
+  static_assert(kStages >= 2 * kKST + 1, "a K and a V tile, and one stage ahead");
   static_assert(kOCol + kNQ * NS * 64 <= 512, "TMEM columns");
 };
 
 struct TilesBars {
   uint64_t full[12], empty[12];
   uint64_t dirty, clean;  // a masked tile's V is there; it is cleaned
-  uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
+  uint64_t s_full[2], p_half[2], p_full[2], pv_done[2], o_free[2];
   uint64_t q_full, done;
   uint32_t tmem;
   int found[8];  // per segment (mod 8): its number + 1 where a non-finite value was taken out
   int last[2];
 };
 static_assert(sizeof(TilesBars) <= 1024, "barriers");
+
+// Place in the ring: stage and phase parity.
+template <int N>
+struct TilesRing {
+  int s = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void step(int n) {
+    s += n;
+    if (s >= N) {
+      s -= N;
+      ph ^= 1;
+    }
+  }
+  __device__ __forceinline__ TilesRing at(int n) const {
+    TilesRing r = *this;
+    r.step(n);
+    return r;
+  }
+};
 
 // ------------------------------------------------------------------ tcgen05
 __device__ __forceinline__ void tl_mma_ss(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, bool acc) {
@@ -69,6 +93,15 @@ __device__ __forceinline__ void tl_mma_ts(uint32_t d, uint32_t at, uint64_t bd, 
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
       "r"(at), "l"(bd), "r"(idesc), "r"(uint32_t(acc))
       : "memory");
+}
+// One lane of the warp.  (The compiler knows that a branch on this has one
+// thread, and the products' operands then reach their uniform registers
+// directly; behind `lane == 0` it loops over the threads there might be, at
+// ~190 cycles a product.)
+__device__ __forceinline__ bool tl_elect() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}\n" : "=r"(p));
+  return p != 0;
 }
 __device__ __forceinline__ void tl_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(sa(bar)) : "memory");
@@ -155,17 +188,18 @@ __global__ void __launch_bounds__(TilesCfg<NS>::kThreads, 1)
     attn_tiles_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                       const __grid_constant__ CUtensorMap mv, const __grid_constant__ AttnArgs a) {
   using C = TilesCfg<NS>;
-  constexpr int NQ = C::kNQ, NV = C::kNV, VK = C::kVK, SLOTS = C::kSlots;
+  constexpr int NQ = C::kNQ, VK = C::kVK, KST = C::kKST, VST = C::kVST, STAGES = C::kStages;
+  using Ring = TilesRing<STAGES>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* s_q = base;
   uint8_t* ring = base + C::kQBytes;
-  TilesBars& bars = *reinterpret_cast<TilesBars*>(ring + SLOTS * kSlotBytes);
+  TilesBars& bars = *reinterpret_cast<TilesBars*>(ring + STAGES * C::kStage);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch_dependents();
   if (tid == 0) {
-    for (int s = 0; s < SLOTS; ++s) {
+    for (int s = 0; s < STAGES; ++s) {
       bar_init(&bars.full[s], 1);
       bar_init(&bars.empty[s], 1);
     }
@@ -173,6 +207,7 @@ __global__ void __launch_bounds__(TilesCfg<NS>::kThreads, 1)
     bar_init(&bars.clean, 2);
     for (int q = 0; q < 2; ++q) {
       bar_init(&bars.s_full[q], 1);
+      bar_init(&bars.p_half[q], 4);
       bar_init(&bars.p_full[q], 4);
       bar_init(&bars.pv_done[q], 1);
       bar_init(&bars.o_free[q], 4);
@@ -192,7 +227,7 @@ __global__ void __launch_bounds__(TilesCfg<NS>::kThreads, 1)
   tl_fence_before();
   pdl_wait();
   const int tpt = 128 / a.group, ut = NQ * tpt;
-  const AttnShare share = attn_share<C::kThreads>(a, ut, kTileKeys);  // its block barriers publish the ones above
+  const AttnShare share = attn_share<C::kThreads>(a, ut, kTileKeys, kTileSnap);  // its block barriers publish the ones above
   tl_fence_after();
   const uint32_t tmem = bars.tmem;
   AttnWalk walk;
@@ -203,122 +238,142 @@ __global__ void __launch_bounds__(TilesCfg<NS>::kThreads, 1)
   bool ok = true;
 
   if (warp >= C::kSoftWarps) {
-    if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == C::kSoftWarps) {
       // ---- the products (one thread)
-      if (lane == 0) {
+      if (tl_elect()) {
         constexpr uint32_t id_qk = tl_idesc(kTileKeys, false), id_pv = tl_idesc(NS * 64, true);
-        int p = 0;                 // ring slots used
-        int n_masked = 0;          // masked tiles so far
-        int n_q = 0, n_s[2] = {0, 0}, n_o[2] = {0, 0}, tile_no = 0;
+        const uint64_t dq = tl_desc(sa(s_q), 0), dk = tl_desc(sa(ring), 0), dv = tl_desc(sa(ring), VK * 128);
+        constexpr uint64_t kStageD = C::kStage / 16, kSlabD = kSlabBytes / 16;
+        Ring r;
+        uint32_t ph_q = 0, ph_clean = 0, ph_p[2] = {0, 0}, ph_o[2] = {1, 1};  // the first wait for a free O passes
+        uint32_t buf1 = 0;  // one row tile: the S buffer of the tile
         auto load_q = [&]() {
           t.set(a, g, tpt);
           if (g.b == g.a) return;
-          int tiles = 0;
-          for (int q = 0; q < NQ; ++q) tiles += t.n_tok[q] > 0;
+          const int tiles = NQ == 2 && t.n_tok[NQ - 1] > 0 ? 2 : 1;
           bar_expect_tx(&bars.q_full, uint32_t(tiles * NS * tpt * a.group) * 128);
           for (int q = 0; q < tiles; ++q)
             for (int s = 0; s < NS; ++s)
-              tl_load_query(sa(s_q + (q * NS + s) * kSlotBytes), &mq, sa(&bars.q_full), s * 64, g.h * a.group,
-                            g.q.q0 + t.tok0[q]);
+              tl_load_query(sa(s_q + (q * NS + s) * kSlabBytes), &mq, sa(&bars.q_full), s * 64, g.h * a.group,
+                            g.q.q0 + t.tok0[0] + q * tpt);
         };
-        auto wait_slots = [&](int first, int n, bool masked) {
-          for (int i = first; ok && i < first + n; ++i)
-            ok = bar_wait(&bars.full[i % SLOTS], uint32_t(i / SLOTS) & 1u, err);
-          if (masked && ok) {
-            bar_arrive(&bars.dirty);
-            ok = bar_wait(&bars.clean, uint32_t(n_masked++) & 1u, err);
-          }
+        auto wait_full = [&](const Ring& x) {
+          ok = ok && bar_wait(&bars.full[x.s], x.ph, err);
           tl_fence_after();
         };
-        auto release = [&](int first, int n) {
-          for (int i = first; i < first + n; ++i) tl_commit(&bars.empty[i % SLOTS]);
+        // the V stages at x are there, and cleaned
+        auto wait_v = [&](const Ring& x, bool masked) {
+#pragma unroll
+          for (int i = 0; i < VST; ++i) wait_full(x.at(i));
+          if (masked && ok) {
+            bar_arrive(&bars.dirty);
+            ok = bar_wait(&bars.clean, ph_clean, err);
+            ph_clean ^= 1;
+            tl_fence_after();
+          }
         };
-        auto qk = [&](int q, int buf, int slot) {
+        auto release = [&](const Ring& x, int n) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (i < n) tl_commit(&bars.empty[x.at(i).s]);
+        };
+        // S[buf] = Q_q K^T, K in the stages at x
+        auto qk = [&](int q, uint32_t buf, const Ring& x) {
 #pragma unroll
           for (int s = 0; s < NS; ++s) {
-            const uint64_t ad = tl_desc(sa(s_q + (q * NS + s) * kSlotBytes), 0);
-            const uint64_t bd = tl_desc(sa(ring + ((slot + s) % SLOTS) * kSlotBytes), 0);
+            const uint64_t ad = dq + uint64_t(q * NS + s) * kSlabD;
+            const uint64_t bd = dk + uint64_t(x.at(s / 2).s) * kStageD + uint64_t(s % 2) * kSlabD;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               tl_mma_ss(tmem + buf * 128, ad + uint64_t(2 * k), bd + uint64_t(2 * k), id_qk, (s | k) != 0);
           }
           tl_commit(&bars.s_full[buf]);
         };
-        auto pv = [&](int q, int buf, int slot, bool first) {
+        // O_q += P[buf] V, V in the stages at x.  (Issued by one thread, the products run in order: S[buf] may be
+        // written again by the next one.)
+        // The weights of the first 64 keys come first, so half of the product runs while the others are formed.
+        auto pv = [&](int q, uint32_t buf, uint32_t parity, const Ring& x, bool first) {
+          ok = ok && bar_wait(&bars.p_half[buf], parity, err);
+          tl_fence_after();
+          if (!ok) return;
 #pragma unroll
           for (int k = 0; k < kTileKeys / 16; ++k) {
-            const uint64_t bd = tl_desc(sa(ring + ((slot + k * 16 / VK) % SLOTS) * kSlotBytes) + (k * 16 % VK) * 128, VK * 128);
+            if (k == kTileKeys / 32) {
+              ok = bar_wait(&bars.p_full[buf], parity, err);
+              tl_fence_after();
+              if (!ok) return;
+            }
+            const uint64_t bd = dv + uint64_t(x.at(k * 16 / VK).s) * kStageD + uint64_t((k * 16 % VK) * 8);
             tl_mma_ts(tmem + C::kOCol + q * 128, tmem + buf * 128 + k * 8, bd, id_pv, !(first && k == 0));
           }
-          tl_commit(&bars.pv_done[q]);
+        };
+        auto wait_o = [&](int q) {
+          ok = ok && bar_wait(&bars.o_free[q], ph_o[q], err);
+          ph_o[q] ^= 1;
         };
         bool have = walk.next(a, g);
         if (have) load_q();
         while (ok && have) {
           if (g.b > g.a) {
-            ok = bar_wait(&bars.q_full, uint32_t(n_q++) & 1u, err);
+            ok = bar_wait(&bars.q_full, ph_q, err);
+            ph_q ^= 1;
             tl_fence_after();
+#pragma unroll
+            for (int i = 0; i < KST; ++i) wait_full(r.at(i));
             if constexpr (NQ == 2) {
-              if (ok) wait_slots(p, NS, false);
               if (ok) {
+#pragma unroll
                 for (int q = 0; q < 2; ++q)
-                  if (t.sees(q, g.a)) qk(q, q, p);
-                release(p, NS);
+                  if (t.sees(q, g.a)) qk(q, q, r);
+                release(r, 1);
               }
+              r.step(1);
               for (int j = g.a; ok && j < g.b; ++j) {
-                const int vs = p + NS, ks = vs + NV;
-                bool v_in = false, k_in = false;
-                for (int q = 0; q < 2 && ok; ++q) {
+                const Ring v = r, k = r.at(1);
+                const bool more = j + 1 < g.b;
+                wait_v(v, t.masked(g.t0 + j));
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
                   if (t.sees(q, j)) {
-                    if (!v_in) wait_slots(vs, NV, t.masked(g.t0 + j));
-                    v_in = true;
                     const bool first = j == t.ja[q];
-                    if (ok && first && n_o[q] > 0) ok = bar_wait(&bars.o_free[q], uint32_t(n_o[q] - 1) & 1u, err);
-                    n_o[q] += first;
-                    if (ok) ok = bar_wait(&bars.p_full[q], uint32_t(n_s[q]++) & 1u, err);
-                    tl_fence_after();
-                    if (ok) pv(q, q, vs, first);
+                    if (first) wait_o(q);
+                    if (ok) pv(q, q, ph_p[q], v, first);
+                    ph_p[q] ^= 1;
+                    if (ok && j + 1 == t.jb[q]) tl_commit(&bars.pv_done[q]);
                   }
-                  if (ok && j + 1 < g.b && t.sees(q, j + 1)) {
-                    if (!k_in) wait_slots(ks, NS, false);
-                    k_in = true;
-                    if (ok) qk(q, q, ks);
-                  }
+                  if (q == 1 && ok) release(v, 1);
+                  if (q == 0 && more) wait_full(k);
+                  if (more && ok && t.sees(q, j + 1)) qk(q, q, k);
                 }
-                // a slot is given back only after its copy has landed
-                if (ok && !v_in) wait_slots(vs, NV, t.masked(g.t0 + j));
-                if (ok && !k_in && j + 1 < g.b) wait_slots(ks, NS, false);
-                if (!ok) break;
-                release(vs, NV);
-                if (j + 1 < g.b) release(ks, NS);
-                p = ks;
+                if (more && ok) release(k, 1);
+                r.step(more ? 2 : 1);
               }
             } else {
-              if (ok) wait_slots(p, NS, false);
               if (ok) {
-                qk(0, tile_no & 1, p);
-                release(p, NS);
+                qk(0, buf1, r);
+                release(r, KST);
               }
-              p += NS;
-              for (int j = g.a; ok && j < g.b; ++j, ++tile_no) {
+              r.step(KST);
+              for (int j = g.a; ok && j < g.b; ++j) {
                 if (j + 1 < g.b) {
-                  wait_slots(p, NS, false);
+#pragma unroll
+                  for (int i = 0; i < KST; ++i) wait_full(r.at(i));
                   if (!ok) break;
-                  qk(0, (tile_no + 1) & 1, p);
-                  release(p, NS);
-                  p += NS;
+                  qk(0, buf1 ^ 1, r);
+                  release(r, KST);
+                  r.step(KST);
                 }
-                wait_slots(p, NV, t.masked(g.t0 + j));
+                wait_v(r, t.masked(g.t0 + j));
                 const bool first = j == g.a;
-                if (ok && first && n_o[0] > 0) ok = bar_wait(&bars.o_free[0], uint32_t(n_o[0] - 1) & 1u, err);
-                n_o[0] += first;
-                if (ok) ok = bar_wait(&bars.p_full[tile_no & 1], uint32_t(tile_no >> 1) & 1u, err);
-                tl_fence_after();
+                if (first) wait_o(0);
+                if (ok) pv(0, buf1, buf1 ? ph_p[1] : ph_p[0], r, first);
                 if (!ok) break;
-                pv(0, tile_no & 1, p, first);
-                release(p, NV);
-                p += NV;
+                if (buf1) ph_p[1] ^= 1; else ph_p[0] ^= 1;
+                tl_commit(&bars.pv_done[0]);
+                release(r, VST);
+                r.step(VST);
+                buf1 ^= 1;
               }
             }
           }
@@ -328,32 +383,33 @@ __global__ void __launch_bounds__(TilesCfg<NS>::kThreads, 1)
         }
         tl_commit(&bars.done);
         bar_wait(&bars.done, 0, err, ok ? kSpinCycles : kSpinCyclesAfterError);
-        if (!ok && n_q >= 0) bar_wait(&bars.q_full, uint32_t(n_q) & 1u, err, kSpinCyclesAfterError);
+        if (!ok) bar_wait(&bars.q_full, ph_q, err, kSpinCyclesAfterError);
       }
       __syncwarp();
     } else if (warp == C::kSoftWarps + 1) {
-      // ---- copies: lane l issues box l of a slot (at most 8)
+      // ---- copies: lane l issues box l of a stage (at most 16)
       const int page = 1 << a.page_shift;
       const int bk = min(page, kTileKeys), bv = min(page, VK);
-      int p = 0;
-      // the copy of one slot: K columns of slab `part`, or V keys of group `part`; pid: lane i has the tile's page i
-      auto slot_copy = [&](bool is_v, int part, int key0, int pid) {
-        const int s = p % SLOTS;
+      Ring r;
+      uint32_t used = 0;  // stages filled so far, up to STAGES
+      // the copy of one stage: K columns from slab 2 `part`, or V keys from VK `part`; pid: lane i has the tile's page i
+      auto copy = [&](bool is_v, int part, int key0, int pid) {
         const int rows = is_v ? bv : bk, per = (is_v ? VK : kTileKeys) / rows;  // boxes of 64 columns
-        const int b = lane % per, slab = is_v ? lane / per : part;
+        const int b = lane % per, slab = lane / per;
         const int row0 = (is_v ? part * VK : 0) + b * rows;  // in the tile
-        const bool mine = lane < (is_v ? NS * per : per) && key0 + row0 < t.lim_all && key0 + row0 + rows > t.lo_all;
+        const int col = is_v ? slab : 2 * part + slab;       // slab of the row
+        const bool mine = slab < (is_v ? NS : 2) && col < NS && key0 + row0 < t.lim_all && key0 + row0 + rows > t.lo_all;
         const int id = __shfl_sync(0xffffffffu, pid, page >= kTileKeys ? 0 : row0 >> a.page_shift);
-        if (p >= SLOTS) ok = __all_sync(0xffffffffu, bar_wait(&bars.empty[s], uint32_t(p / SLOTS - 1) & 1u, err));
+        if (used == STAGES) ok = __all_sync(0xffffffffu, bar_wait(&bars.empty[r.s], r.ph ^ 1u, err)); else ++used;
         if (!ok) return;
         const uint32_t bytes = uint32_t(rows) * 128;
         const int n = __popc(__ballot_sync(0xffffffffu, mine));
-        if (lane == 0) bar_expect_tx(&bars.full[s], uint32_t(n) * bytes);
+        if (lane == 0) bar_expect_tx(&bars.full[r.s], uint32_t(n) * bytes);
         __syncwarp();
         if (mine)
-          tma_load_page(sa(ring + s * kSlotBytes) + (is_v ? slab * VK * 128 : 0) + b * bytes, is_v ? &mv : &mk,
-                        sa(&bars.full[s]), slab * 64, (key0 + row0) & (page - 1), g.h, id);
-        ++p;
+          tma_load_page(sa(ring + r.s * C::kStage) + slab * (is_v ? VK * 128 : kSlabBytes) + b * bytes, is_v ? &mv : &mk,
+                        sa(&bars.full[r.s]), col * 64, (key0 + row0) & (page - 1), g.h, id);
+        r.step(1);
       };
       while (ok && walk.next(a, g)) {
         t.set(a, g, tpt);
@@ -363,70 +419,65 @@ __global__ void __launch_bounds__(TilesCfg<NS>::kThreads, 1)
           return j < g.b && lane * page < kTileKeys && k < t.lim_all && k + page > t.lo_all ? __ldcg(row + (k >> a.page_shift)) : 0;
         };
         int pid = page_of(g.a);
-        if constexpr (NQ == 2) {
-          for (int j = g.a; ok && j < g.b; ++j) {
-            const int next = page_of(j + 1);
-            const int key0 = (g.t0 + j) * kTileKeys;
-            for (int i = 0; ok && i < NS; ++i) slot_copy(false, i, key0, pid);
-            for (int i = 0; ok && i < NV; ++i) slot_copy(true, i, key0, pid);
-            pid = next;
-          }
-        } else {
-          const int k0 = (g.t0 + g.a) * kTileKeys;
-          if (g.b > g.a)
-            for (int i = 0; ok && i < NS; ++i) slot_copy(false, i, k0, pid);
-          for (int j = g.a; ok && j < g.b; ++j) {
-            const int next = page_of(j + 1);
-            const int key0 = (g.t0 + j) * kTileKeys;
-            if (j + 1 < g.b)
-              for (int i = 0; ok && i < NS; ++i) slot_copy(false, i, key0 + kTileKeys, next);
-            for (int i = 0; ok && i < NV; ++i) slot_copy(true, i, key0, pid);
-            pid = next;
-          }
+        if (NQ == 1 && g.b > g.a)
+          for (int i = 0; ok && i < KST; ++i) copy(false, i, (g.t0 + g.a) * kTileKeys, pid);
+        for (int j = g.a; ok && j < g.b; ++j) {
+          const int next = page_of(j + 1);
+          const int key0 = (g.t0 + j) * kTileKeys;
+          if (NQ == 2)
+            copy(false, 0, key0, pid);
+          else if (j + 1 < g.b)
+            for (int i = 0; ok && i < KST; ++i) copy(false, i, key0 + kTileKeys, next);
+          for (int i = 0; ok && i < VST; ++i) copy(true, i, key0, pid);
+          pid = next;
         }
       }
-      // the copies in flight land before the CTA leaves
-      for (int j = max(p - SLOTS, 0); j < p; ++j)
-        bar_wait(&bars.full[j % SLOTS], uint32_t(j / SLOTS) & 1u, err, ok ? kSpinCycles : kSpinCyclesAfterError);
+      // the copies in flight land before the CTA leaves: the last use of every stage that was filled
+      for (uint32_t i = 0; i < used; ++i) {
+        // going back from r: stage r.s - 1 - i, in the phase before r's once the ring has wrapped
+        const int s = r.s - 1 - int(i);
+        bar_wait(&bars.full[s < 0 ? s + STAGES : s], s < 0 ? r.ph ^ 1u : r.ph, err, ok ? kSpinCycles : kSpinCyclesAfterError);
+      }
     } else {
       // ---- masked tiles' V: what lies outside the unit's keys, or is not finite, becomes zero
       const int ct = tid - 32 * (C::kSoftWarps + 2);  // 0 .. 63
-      int p = 0, seg = 0, n_masked = 0;
+      int p = 0, seg = 0;  // stages before this segment
+      uint32_t ph = 0;
       while (ok && walk.next(a, g)) {
         t.set(a, g, tpt);
         for (int j = g.a; ok && j < g.b; ++j) {
-          // the V slots of tile j, in the order of the copies
-          int vs;
-          if constexpr (NQ == 2) {
-            vs = p + (j - g.a) * (NS + NV) + NS;
-          } else {
-            vs = p + NS + (j - g.a) * (NS + NV) + (j + 1 < g.b ? NS : 0);
-          }
           if (!t.masked(g.t0 + j)) continue;
+          // the V stages of tile j, in the order of the copies
+          const int vs = p + KST + (j - g.a) * (KST + VST) + (NQ == 1 && j + 1 < g.b ? KST : 0);
           const int key0 = (g.t0 + j) * kTileKeys;
           bool found = false;
-          ok = __all_sync(0xffffffffu, bar_wait(&bars.dirty, uint32_t(n_masked++) & 1u, err));
+          ok = __all_sync(0xffffffffu, bar_wait(&bars.dirty, ph, err));
+          ph ^= 1;
           if (!ok) break;
-          for (int v = 0; v < NV; ++v) {
-            const int s = (vs + v) % SLOTS;
-            uint8_t* sl = ring + s * kSlotBytes;
-            for (int e = ct; e < NS * VK * 8; e += 64) {  // 16-byte pieces; a row is 128 bytes of a slab
-              const int key = key0 + v * VK + (e >> 3) % VK;
-              uint4* x = reinterpret_cast<uint4*>(sl) + e;
-              if (key < t.lo_all || key >= t.lim_all) {
-                *x = make_uint4(0, 0, 0, 0);
-              } else {
-                uint4 y = *x;
-                uint32_t* w = reinterpret_cast<uint32_t*>(&y);
-                bool bad = false;
+          for (int v = 0; v < VST; ++v) {
+            uint8_t* sl = ring + (vs + v) % STAGES * C::kStage;
+            // 16-byte pieces, eight in flight a thread; a row (key) is 128 bytes of a slab
+            for (int e0 = ct; e0 < NS * VK * 8; e0 += 64 * 8) {
+              uint4 y[8];
 #pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                  if ((w[z] & 0x7f80u) == 0x7f80u) w[z] &= 0xffff0000u, bad = true;
-                  if ((w[z] & 0x7f800000u) == 0x7f800000u) w[z] &= 0xffffu, bad = true;
-                }
-                if (bad) {
-                  *x = y;
-                  found = true;
+              for (int x = 0; x < 8; ++x) y[x] = reinterpret_cast<const uint4*>(sl)[e0 + 64 * x];
+#pragma unroll
+              for (int x = 0; x < 8; ++x) {
+                const int key = key0 + v * VK + ((e0 + 64 * x) >> 3) % VK;
+                uint32_t w[4] = {y[x].x, y[x].y, y[x].z, y[x].w};
+                // an exponent of all ones carries into the sign bit
+                uint32_t bad = 0;
+#pragma unroll
+                for (int z = 0; z < 4; ++z) bad |= (w[z] & 0x7f807f80u) + 0x00800080u;
+                const bool out = key < t.lo_all || key >= t.lim_all;
+                if (out || (bad & 0x80008000u)) {
+#pragma unroll
+                  for (int z = 0; z < 4; ++z)
+                    w[z] &= out ? 0u
+                                : ((w[z] & 0x7f80u) == 0x7f80u ? 0u : 0xffffu) |
+                                      ((w[z] & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u);
+                  reinterpret_cast<uint4*>(sl)[e0 + 64 * x] = make_uint4(w[0], w[1], w[2], w[3]);
+                  found |= !out;
                 }
               }
             }
@@ -436,19 +487,20 @@ __global__ void __launch_bounds__(TilesCfg<NS>::kThreads, 1)
           __syncwarp();
           if (lane == 0) bar_arrive(&bars.clean);
         }
-        p += (g.b - g.a) * (NS + NV);
+        p += (g.b - g.a) * (KST + VST);
         ++seg;
       }
     }
   } else {
     // ---- softmax: a warpgroup a row tile, a thread a row
-    if constexpr (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    if constexpr (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     const int q = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
     const float c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f);  // powers of two; a scale of 0 still masks
     const bool neg = a.scale < 0.f;
     const uint32_t o_at = tmem + lanes + C::kOCol + q * 128;
     int ks = 0, seg = 0;
+    uint32_t ph_pv = 0;  // two row tiles: the segments that ended
     while (walk.next(a, g)) {  // after a wait that gave up too: the warps of a row tile meet at barriers
       t.set(a, g, tpt);
       const int this_seg = seg++;
@@ -483,19 +535,22 @@ __global__ void __launch_bounds__(TilesCfg<NS>::kThreads, 1)
         }
         float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int i = 4; i < 128; i += 4)
+        for (int i = 4; i < 124; i += 8)
 #pragma unroll
-          for (int z = 0; z < 4; ++z) mx[z] = fmaxf(mx[z], s[i + z]);
-        const float m_new = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), m);
+          for (int z = 0; z < 4; ++z) mx[z] = max3(mx[z], s[i + 2 * z], s[i + 2 * z + 1]);
+        const float m_new = max3(max3(mx[0], mx[1], m), max3(mx[2], mx[3], s[124]), max3(s[125], s[126], s[127]));
         // (m_new - m is NaN where both are infinite: nothing to scale)
         if (__any_sync(0xffffffffu, (m_new - m) * c > 8.f)) {
           const float f = m == -INFINITY ? 0.f : ex2((m - m_new) * c);
           m = m_new;
           l *= f;
           if (j > ja) {
-            ok = __all_sync(0xffffffffu, bar_wait(&bars.pv_done[q], uint32_t(ks - 1) & 1u, err));
-            if (!ok) continue;
-            tl_fence_after();
+            // O has to be complete up to the tile before.  With two row tiles this S was made after that product.
+            if constexpr (NQ == 1) {
+              ok = __all_sync(0xffffffffu, bar_wait(&bars.pv_done[0], uint32_t(ks - 1) & 1u, err));
+              if (!ok) continue;
+              tl_fence_after();
+            }
 #pragma unroll 1
             for (int i = 0; i < NS * 2; ++i) {
               uint32_t r[32];
@@ -516,97 +571,142 @@ __global__ void __launch_bounds__(TilesCfg<NS>::kThreads, 1)
           for (int i = 0; i < 128; ++i) s[i] -= d;
           mc = 0.f;
         }
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t pr[64];
+        const unsigned long long c2 = f2_pack(c, c), mc2 = f2_pack(-mc, -mc);
+        unsigned long long sum[2] = {0, 0};
+        // weights of the keys from i0 on; they enter the second product as bf16 (2^-8 of each at most, like the
+        // cache's own rounding)
+        auto weights = [&](int i0, int n, uint32_t* pr) {
 #pragma unroll
-        for (int i = 0; i < 128; i += 2) {
-          const float x = ex2(fmaf(s[i], c, -mc)), y = ex2(fmaf(s[i + 1], c, -mc));
-          sum[i & 2] += x;
-          sum[(i & 2) + 1] += y;
-          // the weights enter the second product as bf16 (2^-8 of each at most, like the cache's own rounding)
-          pr[i / 2] = attn_pack(x, y);
-        }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          for (int i = 0; i < n; i += 2) {
+            float2 w = f2_unpack(f2_fma(f2_pack(s[i0 + i], s[i0 + i + 1]), c2, mc2));
+            w.x = ex2(w.x);
+            w.y = ex2(w.y);
+            sum[(i >> 1) & 1] = f2_add(sum[(i >> 1) & 1], f2_pack(w.x, w.y));
+            pr[i / 2] = attn_pack(w.x, w.y);
+          }
+        };
+        auto give = [&](uint64_t* bar) {
+          tl_wait_st();
+          tl_fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(bar);
+        };
+        uint32_t pr[32];
+        weights(0, 64, pr);
         tl_st32(s_at, pr);
-        tl_st32(s_at + 32, pr + 32);
-        tl_wait_st();
-        tl_fence_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive(&bars.p_full[buf]);
+        uint32_t pr2[32];
+        weights(64, 32, pr2);
+        give(&bars.p_half[buf]);
+        weights(96, 32, pr2 + 16);
+        tl_st32(s_at + 32, pr2);
+        give(&bars.p_full[buf]);
+        const float2 s0 = f2_unpack(f2_add(sum[0], sum[1]));
+        l += s0.x + s0.y;
       }
 
       // ---- the segment's end: the rows are finished, or left as a part
       const bool some = jb > ja;
       if (some && ok) {
-        // with two S buffers only the product before the last but one is known to be done here: a parity wait must
-        // not skip a phase
-        if (NQ == 1 && ks > 1) bar_wait(&bars.pv_done[q], uint32_t(ks - 2) & 1u, err);
-        ok = __all_sync(0xffffffffu, bar_wait(&bars.pv_done[q], uint32_t(ks - 1) & 1u, err));
+        if constexpr (NQ == 2) {
+          ok = __all_sync(0xffffffffu, bar_wait(&bars.pv_done[q], ph_pv, err));
+          ph_pv ^= 1;
+        } else {
+          // only the product before the last but one is known to be done here: a parity wait must not skip a phase
+          if (ks > 1) bar_wait(&bars.pv_done[0], uint32_t(ks - 2) & 1u, err);
+          ok = __all_sync(0xffffffffu, bar_wait(&bars.pv_done[0], uint32_t(ks - 1) & 1u, err));
+        }
         tl_fence_after();
       }
       const bool whole = g.a == 0 && g.b == g.n;
       const bool any = some && *reinterpret_cast<volatile int*>(&bars.found[this_seg & 7]) == this_seg + 1;
-      const int b0 = walk.owner(g.first), b1 = walk.owner(g.last - 1);
+      int b0, b1;
+      walk.parts(g, b0, b1);
+      const float ml = m == -INFINITY ? m : m * c;  // the parts' maxima are in powers of two
+      const unsigned n_parts = unsigned(b1 - b0 + 1);
+      auto wg_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory"); };
+      // The part that begins a unit is the last thing its CTA does and the others' first, so they are there as a
+      // rule: then they are folded in here, and nothing of this one is written.
+      bool fold = false;
+      if (!whole && b0 == int(blockIdx.x)) {
+        if ((warp & 3) == 0 && lane == 0) {
+          unsigned n;
+          asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(n) : "l"(attn_counter(a, b0, q)) : "memory");
+          bars.last[q] = n == n_parts - 1;
+          if (n == n_parts - 1) *attn_counter(a, b0, q) = 0;
+        }
+        wg_sync();
+        fold = *reinterpret_cast<volatile int*>(&bars.last[q]) != 0;
+        wg_sync();
+      }
+      if (any && ok) {
+#pragma unroll 1
+        for (int i = 0; i < a.dim; ++i) {
+          uint32_t x;
+          __syncwarp();
+          asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(x) : "r"(o_at + i));
+          tl_wait_ld();
+          if (row < n_rows)
+            x = __float_as_uint(attn_nonfinite<BF16>(a, g, kTileKeys, lo, lim, t.lo_max, t.lim_min, i, __uint_as_float(x)));
+          __syncwarp();
+          asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(o_at + i), "r"(x) : "memory");
+          tl_wait_st();
+        }
+      }
       float* part = attn_part(a, 2 * int(blockIdx.x) + (int(blockIdx.x) == b0), NQ, q, 128);
-      const float inv = l == 0.f ? 0.f : 1.f / l;
       const int64_t out = row < n_rows ? attn_out_row(a, g, tok0, row) * a.dim : 0;
 #pragma unroll 1
-      for (int i = 0; i < NS * 2; ++i) {
-        uint32_t r[32];
+      for (int i = 0; i < NS; ++i) {
+        uint32_t r[64];
         __syncwarp();
         if (some && ok) {
-          tl_ld32(o_at + 32 * i, r);
+          tl_ld32(o_at + 64 * i, r);
+          tl_ld32(o_at + 64 * i + 32, r + 32);
           tl_wait_ld();
         } else {
 #pragma unroll
-          for (int z = 0; z < 32; ++z) r[z] = 0;
+          for (int z = 0; z < 64; ++z) r[z] = 0;
         }
         if (row < n_rows) {
+          float v[64];
 #pragma unroll
-          for (int z = 0; z < 32; z += 8) {
-            const int col = 32 * i + z;
-            if (col >= a.dim) break;
-            float v[8];
+          for (int z = 0; z < 64; ++z) v[z] = __uint_as_float(r[z]);
+          if (whole || fold) {
+            float fm = ml, fl = l;
+            if (fold) attn_fold<false, 64>(a, b0 + 1, b1, b0, NQ, q, 128, row, 64 * i, fm, fl, v);
+            attn_finish<BF16, 64>(a, out + 64 * i, 64 * i, fl, v);
+          } else {
 #pragma unroll
-            for (int x = 0; x < 8; ++x) v[x] = __uint_as_float(r[z + x]);
-            if (any)
-#pragma unroll 1
-              for (int x = 0; x < 8; ++x)
-                v[x] = attn_nonfinite<BF16>(a, g, kTileKeys, lo, lim, t.lo_max, t.lim_min, col + x, v[x]);
-            if (whole) {
-#pragma unroll
-              for (int x = 0; x < 8; ++x) v[x] *= inv;
-              attn_store8<BF16>(a, out + col, v);
-            } else {
-              *attn_piece<false>(part, 128, a.dim, row, col) = make_float4(v[0], v[1], v[2], v[3]);
-              *attn_piece<false>(part, 128, a.dim, row, col + 4) = make_float4(v[4], v[5], v[6], v[7]);
-            }
+            for (int z = 0; z < 64; z += 4)
+              if (64 * i + z < a.dim)
+                *attn_piece<false>(part, 128, a.dim, row, 64 * i + z) = make_float4(v[z], v[z + 1], v[z + 2], v[z + 3]);
           }
         }
       }
+      __syncwarp();
       if (some) {
         tl_fence_before();
         __syncwarp();
         if (lane == 0) bar_arrive(&bars.o_free[q]);
       }
-      if (!whole) {
+      if (!whole && !fold) {
         if (row < n_rows) {
-          part[row] = m == -INFINITY ? m : m * c;
+          part[row] = ml;
           part[128 + row] = l;
         }
         __threadfence();
-        asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory");
+        wg_sync();
         if ((warp & 3) == 0 && lane == 0) {
-          const unsigned n = unsigned(b1 - b0 + 1);
-          const bool last = atomicAdd(attn_counter(a, b0, q), 1u) == n - 1;
+          const bool last = atomicAdd(attn_counter(a, b0, q), 1u) == n_parts - 1;
           if (last) *attn_counter(a, b0, q) = 0;
           bars.last[q] = last;
         }
-        asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory");
-        if (*reinterpret_cast<volatile int*>(&bars.last[q])) {
+        wg_sync();
+        const bool last = *reinterpret_cast<volatile int*>(&bars.last[q]) != 0;
+        if (last) {
           __threadfence();
-          attn_join<BF16, false>(a, g, b0, b1, NQ, q, 128, n_rows, tok0, row, 128);
+          attn_join<BF16, false, 64>(a, g, b0, b1, NQ, q, 128, n_rows, tok0, row, 128);
         }
+        wg_sync();  // before the flag is written again
       }
     }
   }
@@ -619,7 +719,7 @@ __global__ void __launch_bounds__(TilesCfg<NS>::kThreads, 1)
 template <int NS>
 static cudaError_t launch_tiles(const AttnArgs& a, cudaStream_t s) {
   using C = TilesCfg<NS>;
-  static_assert(C::kSmem <= 232448 && C::kSlots <= 12, "shared memory of an SM");
+  static_assert(C::kSmem <= 232448 && C::kStages <= 12, "shared memory of an SM");
   const int page = 1 << a.page_shift;
   CUtensorMap mq, mk, mv;
   cudaError_t e = attn_query_map(&mq, a, a.group, 128 / a.group);
