@@ -19,6 +19,10 @@ namespace gsi {
 // the lengths are, one long request is spread over all CTAs, and neighbours
 // read the same keys.  A unit that sees no key counts as one tile (its rows
 // of zeros have to be written).  Each CTA finds its share from the lengths.
+// Where the shares are long enough for it, a unit counts for `extra` tiles
+// more than it has (before its first one: what it costs to begin and to
+// finish it), and a cut that falls within `extra` of a unit's end is moved
+// there, since a part of a unit costs about that much to write and join.
 struct AttnReq {
   int q0, q_len, len;
 };
@@ -47,47 +51,63 @@ __device__ __forceinline__ void attn_tiles(const AttnArgs& a, const AttnReq& q, 
   n = max(0, (lim + kt - 1) / kt - t0);
 }
 
-__device__ __forceinline__ long long attn_head_cost(const AttnArgs& a, const AttnReq& q, int ut, int kt) {
+// Cost of a request's units under one head: its tiles, and `extra` more a unit.
+__device__ __forceinline__ long long attn_head_cost(const AttnArgs& a, const AttnReq& q, int ut, int kt, int extra) {
   long long s = 0;
   for (int u = 0; u * ut < q.q_len; ++u) {
     int t0, n;
     attn_tiles(a, q, u, ut, kt, t0, n);
-    s += max(1, n);
+    s += max(1, n) + extra;
   }
   return s;
 }
 
-// A cut within `snap` tiles of a unit's end is moved there: the share grows or
-// shrinks by less than the part of a unit would cost to write and join.
 struct AttnShare {
   long long total, pos, end;  // tiles of the line: all, and this CTA's
   long long off;              // pos inside request r
-  int r, grid, snap;          // grid: the CTAs that have a share (all, or as many as there are tiles)
+  int r, grid, extra;         // grid: the CTAs that have a share (all, or as many as there are tiles)
 };
 
 // The cut at place `at` of request r, moved to the end of its unit where that is near.
-__device__ __forceinline__ long long attn_snap(const AttnArgs& a, const AttnReq& q, long long at, int ut, int kt, int snap) {
-  if (snap == 0) return at;
-  const long long per = attn_head_cost(a, q, ut, kt);
+__device__ __forceinline__ long long attn_snap(const AttnArgs& a, const AttnReq& q, long long at, int ut, int kt, int extra) {
+  if (extra == 0) return at;
+  const long long per = attn_head_cost(a, q, ut, kt, extra);
   long long rem = at % per;
   for (int u = 0;; ++u) {
     int t0, n;
     attn_tiles(a, q, u, ut, kt, t0, n);
-    const int c = max(1, n);
-    if (rem < c) return rem <= snap ? at - rem : c - rem <= snap ? at + c - rem : at;
+    const int c = max(1, n) + extra;
+    if (rem < c) return rem <= extra ? at - rem : c - rem <= extra ? at + c - rem : at;
     rem -= c;
   }
 }
 
 // The share of CTA blockIdx.x; all NT threads of the block.
 template <int NT>
-__device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, int ut, int kt, int snap) {
+__device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, int ut, int kt, int extra) {
   __shared__ long long s_sum[NT / 32], s_off, s_cut[2];
-  __shared__ int s_r;
+  __shared__ int s_r, s_tiles[NT / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r0 = int((long long)a.n_req * tid / NT), r1 = int((long long)a.n_req * (tid + 1) / NT);
+  AttnShare s;
+  s.extra = 0;
+  if (extra > 0) {  // shares of fewer than 4 extra tiles are cut where they fall
+    int tiles = 0;
+    const int enough = 4 * extra * int(gridDim.x);
+    for (int r = r0; r < r1 && tiles < enough; ++r) {
+      const long long c = attn_head_cost(a, attn_request(a, r), ut, kt, 0) * a.hkv;
+      tiles += int(c < enough ? c : enough);
+    }
+    tiles = __reduce_add_sync(0xffffffffu, min(tiles, enough));
+    if (lane == 0) s_tiles[warp] = min(tiles, enough);
+    __syncthreads();
+    tiles = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) tiles += s_tiles[w];
+    if (tiles >= enough) s.extra = extra;
+  }
   long long mine = 0;
-  for (int r = r0; r < r1; ++r) mine += attn_head_cost(a, attn_request(a, r), ut, kt) * a.hkv;
+  for (int r = r0; r < r1; ++r) mine += attn_head_cost(a, attn_request(a, r), ut, kt, s.extra) * a.hkv;
   long long inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -102,10 +122,8 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, int ut, int k
     if (w < warp) before += s_sum[w];
     total += s_sum[w];
   }
-  AttnShare s;
   s.total = total;
   s.grid = int(total < (long long)gridDim.x ? total : (long long)gridDim.x);
-  s.snap = total >= (long long)s.grid * 4 * snap ? snap : 0;  // small shares are cut where they fall
   s.pos = s.end = 0;
   if (int(blockIdx.x) < s.grid) {
     const long long cut[2] = {total * blockIdx.x / s.grid, total * (blockIdx.x + 1) / s.grid};
@@ -115,9 +133,9 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, int ut, int k
         long long at = cut[i] - before;
         for (int r = r0; r < r1; ++r) {
           const AttnReq q = attn_request(a, r);
-          const long long c = attn_head_cost(a, q, ut, kt) * a.hkv;
+          const long long c = attn_head_cost(a, q, ut, kt, s.extra) * a.hkv;
           if (at < c) {
-            const long long to = attn_snap(a, q, at, ut, kt, s.snap);
+            const long long to = attn_snap(a, q, at, ut, kt, s.extra);
             s_cut[i] = cut[i] + to - at;
             if (i == 0) {
               s_r = r;
@@ -159,7 +177,7 @@ struct AttnWalk {
   __device__ __forceinline__ void enter(const AttnArgs& a, long long at) {
     for (;; ++r) {  // the first request that goes on beyond `at`: there is one, the share does
       q = attn_request(a, r);
-      per_head = attn_head_cost(a, q, ut, kt);
+      per_head = attn_head_cost(a, q, ut, kt, s.extra);
       if (at < per_head * a.hkv) break;
       at -= per_head * a.hkv;
     }
@@ -168,8 +186,8 @@ struct AttnWalk {
     for (u = 0;; ++u) {
       int t0, n;
       attn_tiles(a, q, u, ut, kt, t0, n);
-      if (off < max(1, n)) break;
-      off -= max(1, n);
+      if (off < max(1, n) + s.extra) break;
+      off -= max(1, n) + s.extra;
     }
   }
   __device__ __forceinline__ void begin(const AttnArgs& a, const AttnShare& share, int ut_, int kt_) {
@@ -182,7 +200,7 @@ struct AttnWalk {
   __device__ __forceinline__ bool next(const AttnArgs& a, AttnSeg& g) {
     if (s.pos >= s.end) return false;
     attn_tiles(a, q, u, ut, kt, g.t0, g.n);
-    const long long cost = max(1, g.n);
+    const long long cost = max(1, g.n) + s.extra;
     const long long take = cost - off < s.end - s.pos ? cost - off : s.end - s.pos;
     g.q = q;
     g.r = r;
@@ -190,8 +208,8 @@ struct AttnWalk {
     g.u = u;
     g.first = s.pos - off;
     g.last = g.first + cost;
-    g.a = int(off);
-    g.b = g.n == 0 ? 0 : int(off + take);
+    g.a = max(0, int(off) - s.extra);
+    g.b = min(g.n, max(0, int(off + take) - s.extra));
     s.pos += take;
     off += take;
     if (off == cost && s.pos < s.end) {
@@ -211,8 +229,8 @@ struct AttnWalk {
   // The CTAs that hold parts of a unit: the cuts inside it, beyond what is moved to its ends, are those of the CTAs
   // b0 + 1 .. b1 (none: b0 >= b1).
   __device__ __forceinline__ void parts(const AttnSeg& g, int& b0, int& b1) const {
-    b0 = int(((g.first + s.snap + 1) * s.grid + s.total - 1) / s.total) - 1;
-    b1 = int(((g.last - s.snap) * s.grid - 1) / s.total);
+    b0 = int(((g.first + s.extra + 1) * s.grid + s.total - 1) / s.total) - 1;
+    b1 = int(((g.last - s.extra) * s.grid - 1) / s.total);
   }
 };
 

@@ -28,8 +28,8 @@ namespace gsi {
 // and the non-finite ones that a row does see are added at its end.
 constexpr int kTileKeys = 128;
 constexpr int kSlabBytes = 16384;  // 64 columns of 128 rows
-// A cut nearer than this to a unit's end is moved there (tiles; a part of a unit costs about as much to write and join).
-constexpr int kTileSnap = 2;
+// What a unit costs beside its tiles, in tiles (its queries' load and its rows' output), and a part of one to write and fold.
+constexpr int kTileUnit = 2;
 
 template <int NS>
 struct TilesCfg {
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(TilesCfg<NS>::kThreads, 1)
   tl_fence_before();
   pdl_wait();
   const int tpt = 128 / a.group, ut = NQ * tpt;
-  const AttnShare share = attn_share<C::kThreads>(a, ut, kTileKeys, kTileSnap);  // its block barriers publish the ones above
+  const AttnShare share = attn_share<C::kThreads>(a, ut, kTileKeys, kTileUnit);  // its block barriers publish the ones above
   tl_fence_after();
   const uint32_t tmem = bars.tmem;
   AttnWalk walk;
@@ -457,27 +457,35 @@ __global__ void __launch_bounds__(TilesCfg<NS>::kThreads, 1)
           for (int v = 0; v < VST; ++v) {
             uint8_t* sl = ring + (vs + v) % STAGES * C::kStage;
             // 16-byte pieces, eight in flight a thread; a row (key) is 128 bytes of a slab
+            const bool inside = key0 >= t.lo_all && key0 + kTileKeys <= t.lim_all;
+#pragma unroll 1
             for (int e0 = ct; e0 < NS * VK * 8; e0 += 64 * 8) {
               uint4 y[8];
 #pragma unroll
               for (int x = 0; x < 8; ++x) y[x] = reinterpret_cast<const uint4*>(sl)[e0 + 64 * x];
+              uint32_t bad = 0;  // an exponent of all ones carries into the sign bit
 #pragma unroll
-              for (int x = 0; x < 8; ++x) {
-                const int key = key0 + v * VK + ((e0 + 64 * x) >> 3) % VK;
-                uint32_t w[4] = {y[x].x, y[x].y, y[x].z, y[x].w};
-                // an exponent of all ones carries into the sign bit
-                uint32_t bad = 0;
-#pragma unroll
-                for (int z = 0; z < 4; ++z) bad |= (w[z] & 0x7f807f80u) + 0x00800080u;
-                const bool out = key < t.lo_all || key >= t.lim_all;
-                if (out || (bad & 0x80008000u)) {
-#pragma unroll
-                  for (int z = 0; z < 4; ++z)
-                    w[z] &= out ? 0u
-                                : ((w[z] & 0x7f80u) == 0x7f80u ? 0u : 0xffffu) |
-                                      ((w[z] & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u);
-                  reinterpret_cast<uint4*>(sl)[e0 + 64 * x] = make_uint4(w[0], w[1], w[2], w[3]);
-                  found |= !out;
+              for (int x = 0; x < 8; ++x)
+                bad |= ((y[x].x & 0x7f807f80u) + 0x00800080u) | ((y[x].y & 0x7f807f80u) + 0x00800080u) |
+                       ((y[x].z & 0x7f807f80u) + 0x00800080u) | ((y[x].w & 0x7f807f80u) + 0x00800080u);
+              const bool some_bad = (bad & 0x80008000u) != 0;
+              if (inside && !some_bad) continue;
+#pragma unroll 1
+              for (int e = e0; e < e0 + 64 * 8; e += 64) {
+                const int key = key0 + v * VK + (e >> 3) % VK;
+                if (key < t.lo_all || key >= t.lim_all) {
+                  reinterpret_cast<uint4*>(sl)[e] = make_uint4(0, 0, 0, 0);
+                } else if (some_bad) {
+                  uint32_t* w = reinterpret_cast<uint32_t*>(sl) + 4 * e;
+#pragma unroll 1
+                  for (int z = 0; z < 4; ++z) {
+                    const uint32_t keep = ((w[z] & 0x7f80u) == 0x7f80u ? 0u : 0xffffu) |
+                                          ((w[z] & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u);
+                    if (keep != 0xffffffffu) {
+                      w[z] &= keep;
+                      found = true;
+                    }
+                  }
                 }
               }
             }
@@ -529,9 +537,16 @@ __global__ void __launch_bounds__(TilesCfg<NS>::kThreads, 1)
           for (int i = 0; i < 128; ++i) s[i] = -s[i];
         }
         if (tile < lo_max || tile + kTileKeys > lim_min) {
+          // a bit a key: those from `from` on that lie before `to`
           const int from = lo - tile, to = lim - tile;
 #pragma unroll
-          for (int i = 0; i < 128; ++i) s[i] = i >= from && i < to ? s[i] : -INFINITY;
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t below_to = to >= 32 * w + 32 ? ~0u : to <= 32 * w ? 0u : (1u << (to - 32 * w)) - 1u;
+            const uint32_t below_from = from >= 32 * w + 32 ? ~0u : from <= 32 * w ? 0u : (1u << (from - 32 * w)) - 1u;
+            const uint32_t see = below_to & ~below_from;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[32 * w + i] = (see >> i) & 1u ? s[32 * w + i] : -INFINITY;
+          }
         }
         float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
