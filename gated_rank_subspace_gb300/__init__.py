@@ -151,7 +151,9 @@ def _stream(stream):
 
 def _raw_stream(stream, t):
     """The stream's handle as a number (the current stream of t's device by default)."""
-    return stream.cuda_stream if stream is not None else torch.cuda.current_stream(t.device).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(t.get_device())  # current_stream(t.device) builds two objects for it
 
 
 def _dtype_code(dt: torch.dtype) -> int:
@@ -498,7 +500,7 @@ class PagedCache:
         if not K.is_cuda or not V.is_cuda or st[3] != 1:
             raise ValueError("K and V must be CUDA tensors with contiguous head_dim")
         n, h, p, d = K.shape
-        return CacheDesc(n, p, h, d, _dtype_code(K.dtype), st[0], st[1], st[2], K.data_ptr(), V.data_ptr())
+        return CacheDesc(n, p, h, d, _dtype_code(K.dtype), *st[:3], K.data_ptr(), V.data_ptr())
 
 
 @dataclass

@@ -147,7 +147,7 @@ int attn_sm_count() {
 size_t attention_work_bytes(gsi_dtype dt, int dim, int group) { return dt == GSI_BF16 ? attn_tiles_work_bytes(dim) : sizeof(Ctrl); }
 
 cudaError_t launch_paged_attention(const AttnArgs& a, gsi_dtype dt, int64_t max_q, cudaStream_t s) {
-  if (dt == GSI_BF16) return max_q * a.group <= 16 ? launch_attn_rows16(a, s) : launch_attn_tiles(a, s);
+  if (dt == GSI_BF16) return max_q * a.group <= 16 ? launch_attn_rows(a, max_q * a.group <= 8, s) : launch_attn_tiles(a, s);
   const int64_t rows = int64_t(a.N) * a.hkv * a.group;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(unsigned((rows + kPlainWarps - 1) / kPlainWarps));

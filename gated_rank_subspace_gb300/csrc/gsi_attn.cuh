@@ -62,31 +62,56 @@ __device__ __forceinline__ long long attn_head_cost(const AttnArgs& a, const Att
   return s;
 }
 
-struct AttnShare {
-  long long total, pos, end;  // tiles of the line: all, and this CTA's
-  long long off;              // pos inside request r
-  int r, grid, extra;         // grid: the CTAs that have a share (all, or as many as there are tiles)
-};
-
-// The cut at place `at` of request r, moved to the end of its unit where that is near.
-__device__ __forceinline__ long long attn_snap(const AttnArgs& a, const AttnReq& q, long long at, int ut, int kt, int extra) {
-  if (extra == 0) return at;
-  const long long per = attn_head_cost(a, q, ut, kt, extra);
-  long long rem = at % per;
-  for (int u = 0;; ++u) {
-    int t0, n;
-    attn_tiles(a, q, u, ut, kt, t0, n);
-    const int c = max(1, n) + extra;
-    if (rem < c) return rem <= extra ? at - rem : c - rem <= extra ? at + c - rem : at;
-    rem -= c;
-  }
+// Whole quotient of a by b > 0 (in 32 bits, a fifth of the time, where they suffice).
+__device__ __forceinline__ long long attn_div(long long a, long long b) {
+  if (((a | b) >> 31) == 0) return int(a) / int(b);
+  return a / b;
 }
 
-// The share of CTA blockIdx.x; all NT threads of the block.
+// A place on the line: `off` tiles into unit u of head h of request r.
+struct AttnPlace {
+  AttnReq q;
+  int r, h, u;
+  long long per_head, off;
+  // `at` tiles behind the first one of request r, whose lengths are q (there are tiles beyond)
+  __device__ __forceinline__ void set(const AttnArgs& a, int r_, const AttnReq& q_, long long at, int ut, int kt, int extra) {
+    r = r_;
+    q = q_;
+    for (;;) {
+      per_head = attn_head_cost(a, q, ut, kt, extra);
+      if (at < per_head * a.hkv) break;
+      at -= per_head * a.hkv;
+      q = attn_request(a, ++r);
+    }
+    h = int(attn_div(at, per_head));
+    off = at - h * per_head;
+    for (u = 0;; ++u) {
+      int t0, n;
+      attn_tiles(a, q, u, ut, kt, t0, n);
+      if (off < max(1, n) + extra) break;
+      off -= max(1, n) + extra;
+    }
+  }
+  // tiles by which a cut here is moved
+  __device__ __forceinline__ int snap(const AttnArgs& a, int ut, int kt, int extra) const {
+    int t0, n;
+    attn_tiles(a, q, u, ut, kt, t0, n);
+    const int c = max(1, n) + extra, rem = int(off);
+    return rem <= extra ? -rem : c - rem <= extra ? c - rem : 0;
+  }
+};
+
+struct AttnShare {
+  long long total, pos, end;  // tiles of the line: all, and this CTA's
+  int grid, extra;            // grid: the CTAs that have a share (all, or as many as there are tiles)
+};
+
+// The share of CTA blockIdx.x and where it begins; all NT threads of the block.
 template <int NT>
-__device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, int ut, int kt, int extra) {
-  __shared__ long long s_sum[NT / 32], s_off, s_cut[2];
-  __shared__ int s_r, s_tiles[NT / 32];
+__device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, int ut, int kt, int extra, AttnPlace& begin) {
+  __shared__ long long s_sum[NT / 32], s_cut[2];
+  __shared__ int s_tiles[NT / 32];
+  __shared__ AttnPlace s_begin;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r0 = int((long long)a.n_req * tid / NT), r1 = int((long long)a.n_req * (tid + 1) / NT);
   AttnShare s;
@@ -107,7 +132,11 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, int ut, int k
     if (tiles >= enough) s.extra = extra;
   }
   long long mine = 0;
-  for (int r = r0; r < r1; ++r) mine += attn_head_cost(a, attn_request(a, r), ut, kt, s.extra) * a.hkv;
+  AttnReq q{};  // of request r1 - 1
+  for (int r = r0; r < r1; ++r) {
+    q = attn_request(a, r);
+    mine += attn_head_cost(a, q, ut, kt, s.extra) * a.hkv;
+  }
   long long inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -125,35 +154,32 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, int ut, int k
   s.total = total;
   s.grid = int(total < (long long)gridDim.x ? total : (long long)gridDim.x);
   s.pos = s.end = 0;
-  if (int(blockIdx.x) < s.grid) {
-    const long long cut[2] = {total * blockIdx.x / s.grid, total * (blockIdx.x + 1) / s.grid};
+  const bool some = int(blockIdx.x) < s.grid;
+  if (some) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (before <= cut[i] && cut[i] < before + mine) {
-        long long at = cut[i] - before;
-        for (int r = r0; r < r1; ++r) {
-          const AttnReq q = attn_request(a, r);
-          const long long c = attn_head_cost(a, q, ut, kt, s.extra) * a.hkv;
-          if (at < c) {
-            const long long to = attn_snap(a, q, at, ut, kt, s.extra);
-            s_cut[i] = cut[i] + to - at;
-            if (i == 0) {
-              s_r = r;
-              s_off = to;
-            }
-            break;
-          }
-          at -= c;
+    for (int i = 0; i < 2; ++i) {
+      const long long cut = attn_div(total * (blockIdx.x + i), s.grid);
+      if (before <= cut && cut < before + mine) {
+        long long at = cut - before;
+        if (r1 - r0 > 1) q = attn_request(a, r0);
+        AttnPlace p;
+        if (i == 0 || s.extra > 0) p.set(a, r0, q, at, ut, kt, s.extra);
+        const int move = s.extra > 0 ? p.snap(a, ut, kt, s.extra) : 0;
+        s_cut[i] = cut + move;
+        if (i == 0) {
+          if (move > 0 && cut + move < total) p.set(a, r0, r1 - r0 > 1 ? attn_request(a, r0) : q, at + move, ut, kt, s.extra);
+          if (move < 0) p.off += move;
+          s_begin = p;
         }
       }
+    }
   }
   __syncthreads();
-  if (int(blockIdx.x) < s.grid) {
+  if (some) {
     s.pos = s_cut[0];
     s.end = int(blockIdx.x) + 1 == s.grid ? total : s_cut[1];
+    begin = s_begin;
   }
-  s.r = s_r;
-  s.off = s_off;
   return s;
 }
 
@@ -169,59 +195,32 @@ struct AttnSeg {
 struct AttnWalk {
   AttnShare s;
   int ut, kt;
-  AttnReq q;
-  long long per_head;
-  int r, h, u;
-  long long off;  // tiles of unit u that lie before pos
+  AttnPlace p;
 
-  __device__ __forceinline__ void enter(const AttnArgs& a, long long at) {
-    for (;; ++r) {  // the first request that goes on beyond `at`: there is one, the share does
-      q = attn_request(a, r);
-      per_head = attn_head_cost(a, q, ut, kt, s.extra);
-      if (at < per_head * a.hkv) break;
-      at -= per_head * a.hkv;
-    }
-    h = int(at / per_head);
-    off = at - h * per_head;
-    for (u = 0;; ++u) {
-      int t0, n;
-      attn_tiles(a, q, u, ut, kt, t0, n);
-      if (off < max(1, n) + s.extra) break;
-      off -= max(1, n) + s.extra;
-    }
-  }
-  __device__ __forceinline__ void begin(const AttnArgs& a, const AttnShare& share, int ut_, int kt_) {
-    s = share;
-    ut = ut_;
-    kt = kt_;
-    r = s.r;
-    if (s.pos < s.end) enter(a, s.off);
-  }
   __device__ __forceinline__ bool next(const AttnArgs& a, AttnSeg& g) {
     if (s.pos >= s.end) return false;
-    attn_tiles(a, q, u, ut, kt, g.t0, g.n);
+    attn_tiles(a, p.q, p.u, ut, kt, g.t0, g.n);
     const long long cost = max(1, g.n) + s.extra;
-    const long long take = cost - off < s.end - s.pos ? cost - off : s.end - s.pos;
-    g.q = q;
-    g.r = r;
-    g.h = h;
-    g.u = u;
-    g.first = s.pos - off;
+    const long long take = cost - p.off < s.end - s.pos ? cost - p.off : s.end - s.pos;
+    g.q = p.q;
+    g.r = p.r;
+    g.h = p.h;
+    g.u = p.u;
+    g.first = s.pos - p.off;
     g.last = g.first + cost;
-    g.a = max(0, int(off) - s.extra);
-    g.b = min(g.n, max(0, int(off + take) - s.extra));
+    g.a = max(0, int(p.off) - s.extra);
+    g.b = min(g.n, max(0, int(p.off + take) - s.extra));
     s.pos += take;
-    off += take;
-    if (off == cost && s.pos < s.end) {
-      off = 0;
-      if ((u + 1) * ut < q.q_len) {
-        ++u;
-      } else if (h + 1 < a.hkv) {
-        u = 0;
-        ++h;
+    p.off += take;
+    if (p.off == cost && s.pos < s.end) {
+      p.off = 0;
+      if ((p.u + 1) * ut < p.q.q_len) {
+        ++p.u;
+      } else if (p.h + 1 < a.hkv) {
+        p.u = 0;
+        ++p.h;
       } else {
-        ++r;
-        enter(a, 0);
+        p.set(a, p.r + 1, attn_request(a, p.r + 1), 0, ut, kt, s.extra);
       }
     }
     return true;
@@ -229,8 +228,8 @@ struct AttnWalk {
   // The CTAs that hold parts of a unit: the cuts inside it, beyond what is moved to its ends, are those of the CTAs
   // b0 + 1 .. b1 (none: b0 >= b1).
   __device__ __forceinline__ void parts(const AttnSeg& g, int& b0, int& b1) const {
-    b0 = int(((g.first + s.extra + 1) * s.grid + s.total - 1) / s.total) - 1;
-    b1 = int(((g.last - s.extra) * s.grid - 1) / s.total);
+    b0 = int(attn_div((g.first + s.extra + 1) * s.grid + s.total - 1, s.total)) - 1;
+    b1 = int(attn_div((g.last - s.extra) * s.grid - 1, s.total));
   }
 };
 
@@ -396,10 +395,22 @@ cudaError_t attn_page_map(CUtensorMap* m, const AttnArgs& a, const void* base, i
 // SMs of the current device.
 int attn_sm_count();
 
+// Shared memory for a kernel, and the registers its warpgroups trade: setmaxnreg.inc waits for what the launch's
+// registers do not hold, so a build that gave the kernel fewer than `regs` a block is refused here.
+template <class K>
+inline cudaError_t attn_prepare_kernel(K kern, size_t smem, int threads, int regs) {
+  cudaFuncAttributes at;
+  cudaError_t e = cudaFuncGetAttributes(&at, kern);
+  if (e != cudaSuccess) return e;
+  if (at.numRegs * threads < regs) return cudaErrorInvalidKernelImage;
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+}
+
 // Map of the query rows: (column, head, token) boxes of 64 x box_heads x box_tokens.
 cudaError_t attn_query_map(CUtensorMap* m, const AttnArgs& a, int box_heads, int box_tokens);
 
-cudaError_t launch_attn_rows16(const AttnArgs& a, cudaStream_t s);
+// Units of at most 16 query rows (half: 8).
+cudaError_t launch_attn_rows(const AttnArgs& a, bool half, cudaStream_t s);
 cudaError_t launch_attn_tiles(const AttnArgs& a, cudaStream_t s);
 size_t attn_tiles_work_bytes(int dim);
 

@@ -227,11 +227,12 @@ __global__ void __launch_bounds__(TilesCfg<NS>::kThreads, 1)
   tl_fence_before();
   pdl_wait();
   const int tpt = 128 / a.group, ut = NQ * tpt;
-  const AttnShare share = attn_share<C::kThreads>(a, ut, kTileKeys, kTileUnit);  // its block barriers publish the ones above
+  AttnWalk walk;
+  walk.ut = ut;
+  walk.kt = kTileKeys;
+  walk.s = attn_share<C::kThreads>(a, ut, kTileKeys, kTileUnit, walk.p);  // its block barriers publish the ones above
   tl_fence_after();
   const uint32_t tmem = bars.tmem;
-  AttnWalk walk;
-  walk.begin(a, share, ut, kTileKeys);
   uint32_t* err = attn_err(a);
   AttnSeg g;
   TilesSeg<NQ> t;
@@ -741,12 +742,8 @@ static cudaError_t launch_tiles(const AttnArgs& a, cudaStream_t s) {
   if (e == cudaSuccess) e = attn_page_map(&mk, a, a.K, page < kTileKeys ? page : kTileKeys);
   if (e == cudaSuccess) e = attn_page_map(&mv, a, a.V, page < C::kVK ? page : C::kVK);
   if (e != cudaSuccess) return e;
-  static bool set = false;  // a function attribute, the same for every call
-  if (!set) {
-    e = cudaFuncSetAttribute(attn_tiles_kernel<NS>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::kSmem));
-    if (e != cudaSuccess) return e;
-    set = true;
-  }
+  static const cudaError_t ready = attn_prepare_kernel(attn_tiles_kernel<NS>, C::kSmem, C::kThreads, C::kNQ == 2 ? 104 * 128 + 200 * 256 : 0);
+  if (ready != cudaSuccess) return ready;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(min(attn_sm_count(), kAttnCtas));
   cfg.blockDim = dim3(C::kThreads);

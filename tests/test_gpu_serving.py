@@ -316,6 +316,27 @@ def test_attention_extreme_scores(gsi, dt):
     attention_case(gsi, dt, 2, 2, 64, 16, [(140, 300), (1, 77)], touch=lowest)
 
 
+@pytest.mark.parametrize("D", [64, 128, 192, 256])
+@pytest.mark.parametrize("q,group", [(1, 1), (1, 16), (40, 4)])
+def test_attention_streams_from_memory(gsi, D, q, group):
+    # more keys than the caches hold: copies land out of order, rings wrap thousands of times
+    hkv, page, k = 8, 16, 60001
+    n = -(-k // page)
+    g = torch.Generator(device="cuda").manual_seed(D + q)
+    K, V = (torch.randn(n, hkv, page, D, device="cuda", generator=g, dtype=BF) for _ in range(2))
+    Q = 2 * torch.randn(q, hkv * group, D, device="cuda", generator=g, dtype=BF)
+    table = torch.randperm(n, device="cuda", generator=g).int()[None]
+    ws = gsi.new_workspace(gsi.paged_attention_workspace_size(gsi.PagedCache(K, V), hkv * group))
+    out = gsi.paged_attention(gsi.PagedCache(K, V), Q, i32([0, q]), i32([k]), table, workspace=ws)
+    assert gsi.workspace_status(ws) == 0
+    hidden = torch.arange(k, device="cuda") > torch.arange(k - q, k, device="cuda")[:, None]
+    for h in range(hkv * group):
+        ks, vs = (t[table[0].long(), h // group].reshape(-1, D)[:k].double() for t in (K, V))
+        p = torch.softmax((Q[:, h].double() @ ks.T * D ** -0.5).masked_fill(hidden, -float("inf")), -1)
+        want, A = p @ vs, p @ vs.abs()
+        assert ((out[:, h].double() - want).abs() <= 1e-4 * A + 2**-8 * (A + want.abs())).all()
+
+
 def test_attention_offsets_beyond_32_bits(gsi):
     # a cache of more than 2^31 elements, the request's pages at its far end and at its beginning
     hkv, D, page, k = 8, 128, 64, 300
