@@ -8,8 +8,8 @@ namespace gsi {
 // With G = group query heads a key/value head and ut = floor(R / G) tokens a
 // unit, S = Q K^T and O = P V have at most R = 8 or 16 rows: 16 FLOP a byte of
 // cache at most, far below what the warp-level tensor products sustain, so the
-// bytes bound the kernel and its work is to keep them coming.  One CTA an SM; a
-// copy warp keeps a ring of 192 KB filled (64 keys and their values a stage,
+// bytes bound the kernel and its work is to keep them coming.  One CTA an SM;
+// copy warps keep a ring of 192 KB filled (64 keys and their values a stage,
 // one TMA box a page and 64 columns, each lane issuing its own box); eight warps
 // take every stage, two to each 16 keys: both form the scores and the softmax
 // (running maximum m, sum l) of these keys, and each half of the output's
@@ -24,7 +24,7 @@ constexpr int kRowsKt = 64;  // keys a stage
 template <int NS, bool HALF>  // 64-column slabs of a row; at most 8 rows
 struct RowsCfg {
   static constexpr int kWarps = 8;  // compute warps
-  // three warpgroups: the copy warp's hands registers to the others
+  // three warpgroups: the copy warps' hands registers to the others
   static constexpr int kThreads = 384;
   static constexpr int kRows = HALF ? 8 : 16;
   static constexpr int kSlab = kRowsKt * 128;            // bytes
@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(RowsCfg<NS, HALF>::kThreads, 1)
   pdl_launch_dependents();
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      bar_init(&full[s], 1);
+      bar_init(&full[s], 4);
       bar_init(&empty[s], NW);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -113,8 +113,9 @@ __global__ void __launch_bounds__(RowsCfg<NS, HALF>::kThreads, 1)
 
   if (warp >= NW) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp > NW) return;
-    // ---- copy warp: lane l issues box l of a stage (2 NS slabs of at most 4 boxes)
+    // ---- copy warps: a stage's boxes (2 NS slabs of at most 4) are dealt out to their lanes.  Four warps, because a
+    // warp issues its lanes' boxes one after the other, ~80 cycles each: 16 of them take one warp as long as the
+    // stage's bytes take to arrive.
     const int page = 1 << a.page_shift;
     const int box = min(page, kRowsKt), boxes = kRowsKt / box;  // tokens of a box; boxes of a slab
     const uint32_t box_bytes = uint32_t(box) * 128;
@@ -124,7 +125,7 @@ __global__ void __launch_bounds__(RowsCfg<NS, HALF>::kThreads, 1)
       const int lo_all = attn_lo(a, attn_lim(a, g.q, g.u * ut));
       const int32_t* row = a.table + int64_t(g.r) * a.width;
       // this lane's box: slabs of K, then of V
-      const int b = lane % boxes, slab = lane / boxes;
+      const int mine_no = lane * 4 + warp - NW, b = mine_no % boxes, slab = mine_no / boxes;
       // its page in tile i, if it has a key that some row sees (loaded a stage ahead: the table's latency is half a
       // stage's time)
       auto wanted = [&](int i) {
@@ -142,9 +143,9 @@ __global__ void __launch_bounds__(RowsCfg<NS, HALF>::kThreads, 1)
         if (it >= C::kStages)
           ok = __all_sync(0xffffffffu, bar_wait(&empty[s], uint32_t(it / C::kStages - 1) & 1u, err));
         if (!ok) break;
+        // each copy warp arrives for its own boxes, with none of them too: no warp falls behind a stage's next use
         const int n = __popc(__ballot_sync(0xffffffffu, mine));
         if (lane == 0) bar_expect_tx(&full[s], uint32_t(n) * box_bytes);
-        __syncwarp();
         if (mine)
           tma_load_page(sa(ring + size_t(s) * C::kStage + slab * C::kSlab) + b * box_bytes, slab < NS ? &mk : &mv,
                         sa(&full[s]), (slab < NS ? slab : slab - NS) * 64, (key0 + b * box) & (page - 1), g.h, pid);
