@@ -9,29 +9,31 @@ namespace gsi {
 // unit, S = Q K^T and O = P V have at most R = 8 or 16 rows: 16 FLOP a byte of
 // cache at most, far below what the warp-level tensor products sustain, so the
 // bytes bound the kernel and its work is to keep them coming.  One CTA an SM;
-// copy warps keep a ring of 192 KB filled (64 keys and their values a stage,
+// copy warps keep a ring of 192 KB filled (64 or 128 keys and their values a stage,
 // one TMA box a page and 64 columns, each lane issuing its own box); eight warps
-// take every stage, two to each 16 keys: both form the scores and the softmax
-// (running maximum m, sum l) of these keys, and each half of the output's
-// columns -- a stage's chain of products, maxima and exponentials has to be
-// shorter than its bytes take, and the scores are the cheap half of it.  The
+// take every stage, one to each 16 keys with a softmax of its own (running
+// maximum m, sum l).  A stage's chain of products, maxima, exponentials and
+// products has to be shorter than its 64 KB take to arrive (~2700 cycles): 128
+// keys a stage up to 128 columns; above, 64 keys, and two warps to each 16 of
+// them, which both form the scores and each half of the output's columns.  The
 // warps' parts are joined when the CTA's part of a unit ends.  The scores'
 // fragment of m16n8k16 is the next product's left operand as it stands, so P
 // never leaves the registers.  Up to 8 rows the lower half of the fragments is
 // neither kept nor scaled.
-constexpr int kRowsKt = 64;  // keys a stage
-
 template <int NS, bool HALF>  // 64-column slabs of a row; at most 8 rows
 struct RowsCfg {
-  static constexpr int kWarps = 8;  // compute warps
+  static constexpr int kWarps = 8;                       // compute warps
+  static constexpr int kKeyWarps = NS <= 2 ? 8 : 4;      // 16 keys of a stage each
+  static constexpr int kColWarps = kWarps / kKeyWarps;   // with the same keys: parts of the columns
+  static constexpr int kKt = 16 * kKeyWarps;             // keys a stage
   // three warpgroups: the copy warps' hands registers to the others
   static constexpr int kThreads = 384;
   static constexpr int kRows = HALF ? 8 : 16;
-  static constexpr int kSlab = kRowsKt * 128;            // bytes
+  static constexpr int kSlab = kKt * 128;                // bytes
   static constexpr int kStage = 2 * NS * kSlab;          // K slabs, then V slabs
-  static constexpr int kStages = 12 / NS;                // 192 KB
+  static constexpr int kStages = 196608 / kStage;        // 192 KB
   static constexpr int kDim = NS * 64;
-  static constexpr size_t kSmem = 1024 + size_t(kStages) * kStage + 16 * kDim * 4 + 4 * 32 * 4 + 2 * kStages * 8 + 16;
+  static constexpr size_t kSmem = 1024 + size_t(kStages) * kStage + 16 * kDim * 4 + kKeyWarps * 32 * 4 + 2 * kStages * 8 + 16;
 };
 
 __device__ __forceinline__ void rows_ldsm(uint32_t addr, uint32_t (&r)[4]) {
@@ -81,12 +83,12 @@ __global__ void __launch_bounds__(RowsCfg<NS, HALF>::kThreads, 1)
                      const __grid_constant__ AttnArgs a) {
   using C = RowsCfg<NS, HALF>;
   constexpr int NW = C::kWarps, NC = HALF ? 2 : 4, NY = NC / 2;  // values of a fragment a lane keeps; its rows
-  constexpr int NO = 4 * NS;                                     // 8-column pieces of the output a warp holds
+  constexpr int KW = C::kKeyWarps, NO = 8 * NS / C::kColWarps;  // 8-column pieces of the output a warp holds
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* s_o = reinterpret_cast<float*>(ring + size_t(C::kStages) * C::kStage);  // [16][kDim]
   float* s_ml = s_o + 16 * C::kDim;                                            // [keys' warp][m: 16, l: 16]
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_ml + 4 * 32);
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_ml + KW * 32);
   uint64_t* empty = full + C::kStages;
   int* s_flag = reinterpret_cast<int*>(empty + C::kStages);
 
@@ -105,19 +107,19 @@ __global__ void __launch_bounds__(RowsCfg<NS, HALF>::kThreads, 1)
   pdl_wait();
   AttnWalk walk;
   const int ut = walk.ut = C::kRows / a.group;
-  walk.kt = kRowsKt;
-  walk.s = attn_share<C::kThreads>(a, ut, kRowsKt, 0, walk.p);  // also publishes the barriers to the block
+  walk.kt = C::kKt;
+  walk.s = attn_share<C::kThreads>(a, ut, C::kKt, 0, walk.p);  // also publishes the barriers to the block
   uint32_t* err = attn_err(a);
   AttnSeg g;
   int it = 0;  // stages so far
 
   if (warp >= NW) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    // ---- copy warps: a stage's boxes (2 NS slabs of at most 4) are dealt out to their lanes.  Four warps, because a
+    // ---- copy warps: a stage's boxes (at most 32: 2 NS slabs, a box a page) are dealt out to their lanes.  Four warps, because a
     // warp issues its lanes' boxes one after the other, ~80 cycles each: 16 of them take one warp as long as the
     // stage's bytes take to arrive.
     const int page = 1 << a.page_shift;
-    const int box = min(page, kRowsKt), boxes = kRowsKt / box;  // tokens of a box; boxes of a slab
+    const int box = min(page, C::kKt), boxes = C::kKt / box;  // tokens of a box; boxes of a slab
     const uint32_t box_bytes = uint32_t(box) * 128;
     bool ok = true;
     while (ok && walk.next(a, g)) {
@@ -129,14 +131,14 @@ __global__ void __launch_bounds__(RowsCfg<NS, HALF>::kThreads, 1)
       // its page in tile i, if it has a key that some row sees (loaded a stage ahead: the table's latency is half a
       // stage's time)
       auto wanted = [&](int i) {
-        const int key0 = (g.t0 + i) * kRowsKt, first = max(lo_all - key0, 0) / box;
+        const int key0 = (g.t0 + i) * C::kKt, first = max(lo_all - key0, 0) / box;
         return i < g.b && slab < 2 * NS && b >= first && key0 + b * box < lim_all;
       };
-      auto page_of = [&](int i) { return wanted(i) ? __ldcg(row + (((g.t0 + i) * kRowsKt + b * box) >> a.page_shift)) : 0; };
+      auto page_of = [&](int i) { return wanted(i) ? __ldcg(row + (((g.t0 + i) * C::kKt + b * box) >> a.page_shift)) : 0; };
       int next = page_of(g.a);
       for (int i = g.a; i < g.b; ++i, ++it) {
         const int s = it % C::kStages;
-        const int key0 = (g.t0 + i) * kRowsKt;
+        const int key0 = (g.t0 + i) * C::kKt;
         const bool mine = wanted(i);
         const int pid = next;
         next = page_of(i + 1);
@@ -157,9 +159,9 @@ __global__ void __launch_bounds__(RowsCfg<NS, HALF>::kThreads, 1)
     return;
   }
 
-  // ---- compute warps: 16 keys of every stage (kg) and half of the columns (dh)
+  // ---- compute warps: 16 keys of every stage (kg), and a part of the columns (dh)
   asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-  const int kg = warp & 3, dh = warp >> 2;
+  const int kg = warp % KW, dh = warp / KW;
   const float sl = a.scale * 1.4426950408889634f;  // scores in powers of two
   const int r0 = lane >> 2, c0 = (lane & 3) * 2;
   bool ok = true;
@@ -200,8 +202,8 @@ __global__ void __launch_bounds__(RowsCfg<NS, HALF>::kThreads, 1)
 
     for (int i = g.a; i < g.b; ++i, ++it) {
       const int s = it % C::kStages;
-      const int tile = (g.t0 + i) * kRowsKt;
-      const bool partial = tile < lo_max || tile + kRowsKt > lim_min;
+      const int tile = (g.t0 + i) * C::kKt;
+      const bool partial = tile < lo_max || tile + C::kKt > lim_min;
       ok = ok && __all_sync(0xffffffffu, bar_wait(&full[s], uint32_t(it / C::kStages) & 1u, err));
       if (!ok) continue;
       const uint32_t kb = sa(ring + size_t(s) * C::kStage), vb = kb + NS * C::kSlab;
@@ -289,8 +291,8 @@ __global__ void __launch_bounds__(RowsCfg<NS, HALF>::kThreads, 1)
       if (lane == 0) bar_arrive(&empty[s]);
     }
 
-    // ---- the warps' parts of the segment: common maximum, one sum.  The shared rows hold up to four copies of the
-    // output (16 / n_rows); in each round the warps of that many 16 keys add to a copy each, in their order, and the
+    // ---- the warps' parts of the segment: common maximum, one sum.  The shared rows hold 16 / n_rows copies of the
+    // output; in each round the warps of that many 16 keys add to a copy each, in their order, and the
     // copies are added at the end.
 #pragma unroll
     for (int y = 0; y < NY; ++y) {
@@ -308,10 +310,10 @@ __global__ void __launch_bounds__(RowsCfg<NS, HALF>::kThreads, 1)
     for (int y = 0; y < NY; ++y) {
       float mx = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) mx = fmaxf(mx, s_ml[w * 32 + r0 + 8 * y]);
+      for (int w = 0; w < KW; ++w) mx = fmaxf(mx, s_ml[w * 32 + r0 + 8 * y]);
       m[y] = attn_scale(m[y], mx);  // this warp's factor
     }
-    const int copies = min(4, 16 / n_rows), rounds = (4 + copies - 1) / copies;
+    const int copies = min(KW, 16 / n_rows), rounds = (KW + copies - 1) / copies;
     for (int round = 0; round < rounds; ++round) {
       if (kg / copies == round) {
 #pragma unroll
@@ -342,9 +344,9 @@ __global__ void __launch_bounds__(RowsCfg<NS, HALF>::kThreads, 1)
       const int row = e / vec, c = (e - row * vec) * 8;
       float mx = -INFINITY, sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) mx = fmaxf(mx, s_ml[w * 32 + row]);
+      for (int w = 0; w < KW; ++w) mx = fmaxf(mx, s_ml[w * 32 + row]);
 #pragma unroll
-      for (int w = 0; w < 4; ++w) sum += s_ml[w * 32 + 16 + row] * attn_scale(s_ml[w * 32 + row], mx);
+      for (int w = 0; w < KW; ++w) sum += s_ml[w * 32 + 16 + row] * attn_scale(s_ml[w * 32 + row], mx);
       float v[8];
 #pragma unroll
       for (int x = 0; x < 8; ++x) v[x] = s_o[row * C::kDim + c + x];
@@ -354,7 +356,7 @@ __global__ void __launch_bounds__(RowsCfg<NS, HALF>::kThreads, 1)
       if (any) {
         const int rl = attn_lim(a, g.q, tok0 + row / a.group);
         for (int x = 0; x < 8; ++x)
-          v[x] = attn_nonfinite<BF16>(a, g, kRowsKt, attn_lo(a, rl), rl, lo_max, lim_min, c + x, v[x]);
+          v[x] = attn_nonfinite<BF16>(a, g, C::kKt, attn_lo(a, rl), rl, lo_max, lim_min, c + x, v[x]);
       }
       if (whole) {
         attn_finish<BF16, 8>(a, attn_out_row(a, g, tok0, row) * a.dim + c, c, sum, v);
@@ -391,7 +393,7 @@ template <int NS, bool HALF>
 static cudaError_t launch_rows(const AttnArgs& a, cudaStream_t s) {
   using C = RowsCfg<NS, HALF>;
   static_assert(C::kSmem + 512 <= 232448, "shared memory of an SM, some of it static");
-  const int box = (1 << a.page_shift) < kRowsKt ? (1 << a.page_shift) : kRowsKt;
+  const int box = (1 << a.page_shift) < C::kKt ? (1 << a.page_shift) : C::kKt;
   CUtensorMap mk, mv;
   cudaError_t e = attn_page_map(&mk, a, a.K, box);
   if (e == cudaSuccess) e = attn_page_map(&mv, a, a.V, box);
