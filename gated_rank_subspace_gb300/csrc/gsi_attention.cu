@@ -134,7 +134,7 @@ cudaError_t attn_query_map(CUtensorMap* m, const AttnArgs& a, int box_heads, int
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-int attn_sm_count() {
+int sm_count() {
   static const int n = [] {
     int dev = 0, v = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)

@@ -305,7 +305,7 @@ __device__ __forceinline__ void attn_store8(const AttnArgs& a, int64_t at, const
 template <bool kRowMajor, int CW>
 __device__ __forceinline__ void attn_fold(const AttnArgs& a, int from, int to, int b0, int tiles, int tile, int rows,
                                           int row, int c, float& m, float& l, float (&o)[CW]) {
-#pragma unroll(CW <= 8 ? 4 : 1)
+#pragma unroll(CW <= 8 ? 8 : 1)
   for (int b = from; b <= to; ++b) {
     float* p = attn_part(a, 2 * b + (b == b0), tiles, tile, rows);
     const float mp = __ldcg(p + row), lp = __ldcg(p + rows + row);
@@ -391,9 +391,6 @@ __device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap* m
 // Maps of K and V with boxes of 64 columns x box_rows tokens (128-byte
 // swizzle; columns beyond head_dim and pages outside the cache read as zeros).
 cudaError_t attn_page_map(CUtensorMap* m, const AttnArgs& a, const void* base, int box_rows);
-
-// SMs of the current device.
-int attn_sm_count();
 
 // Shared memory for a kernel, and the registers its warpgroups trade: setmaxnreg.inc waits for what the launch's
 // registers do not hold, so a build that gave the kernel fewer than `regs` a block is refused here.

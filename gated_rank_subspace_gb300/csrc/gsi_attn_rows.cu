@@ -401,7 +401,7 @@ static cudaError_t launch_rows(const AttnArgs& a, cudaStream_t s) {
   static const cudaError_t ready = attn_prepare_kernel(attn_rows_kernel<NS, HALF>, C::kSmem, C::kThreads, 72 * 128 + 216 * 256);
   if (ready != cudaSuccess) return ready;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(min(attn_sm_count(), kAttnCtas));
+  cfg.gridDim = dim3(min(sm_count(), kAttnCtas));
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;

@@ -745,7 +745,7 @@ static cudaError_t launch_tiles(const AttnArgs& a, cudaStream_t s) {
   static const cudaError_t ready = attn_prepare_kernel(attn_tiles_kernel<NS>, C::kSmem, C::kThreads, C::kNQ == 2 ? 104 * 128 + 200 * 256 : 0);
   if (ready != cudaSuccess) return ready;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(min(attn_sm_count(), kAttnCtas));
+  cfg.gridDim = dim3(min(sm_count(), kAttnCtas));
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;

@@ -255,6 +255,9 @@ cudaError_t launch_image(const void* W, const void* V, void* M, float* gram, int
                          int64_t d_out, int64_t k, gsi_dtype dt, cudaStream_t s);
 
 
+// SMs of the current device.
+int sm_count();
+
 // Serving operators (see gsi_paged.cu, gsi_norm.cu, gsi_attention.cu).
 struct PlanArgs {
   const int32_t* cached;

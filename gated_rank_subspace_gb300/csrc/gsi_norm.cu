@@ -1,158 +1,332 @@
 // The end of one block and the beginning of the next in one pass:
 //   h' = alpha h + gate * post(y),   x = pre(h').
 
+#include <type_traits>
+
 #include "gsi_common.cuh"
 #include "gsi_kernels.h"
 
 namespace gsi {
 
-// One CTA a token.  Every value of the row stays in registers from its load
-// to its stores: y and h are read once, h' and x written once, and the norms'
-// sums are block reductions between (LAYER: the mean first, then the centred
-// squares, so no difference of large sums).  The bytes bound it at prompt
-// sizes; one token is a chain of loads and up to four reductions.
-template <int N>
+// Every value of a row stays in registers from its load to its stores: y and h
+// are read once, h' and x written once, and the norms' sums are block
+// reductions between (LAYER: the mean first, then the centred squares, so no
+// difference of large sums appears).  A thread holds pieces of four values, the
+// next thread the next piece: a warp's 16-byte accesses cover whole lines (with
+// eight float32 values a thread every access touched half of twice the sectors).
+//
+// Few tokens are latency: a CTA a token.  Many are bytes, and a CTA a token
+// waits for its first loads and its weights most of its life: there the CTAs
+// stay, keep the weights in shared memory and copy the rows to come ahead of
+// the one they work on, each thread its own pieces, so that no barrier guards
+// them.
 __device__ __forceinline__ float norm_block_sum(float v, float* red) {
   v = warp_sum(v);
-  const int warps = blockDim.x >> 5;
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  if (lane == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  float s = (threadIdx.x & 31) < warps ? red[threadIdx.x & 31] : 0.f;
-  s = warp_sum(s);
-  return s;
+  return warp_sum(lane < warps ? red[lane] : 0.f);
 }
 
+// Four values from 16 bytes of float32, or 8 of bf16.
+__device__ __forceinline__ void norm_unpack(const uint4& v, float* f) {
+  f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y), f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
+}
+__device__ __forceinline__ void norm_unpack(const uint2& v, float* f) {
+  BF16::unpack2(v.x, f[0], f[1]);
+  BF16::unpack2(v.y, f[2], f[3]);
+}
 template <class T>
-__device__ __forceinline__ void norm_load8(const void* p, int64_t e, float* f) {
+struct NormPiece;
+template <>
+struct NormPiece<F32> {
+  using Raw = uint4;
+};
+template <>
+struct NormPiece<BF16> {
+  using Raw = uint2;
+};
+template <class T>
+__device__ __forceinline__ void norm_load4(const void* p, int64_t e, float* f) {
+  norm_unpack(__ldcg(reinterpret_cast<const typename NormPiece<T>::Raw*>(static_cast<const char*>(p) + e * T::kBytes)), f);
+}
+template <class T>
+__device__ __forceinline__ void norm_store4(void* p, int64_t e, const float* f) {
   if constexpr (T::kBytes == 2) {
-    T::unpack(ld_cg_v4(static_cast<const char*>(p) + e * 2), f);
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(f[0], f[1]), hi = __floats2bfloat162_rn(f[2], f[3]);
+    *reinterpret_cast<uint2*>(static_cast<char*>(p) + e * 2) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
   } else {
-    T::unpack(ld_cg_v4(static_cast<const char*>(p) + e * 4), f);
-    T::unpack(ld_cg_v4(static_cast<const char*>(p) + e * 4 + 16), f + 4);
+    *reinterpret_cast<float4*>(static_cast<char*>(p) + e * 4) = make_float4(f[0], f[1], f[2], f[3]);
   }
 }
-
-template <class T>
-__device__ __forceinline__ void norm_store8(void* p, int64_t e, const float* f) {
-  if constexpr (T::kBytes == 2) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&v);
-    }
-    *reinterpret_cast<uint4*>(static_cast<char*>(p) + e * 2) = make_uint4(w[0], w[1], w[2], w[3]);
-  } else {
-    float4* q = reinterpret_cast<float4*>(static_cast<char*>(p) + e * 4);
-    q[0] = make_float4(f[0], f[1], f[2], f[3]);
-    q[1] = make_float4(f[4], f[5], f[6], f[7]);
-  }
+// Four float32 parameters (SHARED: staged in shared memory).
+template <bool SHARED>
+__device__ __forceinline__ float4 norm_param4(const float* p, int c) {
+  if constexpr (SHARED) return *reinterpret_cast<const float4*>(p + c);
+  else return __ldcg(reinterpret_cast<const float4*>(p + c));
 }
-
-// v <- norm(v) * weight + bias over the row (VPT vectors of 8 a thread; red:
-// two rows of 32 partial sums).
+// Where a norm's weight and bias come from: piece i, column c (absent: 1 and 0).
+template <bool SHARED>
+struct NormMem {
+  const float *w, *b;
+  __device__ __forceinline__ float4 weight(int, int c) const { return w ? norm_param4<SHARED>(w, c) : make_float4(1.f, 1.f, 1.f, 1.f); }
+  __device__ __forceinline__ float4 bias(int, int c) const { return b ? norm_param4<SHARED>(b, c) : make_float4(0.f, 0.f, 0.f, 0.f); }
+};
 template <int VPT>
-__device__ __forceinline__ void norm_row(float (&v)[VPT][8], int kind, float eps, const float* w, const float* b, int d,
-                                         float (*red)[32]) {
+struct NormRegs {
+  float4 w[VPT], b[VPT];
+  __device__ __forceinline__ void load(const float* wp, const float* bp, int d) {
+    const NormMem<false> m{wp, bp};
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = (threadIdx.x + i * blockDim.x) * 4;
+      if (c < d) {
+        w[i] = m.weight(i, c);
+        b[i] = m.bias(i, c);
+      }
+    }
+  }
+  __device__ __forceinline__ float4 weight(int i, int) const { return w[i]; }
+  __device__ __forceinline__ float4 bias(int i, int) const { return b[i]; }
+};
+
+// v <- norm(v) * weight + bias over the row; red: two rows of 32 sums.
+template <int VPT, class P>
+__device__ __forceinline__ void norm_row(float (&v)[VPT][4], int kind, float eps, const P& par, int d, float (*red)[32]) {
   if (kind == GSI_NORM_NONE) return;
+  const int c0 = threadIdx.x * 4, dc = blockDim.x * 4;
+  const float inv_d = 1.f / float(d);
   if (kind == GSI_NORM_LAYER) {
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s += v[i][e];
-    const float mean = norm_block_sum<VPT>(s, red[0]) / float(d);
+    for (int i = 0; i < VPT; ++i) s += (v[i][0] + v[i][1]) + (v[i][2] + v[i][3]);
+    const float mean = norm_block_sum(s, red[0]) * inv_d;
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
+      if (c0 + i * dc < d)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] -= mean;
+        for (int e = 0; e < 4; ++e) v[i][e] -= mean;
   }
   float q = 0.f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
-    if ((threadIdx.x + i * blockDim.x) * 8 < d)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) q = fmaf(v[i][e], v[i][e], q);
-  const float r = rsqrtf(norm_block_sum<VPT>(q, red[1]) / float(d) + eps);
+    for (int e = 0; e < 4; ++e) q = fmaf(v[i][e], v[i][e], q);
+  const float r = rsqrtf(norm_block_sum(q, red[1]) * inv_d + eps);
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int c = (threadIdx.x + i * blockDim.x) * 8;
-    if (c >= d) continue;
-    float wv[8], bv[8];
-    if (w) norm_load8<F32>(w, c, wv);
-    if (b) norm_load8<F32>(b, c, bv);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      v[i][e] *= r;
-      if (w) v[i][e] *= wv[e];
-      if (b) v[i][e] += bv[e];
+    const int c = c0 + i * dc;
+    if (c < d) {
+      const float4 wv = par.weight(i, c), bv = par.bias(i, c);
+      v[i][0] = fmaf(v[i][0] * r, wv.x, bv.x);
+      v[i][1] = fmaf(v[i][1] * r, wv.y, bv.y);
+      v[i][2] = fmaf(v[i][2] * r, wv.z, bv.z);
+      v[i][3] = fmaf(v[i][3] * r, wv.w, bv.w);
     }
   }
 }
 
+// One row from its values in y and h (0 beyond the row) to its stores.  gate:
+// the token's row of the gate (in shared memory where SHARED_GATE);
+// no_gate: a gate of 0.
+template <class HT, class XT, int VPT, bool SHARED_GATE, class P>
+__device__ __forceinline__ void norm_token(const NormArgs& a, const P& post, const P& pre, int64_t row, float (&y)[VPT][4],
+                                           float (&h)[VPT][4], const float* gate, bool no_gate, float (*red)[32]) {
+  const int c0 = threadIdx.x * 4, dc = blockDim.x * 4;
+  float4 gv[VPT];
+  if (a.gate) {  // ahead of the reduction
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      gv[i] = c0 + i * dc < a.d && !no_gate ? norm_param4<SHARED_GATE>(gate, c0 + i * dc) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  if (a.Y) {
+    norm_row<VPT>(y, a.post, a.post_eps, post, a.d, red);
+    if (a.gate) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) y[i][0] *= gv[i].x, y[i][1] *= gv[i].y, y[i][2] *= gv[i].z, y[i][3] *= gv[i].w;
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) h[i][e] = fmaf(a.alpha, h[i][e], y[i][e]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) h[i][e] *= a.alpha;
+  }
+  if (a.H_out) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      if (c0 + i * dc < a.d) norm_store4<HT>(a.H_out, row + c0 + i * dc, h[i]);
+  }
+  if (!a.X) return;
+  norm_row<VPT>(h, a.pre, a.pre_eps, pre, a.d, red + 2);
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+    if (c0 + i * dc < a.d) norm_store4<XT>(a.X, row + c0 + i * dc, h[i]);
+}
+
+// A CTA a token.
 template <class HT, class YT, class XT, int VPT>
-__global__ void __launch_bounds__(1024) norm_residual_kernel(NormArgs a) {
+__global__ void __launch_bounds__(1024, 1) norm_token_kernel(const __grid_constant__ NormArgs a) {
   __shared__ float red[4][32];
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t t = blockIdx.x;
-  const int64_t row = t * a.d;
-  float h[VPT][8], y[VPT][8];
+  const int64_t t = blockIdx.x, row = t * a.d;
+  float h[VPT][4] = {}, y[VPT][4] = {};
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int c = (threadIdx.x + i * blockDim.x) * 8;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) h[i][e] = y[i][e] = 0.f;
+    const int c = (threadIdx.x + i * blockDim.x) * 4;
     if (c < a.d) {
-      if (a.Y) norm_load8<YT>(a.Y, row + c, y[i]);
-      norm_load8<HT>(a.H, row + c, h[i]);
+      if (a.Y) norm_load4<YT>(a.Y, row + c, y[i]);
+      norm_load4<HT>(a.H, row + c, h[i]);
     }
   }
-  int64_t g = 0;
-  if (a.gate && a.gate_index) g = __ldcg(a.gate_index + t);
-  if (a.Y) norm_row<VPT>(y, a.post, a.post_eps, a.post_w, a.post_b, a.d, red);
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int c = (threadIdx.x + i * blockDim.x) * 8;
-    if (c >= a.d) continue;
-    float gv[8];
-    if (a.gate) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) gv[e] = 0.f;
-      if (g >= 0 && g < a.gate_rows) norm_load8<F32>(a.gate, g * a.d + c, gv);
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float u = a.alpha * h[i][e];
-      if (a.Y) u = a.gate ? fmaf(gv[e], y[i][e], u) : u + y[i][e];
-      h[i][e] = u;
-    }
-    if (a.H_out) norm_store8<HT>(a.H_out, row + c, h[i]);
+  const int g = a.gate && a.gate_index ? __ldcg(a.gate_index + t) : 0;
+  norm_token<HT, XT, VPT, false>(a, NormMem<false>{a.post_w, a.post_b}, NormMem<false>{a.pre_w, a.pre_b}, row, y, h,
+                                 a.gate + int64_t(g) * a.d, g < 0 || g >= a.gate_rows, red);
+}
+
+// CTAs that stay: tokens blockIdx.x, + gridDim.x, ...  Shared memory: a gate of
+// one row, then kNormAhead + 1 rows' pieces, those of a thread written and read
+// by it alone.  The weights are in registers (REGS, two pieces a thread, up to
+// 5120 values), or, where wider rows leave no room for them, in shared memory
+// before the rows (four pieces a thread): 2049 x 5120 LAYER takes 26 us the
+// first way and 42 us the second, whose fewer warps wait on each other longer.
+constexpr int kNormAhead = 3;
+template <bool REGS>
+struct NormRowsCfg {
+  static constexpr int kVpt = REGS ? 2 : 4, kThreads = REGS ? 640 : 512;
+};
+
+template <int BYTES>
+__device__ __forceinline__ void norm_copy(void* dst, const void* src) {
+  const uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(s), "l"(src) : "memory");
+}
+
+template <class HT, class YT, class XT, bool REGS>
+__global__ void __launch_bounds__(NormRowsCfg<REGS>::kThreads, 1) norm_rows_kernel(const __grid_constant__ NormArgs a) {
+  extern __shared__ uint4 norm_smem[];
+  __shared__ float red[4][32];
+  constexpr int VPT = NormRowsCfg<REGS>::kVpt;
+  using Par = std::conditional_t<REGS, NormRegs<VPT>, NormMem<true>>;
+  using RawY = typename NormPiece<YT>::Raw;
+  using RawH = typename NormPiece<HT>::Raw;
+  const int tid = threadIdx.x, nt = blockDim.x;
+  pdl_launch_dependents();
+  pdl_wait();
+  float* par = reinterpret_cast<float*>(norm_smem);
+  auto stage = [&](const float* p) -> const float* {
+    if (!p) return nullptr;
+    float* at = par;
+    for (int c = tid * 4; c < a.d; c += nt * 4) norm_copy<16>(at + c, p + c);
+    par += a.d;
+    return at;
+  };
+  Par post, pre;
+  if constexpr (REGS) {
+    post.load(a.post_w, a.post_b, a.d);
+    pre.load(a.pre_w, a.pre_b, a.d);
+  } else {
+    post = Par{stage(a.post_w), stage(a.post_b)};
+    pre = Par{stage(a.pre_w), stage(a.pre_b)};
   }
-  if (!a.X) return;
-  norm_row<VPT>(h, a.pre, a.pre_eps, a.pre_w, a.pre_b, a.d, red + 2);
+  const bool by_index = a.gate && a.gate_index;
+  const float* gate = by_index ? a.gate : stage(a.gate);
+  RawY* ry = reinterpret_cast<RawY*>(par) + tid;                                     // [slot][piece][thread]
+  RawH* rh = reinterpret_cast<RawH*>(reinterpret_cast<RawY*>(par) + (kNormAhead + 1) * VPT * nt) + tid;
+  auto fetch = [&](int64_t t, int slot) {
+    if (t < a.T) {
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int c = (threadIdx.x + i * blockDim.x) * 8;
-    if (c < a.d) norm_store8<XT>(a.X, row + c, h[i]);
+      for (int v = 0; v < VPT; ++v) {
+        const int c = (tid + v * nt) * 4;
+        if (c < a.d) {
+          if (a.Y) norm_copy<sizeof(RawY)>(ry + (slot * VPT + v) * nt, static_cast<const char*>(a.Y) + (t * a.d + c) * YT::kBytes);
+          norm_copy<sizeof(RawH)>(rh + (slot * VPT + v) * nt, static_cast<const char*>(a.H) + (t * a.d + c) * HT::kBytes);
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  int64_t t = blockIdx.x;
+  const int64_t step = gridDim.x;
+#pragma unroll
+  for (int i = 0; i < kNormAhead; ++i) fetch(t + i * step, i);
+  int g = by_index ? __ldcg(a.gate_index + t) : 0;
+  for (int it = 0; t < a.T; ++it, t += step) {
+    fetch(t + kNormAhead * step, (it + kNormAhead) & kNormAhead);
+    const int g_next = by_index && t + step < a.T ? __ldcg(a.gate_index + t + step) : 0;
+    asm volatile("cp.async.wait_group %0;" ::"n"(kNormAhead) : "memory");  // (the parameters are in the first group)
+    __syncthreads();  // the parameters of every thread are there; the sums of the row before have been read
+    float y[VPT][4] = {}, h[VPT][4] = {};
+    const int slot = it & kNormAhead;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v)
+      if ((tid + v * nt) * 4 < a.d) {
+        if (a.Y) norm_unpack(ry[(slot * VPT + v) * nt], y[v]);
+        norm_unpack(rh[(slot * VPT + v) * nt], h[v]);
+      }
+    if (by_index)
+      norm_token<HT, XT, VPT, false>(a, post, pre, t * a.d, y, h, gate + int64_t(g) * a.d, g < 0 || g >= a.gate_rows, red);
+    else
+      norm_token<HT, XT, VPT, true>(a, post, pre, t * a.d, y, h, gate, false, red);
+    g = g_next;
   }
+}
+static_assert((kNormAhead & (kNormAhead + 1)) == 0, "a slot is the row's number modulo a power of two");
+
+// false: this form does not hold the row.
+template <class HT, class YT, class XT, bool REGS>
+static bool launch_norm_rows(const NormArgs& a, cudaLaunchConfig_t cfg, cudaError_t* e) {
+  using C = NormRowsCfg<REGS>;
+  const int threads = ((a.d / 4 + C::kVpt - 1) / C::kVpt + 31) / 32 * 32;
+  const int params = (!REGS && a.post_w) + (!REGS && a.post_b) + (!REGS && a.pre_w) + (!REGS && a.pre_b) +
+                     (a.gate && !a.gate_index);
+  const size_t smem = size_t(params) * a.d * 4 + size_t(kNormAhead + 1) * C::kVpt * threads * 4 * (HT::kBytes + YT::kBytes);
+  constexpr size_t kMost = 232448 - 1024;
+  if (threads > C::kThreads || smem > kMost) return false;
+  static const cudaError_t ready = cudaFuncSetAttribute(norm_rows_kernel<HT, YT, XT, REGS>,
+                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMost));
+  *e = ready;
+  if (ready != cudaSuccess) return true;
+  // CTAs of an SM: what its registers and shared memory hold
+  const int per_sm = max(1, min(C::kThreads / threads, int(kMost / (smem + 2048))));
+  cfg.gridDim = dim3(min(a.T, sm_count() * per_sm));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  *e = cudaLaunchKernelEx(&cfg, norm_rows_kernel<HT, YT, XT, REGS>, a);
+  return true;
 }
 
 template <class HT, class YT, class XT>
 static cudaError_t launch_norm_types(const NormArgs& a, cudaStream_t s) {
-  const int n_vec = a.d / 8;
-  const int vpt = n_vec > 1024 ? 2 : 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(a.T);
-  cfg.blockDim = dim3(((n_vec + vpt - 1) / vpt + 31) / 32 * 32);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return vpt == 2 ? cudaLaunchKernelEx(&cfg, norm_residual_kernel<HT, YT, XT, 2>, a)
-                  : cudaLaunchKernelEx(&cfg, norm_residual_kernel<HT, YT, XT, 1>, a);
+  // CTAs that stay pay from about two tokens an SM on
+  cudaError_t e;
+  if (a.T >= 2 * sm_count() && (launch_norm_rows<HT, YT, XT, true>(a, cfg, &e) || launch_norm_rows<HT, YT, XT, false>(a, cfg, &e)))
+    return e;
+  const int pieces = a.d / 4;
+  const auto threads_for = [&](int vpt) { return ((pieces + vpt - 1) / vpt + 31) / 32 * 32; };
+  cfg.gridDim = dim3(a.T);
+  const int vpt = pieces <= 1024 ? 1 : pieces <= 2048 ? 2 : 4;
+  cfg.blockDim = dim3(threads_for(vpt));
+  switch (vpt) {
+    case 1: return cudaLaunchKernelEx(&cfg, norm_token_kernel<HT, YT, XT, 1>, a);
+    case 2: return cudaLaunchKernelEx(&cfg, norm_token_kernel<HT, YT, XT, 2>, a);
+    default: return cudaLaunchKernelEx(&cfg, norm_token_kernel<HT, YT, XT, 4>, a);
+  }
 }
 
 cudaError_t launch_norm_residual(const NormArgs& a, gsi_dtype hdt, gsi_dtype ydt, gsi_dtype xdt, cudaStream_t s) {
