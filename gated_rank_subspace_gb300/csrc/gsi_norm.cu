@@ -76,54 +76,63 @@ struct NormMem {
 template <int VPT>
 struct NormRegs {
   float4 w[VPT], b[VPT];
-  __device__ __forceinline__ void load(const float* wp, const float* bp, int d) {
+  __device__ __forceinline__ void load(const float* wp, const float* bp, const int (&c)[VPT]) {
     const NormMem<false> m{wp, bp};
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = (threadIdx.x + i * blockDim.x) * 4;
-      if (c < d) {
-        w[i] = m.weight(i, c);
-        b[i] = m.bias(i, c);
-      }
+      w[i] = m.weight(i, c[i]);
+      b[i] = m.bias(i, c[i]);
     }
   }
   __device__ __forceinline__ float4 weight(int i, int) const { return w[i]; }
   __device__ __forceinline__ float4 bias(int i, int) const { return b[i]; }
 };
 
-// v <- norm(v) * weight + bias over the row; red: two rows of 32 sums.
+// A thread's pieces: their columns (those beyond the row stand on column 0 and
+// count 0 in one[]; their values never leave the thread).
+template <int VPT>
+struct NormRow {
+  int c[VPT];
+  float one[VPT], inv_d;
+  __device__ __forceinline__ NormRow(int d) : inv_d(1.f / float(d)) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      c[i] = (threadIdx.x + i * blockDim.x) * 4;
+      one[i] = c[i] < d ? 1.f : 0.f;
+      if (c[i] >= d) c[i] = 0;
+    }
+  }
+  __device__ __forceinline__ bool in(int i) const { return one[i] != 0.f; }
+};
+
+// v <- norm(v) * weight + bias over the row (on entry 0 beyond it); red: two rows of 32 sums.
 template <int VPT, class P>
-__device__ __forceinline__ void norm_row(float (&v)[VPT][4], int kind, float eps, const P& par, int d, float (*red)[32]) {
+__device__ __forceinline__ void norm_row(float (&v)[VPT][4], int kind, float eps, const P& par, const NormRow<VPT>& k,
+                                         float (*red)[32]) {
   if (kind == GSI_NORM_NONE) return;
-  const int c0 = threadIdx.x * 4, dc = blockDim.x * 4;
-  const float inv_d = 1.f / float(d);
   if (kind == GSI_NORM_LAYER) {
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) s += (v[i][0] + v[i][1]) + (v[i][2] + v[i][3]);
-    const float mean = norm_block_sum(s, red[0]) * inv_d;
+    const float mean = norm_block_sum(s, red[0]) * k.inv_d;
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
-      if (c0 + i * dc < d)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[i][e] -= mean;
+      for (int e = 0; e < 4; ++e) v[i][e] = fmaf(-mean, k.one[i], v[i][e]);
   }
   float q = 0.f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
 #pragma unroll
     for (int e = 0; e < 4; ++e) q = fmaf(v[i][e], v[i][e], q);
-  const float r = rsqrtf(norm_block_sum(q, red[1]) * inv_d + eps);
+  const float r = rsqrtf(fmaf(norm_block_sum(q, red[1]), k.inv_d, eps));
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int c = c0 + i * dc;
-    if (c < d) {
-      const float4 wv = par.weight(i, c), bv = par.bias(i, c);
-      v[i][0] = fmaf(v[i][0] * r, wv.x, bv.x);
-      v[i][1] = fmaf(v[i][1] * r, wv.y, bv.y);
-      v[i][2] = fmaf(v[i][2] * r, wv.z, bv.z);
-      v[i][3] = fmaf(v[i][3] * r, wv.w, bv.w);
-    }
+    const float4 wv = par.weight(i, k.c[i]), bv = par.bias(i, k.c[i]);
+    v[i][0] = fmaf(v[i][0] * r, wv.x, bv.x);
+    v[i][1] = fmaf(v[i][1] * r, wv.y, bv.y);
+    v[i][2] = fmaf(v[i][2] * r, wv.z, bv.z);
+    v[i][3] = fmaf(v[i][3] * r, wv.w, bv.w);
   }
 }
 
@@ -131,41 +140,35 @@ __device__ __forceinline__ void norm_row(float (&v)[VPT][4], int kind, float eps
 // the token's row of the gate (in shared memory where SHARED_GATE);
 // no_gate: a gate of 0.
 template <class HT, class XT, int VPT, bool SHARED_GATE, class P>
-__device__ __forceinline__ void norm_token(const NormArgs& a, const P& post, const P& pre, int64_t row, float (&y)[VPT][4],
-                                           float (&h)[VPT][4], const float* gate, bool no_gate, float (*red)[32]) {
-  const int c0 = threadIdx.x * 4, dc = blockDim.x * 4;
+__device__ __forceinline__ void norm_token(const NormArgs& a, const NormRow<VPT>& k, const P& post, const P& pre, int64_t row,
+                                           float (&y)[VPT][4], float (&h)[VPT][4], const float* gate, bool no_gate,
+                                           float (*red)[32]) {
   float4 gv[VPT];
   if (a.gate) {  // ahead of the reduction
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
-      gv[i] = c0 + i * dc < a.d && !no_gate ? norm_param4<SHARED_GATE>(gate, c0 + i * dc) : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < VPT; ++i) gv[i] = no_gate ? make_float4(0.f, 0.f, 0.f, 0.f) : norm_param4<SHARED_GATE>(gate, k.c[i]);
   }
   if (a.Y) {
-    norm_row<VPT>(y, a.post, a.post_eps, post, a.d, red);
+    norm_row<VPT>(y, a.post, a.post_eps, post, k, red);
     if (a.gate) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i) y[i][0] *= gv[i].x, y[i][1] *= gv[i].y, y[i][2] *= gv[i].z, y[i][3] *= gv[i].w;
     }
-#pragma unroll
-    for (int i = 0; i < VPT; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) h[i][e] = fmaf(a.alpha, h[i][e], y[i][e]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < VPT; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) h[i][e] *= a.alpha;
   }
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[i][e] = fmaf(a.alpha, h[i][e], y[i][e]) * k.one[i];
   if (a.H_out) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
-      if (c0 + i * dc < a.d) norm_store4<HT>(a.H_out, row + c0 + i * dc, h[i]);
+      if (k.in(i)) norm_store4<HT>(a.H_out, row + k.c[i], h[i]);
   }
   if (!a.X) return;
-  norm_row<VPT>(h, a.pre, a.pre_eps, pre, a.d, red + 2);
+  norm_row<VPT>(h, a.pre, a.pre_eps, pre, k, red + 2);
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
-    if (c0 + i * dc < a.d) norm_store4<XT>(a.X, row + c0 + i * dc, h[i]);
+    if (k.in(i)) norm_store4<XT>(a.X, row + k.c[i], h[i]);
 }
 
 // A CTA a token.
@@ -175,17 +178,16 @@ __global__ void __launch_bounds__(1024, 1) norm_token_kernel(const __grid_consta
   pdl_launch_dependents();
   pdl_wait();
   const int64_t t = blockIdx.x, row = t * a.d;
+  const NormRow<VPT> k(a.d);
   float h[VPT][4] = {}, y[VPT][4] = {};
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int c = (threadIdx.x + i * blockDim.x) * 4;
-    if (c < a.d) {
-      if (a.Y) norm_load4<YT>(a.Y, row + c, y[i]);
-      norm_load4<HT>(a.H, row + c, h[i]);
+  for (int i = 0; i < VPT; ++i)
+    if (k.in(i)) {
+      if (a.Y) norm_load4<YT>(a.Y, row + k.c[i], y[i]);
+      norm_load4<HT>(a.H, row + k.c[i], h[i]);
     }
-  }
   const int g = a.gate && a.gate_index ? __ldcg(a.gate_index + t) : 0;
-  norm_token<HT, XT, VPT, false>(a, NormMem<false>{a.post_w, a.post_b}, NormMem<false>{a.pre_w, a.pre_b}, row, y, h,
+  norm_token<HT, XT, VPT, false>(a, k, NormMem<false>{a.post_w, a.post_b}, NormMem<false>{a.pre_w, a.pre_b}, row, y, h,
                                  a.gate + int64_t(g) * a.d, g < 0 || g >= a.gate_rows, red);
 }
 
@@ -229,10 +231,11 @@ __global__ void __launch_bounds__(NormRowsCfg<REGS>::kThreads, 1) norm_rows_kern
     par += a.d;
     return at;
   };
+  const NormRow<VPT> k(a.d);
   Par post, pre;
   if constexpr (REGS) {
-    post.load(a.post_w, a.post_b, a.d);
-    pre.load(a.pre_w, a.pre_b, a.d);
+    post.load(a.post_w, a.post_b, k.c);
+    pre.load(a.pre_w, a.pre_b, k.c);
   } else {
     post = Par{stage(a.post_w), stage(a.post_b)};
     pre = Par{stage(a.pre_w), stage(a.pre_b)};
@@ -244,13 +247,11 @@ __global__ void __launch_bounds__(NormRowsCfg<REGS>::kThreads, 1) norm_rows_kern
   auto fetch = [&](int64_t t, int slot) {
     if (t < a.T) {
 #pragma unroll
-      for (int v = 0; v < VPT; ++v) {
-        const int c = (tid + v * nt) * 4;
-        if (c < a.d) {
-          if (a.Y) norm_copy<sizeof(RawY)>(ry + (slot * VPT + v) * nt, static_cast<const char*>(a.Y) + (t * a.d + c) * YT::kBytes);
-          norm_copy<sizeof(RawH)>(rh + (slot * VPT + v) * nt, static_cast<const char*>(a.H) + (t * a.d + c) * HT::kBytes);
+      for (int v = 0; v < VPT; ++v)
+        if (k.in(v)) {
+          if (a.Y) norm_copy<sizeof(RawY)>(ry + (slot * VPT + v) * nt, static_cast<const char*>(a.Y) + (t * a.d + k.c[v]) * YT::kBytes);
+          norm_copy<sizeof(RawH)>(rh + (slot * VPT + v) * nt, static_cast<const char*>(a.H) + (t * a.d + k.c[v]) * HT::kBytes);
         }
-      }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -268,14 +269,14 @@ __global__ void __launch_bounds__(NormRowsCfg<REGS>::kThreads, 1) norm_rows_kern
     const int slot = it & kNormAhead;
 #pragma unroll
     for (int v = 0; v < VPT; ++v)
-      if ((tid + v * nt) * 4 < a.d) {
+      if (k.in(v)) {
         if (a.Y) norm_unpack(ry[(slot * VPT + v) * nt], y[v]);
         norm_unpack(rh[(slot * VPT + v) * nt], h[v]);
       }
     if (by_index)
-      norm_token<HT, XT, VPT, false>(a, post, pre, t * a.d, y, h, gate + int64_t(g) * a.d, g < 0 || g >= a.gate_rows, red);
+      norm_token<HT, XT, VPT, false>(a, k, post, pre, t * a.d, y, h, gate + int64_t(g) * a.d, g < 0 || g >= a.gate_rows, red);
     else
-      norm_token<HT, XT, VPT, true>(a, post, pre, t * a.d, y, h, gate, false, red);
+      norm_token<HT, XT, VPT, true>(a, k, post, pre, t * a.d, y, h, gate, false, red);
     g = g_next;
   }
 }
