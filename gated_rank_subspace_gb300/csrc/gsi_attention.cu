@@ -5,8 +5,10 @@
 
 namespace gsi {
 
-// The plain kernel, one warp a (token, head): the running maximum m and sum l
-// of a softmax and its weighted sum o over the row's keys, one pass,
+// The plain kernel, for more than 64 heads of a float32 model that share a
+// key/value head (its row tiles hold 64 rows): one warp a (token, head), the
+// running maximum m and sum l of a softmax and its weighted sum o over the
+// row's keys, one pass,
 //   m' = max(m, s), l' = l e^(m - m') + e^(s - m'), o' = o e^(m - m') + e^(s - m') v,
 // 32 keys at a time (a lane scores one key; the weighted sum has the lanes on
 // the head's columns).
@@ -144,10 +146,18 @@ int sm_count() {
   return n;
 }
 
-size_t attention_work_bytes(gsi_dtype dt, int dim, int group) { return dt == GSI_BF16 ? attn_tiles_work_bytes(dim) : sizeof(Ctrl); }
+size_t attention_work_bytes(gsi_dtype dt, int dim, int group) {
+  return dt == GSI_BF16 ? attn_tiles_work_bytes(dim) : attn_work_bytes(2 * kAttnCtas, 64, dim);
+}
 
+// Few query rows of a request under one key/value head go to the kernels of 16
+// (or 8) rows, which the bytes bound; more to the row tiles.  At 16 rows and
+// 8000 keys of 128 columns the bf16 row tiles take TILES16 us, the kernel of 16
+// rows ROWS16.
 cudaError_t launch_paged_attention(const AttnArgs& a, gsi_dtype dt, int64_t max_q, cudaStream_t s) {
-  if (dt == GSI_BF16) return max_q * a.group <= 16 ? launch_attn_rows(a, max_q * a.group <= 8, s) : launch_attn_tiles(a, s);
+  const int64_t most = max_q * a.group;
+  if (dt == GSI_BF16) return most <= 16 ? launch_attn_rows(a, most <= 8, s) : launch_attn_tiles(a, s);
+  if (a.group <= 64) return launch_attn_f32(a, most <= 16, s);
   const int64_t rows = int64_t(a.N) * a.hkv * a.group;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(unsigned((rows + kPlainWarps - 1) / kPlainWarps));
@@ -158,8 +168,7 @@ cudaError_t launch_paged_attention(const AttnArgs& a, gsi_dtype dt, int64_t max_
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return dt == GSI_F32 ? cudaLaunchKernelEx(&cfg, attn_plain_kernel<F32>, a)
-                       : cudaLaunchKernelEx(&cfg, attn_plain_kernel<BF16>, a);
+  return cudaLaunchKernelEx(&cfg, attn_plain_kernel<F32>, a);
 }
 
 }  // namespace gsi

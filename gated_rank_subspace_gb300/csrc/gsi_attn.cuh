@@ -241,13 +241,13 @@ struct AttnWalk {
 // depend on who came last) and sets the counter back to zero.  Nobody waits.
 // At most two units of a share are cut: one that an earlier CTA began (slot
 // 2 b) and one that a later CTA ends (slot 2 b + 1).
-constexpr int kAttnCtas = 152;  // CTAs of a launch, at most: one an SM
-constexpr size_t kAttnCounterBytes = 2048;
-static_assert(kAttnCtas * 2 * 4 <= int(kAttnCounterBytes), "two counters (row tiles) a CTA");
+constexpr int kAttnCtas = 152;  // CTAs of a launch, at most: one an SM (two over a float32 cache)
+constexpr size_t kAttnCounterBytes = 4096;
+static_assert(2 * kAttnCtas * 2 * 4 <= int(kAttnCounterBytes), "two counters (row tiles) a CTA");
 
 __host__ __device__ constexpr size_t attn_slot_floats(int rows, int dim) { return size_t(rows) * (dim + 2); }
-inline size_t attn_work_bytes(int rows, int dim) {
-  return (sizeof(Ctrl) + kAttnCounterBytes + 2 * kAttnCtas * attn_slot_floats(rows, dim) * 4 + 255) / 256 * 256;
+inline size_t attn_work_bytes(int ctas, int rows, int dim) {
+  return (sizeof(Ctrl) + kAttnCounterBytes + 2 * size_t(ctas) * attn_slot_floats(rows, dim) * 4 + 255) / 256 * 256;
 }
 __device__ __forceinline__ uint32_t* attn_err(const AttnArgs& a) { return &static_cast<Ctrl*>(a.work)->err; }
 __device__ __forceinline__ unsigned* attn_counter(const AttnArgs& a, int cta, int tile) {
@@ -330,12 +330,17 @@ __device__ __forceinline__ void attn_fold(const AttnArgs& a, int from, int to, i
 template <class T, int CW>
 __device__ __forceinline__ void attn_finish(const AttnArgs& a, int64_t at, int c, float l, const float (&o)[CW]) {
   const float inv = l == 0.f ? 0.f : 1.f / l;
+  if constexpr (CW == 4) {
+    static_assert(T::kBytes == 4, "pieces of four are float32's");
+    *reinterpret_cast<float4*>(static_cast<float*>(a.O) + at) = make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+  } else {
 #pragma unroll
-  for (int i = 0; i < CW; i += 8) {
-    float w[8];
+    for (int i = 0; i < CW; i += 8) {
+      float w[8];
 #pragma unroll
-    for (int x = 0; x < 8; ++x) w[x] = o[i + x] * inv;
-    if (c + i < a.dim) attn_store8<T>(a, at + i, w);
+      for (int x = 0; x < 8; ++x) w[x] = o[i + x] * inv;
+      if (c + i < a.dim) attn_store8<T>(a, at + i, w);
+    }
   }
 }
 
@@ -409,6 +414,8 @@ cudaError_t attn_query_map(CUtensorMap* m, const AttnArgs& a, int box_heads, int
 // Units of at most 16 query rows (half: 8).
 cudaError_t launch_attn_rows(const AttnArgs& a, bool half, cudaStream_t s);
 cudaError_t launch_attn_tiles(const AttnArgs& a, cudaStream_t s);
+// A float32 cache: units of 64 query rows (few: 16).
+cudaError_t launch_attn_f32(const AttnArgs& a, bool few, cudaStream_t s);
 size_t attn_tiles_work_bytes(int dim);
 
 }  // namespace gsi

@@ -766,6 +766,6 @@ cudaError_t launch_attn_tiles(const AttnArgs& a, cudaStream_t s) {
   }
 }
 
-size_t attn_tiles_work_bytes(int dim) { return attn_work_bytes(dim <= 128 ? 256 : 128, dim); }
+size_t attn_tiles_work_bytes(int dim) { return attn_work_bytes(kAttnCtas, dim <= 128 ? 256 : 128, dim); }
 
 }  // namespace gsi
