@@ -672,13 +672,16 @@ def norm_residual(h: torch.Tensor, y: torch.Tensor = None, post: Norm = None, pr
             _ints("gate_index", gate_index, T)
         elif rows != 1:
             raise ValueError("a gate of several rows needs gate_index")
-    with _on_stream(stream):
-        if h_out is None:
+    if h_out is None:
+        with _on_stream(stream):
             h_out = torch.empty_like(h)
-        if x is None:
+    else:
+        _like("h_out", h_out, (T, d), h.dtype)
+    if x is None:
+        with _on_stream(stream):
             x = torch.empty(T, d, dtype=x_dtype, device=h.device)
-    _like("h_out", h_out, (T, d), h.dtype)
-    _like("x", x, (T, d), x.dtype)
+    else:
+        _like("x", x, (T, d), x.dtype)
     _check(lib().gsi_norm_residual(h.data_ptr(), _dtype_code(h.dtype), None if y is None else y.data_ptr(),
                                    0 if y is None else _dtype_code(y.dtype), T, d, alpha,
                                    None if post is None else ctypes.byref(post.desc(d)),

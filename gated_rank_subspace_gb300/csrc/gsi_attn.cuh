@@ -333,6 +333,18 @@ __device__ __forceinline__ void attn_finish(const AttnArgs& a, int64_t at, int c
   if constexpr (CW == 4) {
     static_assert(T::kBytes == 4, "pieces of four are float32's");
     *reinterpret_cast<float4*>(static_cast<float*>(a.O) + at) = make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+  } else if (CW >= 16 && T::kBytes == 2 && a.dim % 16 == 0 && (reinterpret_cast<uintptr_t>(a.O) & 31) == 0) {
+    // whole sectors: a thread with a row of its own writes 32 bytes at a time
+#pragma unroll
+    for (int i = 0; i + 16 <= CW; i += 16) {
+      uint32_t w[8];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) w[x] = attn_pack(o[i + 2 * x] * inv, o[i + 2 * x + 1] * inv);
+      if (c + i < a.dim)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(static_cast<uint16_t*>(a.O) + at + i),
+                     "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < CW; i += 8) {

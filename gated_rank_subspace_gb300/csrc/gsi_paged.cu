@@ -24,13 +24,24 @@ namespace gsi {
 constexpr int kPlanThreads = 512;
 constexpr int kPlanItems = 8;                          // requests a thread takes of a chunk
 constexpr int kPlanChunk = kPlanThreads * kPlanItems;  // requests whose prefix sums are in shared memory
-constexpr int kPlanTokens = 2048;                      // new tokens a CTA writes, at least
+constexpr int kPlanTokens = 512;                       // new tokens of a CTA, at least
+constexpr int kPlanSmem = (3 * kPlanChunk + 1) * 4;
 
 struct PlanSums {
   long long fresh, pages;
+  unsigned bad;  // GSI_PLAN_ bits, or-ed
 };
 
-// Exclusive prefix over the block's threads of (fresh, pages); *total is the block's sum.
+// What a request adds, or why it cannot be planned.
+__device__ __forceinline__ PlanSums plan_request(const PlanArgs& a, int cached, int fresh) {
+  const int shift = a.page_shift;
+  const long long round = (1ll << shift) - 1, end = (long long)cached + fresh;
+  if (cached < 0 || fresh < 0 || end > 0x7fffffffll) return PlanSums{0, 0, GSI_PLAN_BAD_LENGTH};
+  const long long held = (cached + round) >> shift, want = (end + round) >> shift;
+  return PlanSums{fresh, want - held, want > a.width ? unsigned(GSI_PLAN_TABLE_FULL) : 0u};
+}
+
+// Exclusive prefix over the block's threads; *total is the block's sum.
 __device__ __forceinline__ PlanSums plan_scan(PlanSums v, PlanSums* warp_sums, PlanSums* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   PlanSums inc = v;
@@ -39,49 +50,70 @@ __device__ __forceinline__ PlanSums plan_scan(PlanSums v, PlanSums* warp_sums, P
     const long long f = __shfl_up_sync(0xffffffffu, inc.fresh, o), p = __shfl_up_sync(0xffffffffu, inc.pages, o);
     if (lane >= o) inc.fresh += f, inc.pages += p;
   }
+  inc.bad = __reduce_or_sync(0xffffffffu, v.bad);
   __syncthreads();  // the sums of an earlier call have been read
   if (lane == 31) warp_sums[warp] = inc;
   __syncthreads();
-  PlanSums before{0, 0}, all{0, 0};
+  PlanSums before{0, 0, 0}, all{0, 0, 0};
 #pragma unroll
   for (int w = 0; w < kPlanThreads / 32; ++w) {
     const PlanSums s = warp_sums[w];
     if (w < warp) before.fresh += s.fresh, before.pages += s.pages;
-    all.fresh += s.fresh, all.pages += s.pages;
+    all.fresh += s.fresh, all.pages += s.pages, all.bad |= s.bad;
   }
   *total = all;
-  return PlanSums{before.fresh + inc.fresh - v.fresh, before.pages + inc.pages - v.pages};
+  return PlanSums{before.fresh + inc.fresh - v.fresh, before.pages + inc.pages - v.pages, 0};
 }
 
-__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanArgs a) {
+__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_constant__ PlanArgs a) {
+  extern __shared__ int plan_smem[];
   __shared__ PlanSums s_warp[kPlanThreads / 32];
-  __shared__ int s_start[kPlanChunk + 1];  // S_r of the chunk's requests, and their end
-  __shared__ int s_pages[kPlanChunk];      // A_r
+  int* s_start = plan_smem;                // S_r of the chunk's requests, and their end
+  int* s_pages = s_start + kPlanChunk + 1;  // A_r
+  int* s_cached = s_pages + kPlanChunk;
   pdl_launch_dependents();
   pdl_wait();
   const int tid = threadIdx.x, shift = a.page_shift;
-  const long long page = 1ll << shift;
+  const int round = (1 << shift) - 1;
   const int n_free = __ldcg(a.n_free);
+  const bool one_chunk = a.n_req <= kPlanChunk;
+
+  int c[kPlanItems], f[kPlanItems];
+  auto load = [&](int c0) {
+#pragma unroll
+    for (int i = 0; i < kPlanItems; ++i) {
+      const int r = c0 + tid * kPlanItems + i;
+      c[i] = f[i] = 0;
+      if (r < a.n_req) {
+        c[i] = __ldcg(a.cached + r);
+        f[i] = __ldcg(a.fresh + r);
+      }
+    }
+  };
+  auto sums = [&]() {
+    PlanSums s{0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < kPlanItems; ++i) {
+      const PlanSums q = plan_request(a, c[i], f[i]);
+      s.fresh += q.fresh, s.pages += q.pages, s.bad |= q.bad;
+    }
+    return s;
+  };
 
   // 1. totals and checks, before anything is written
-  PlanSums sum{0, 0};
-  unsigned bad = 0;
-  for (int r = tid; r < a.n_req; r += kPlanThreads) {
-    const long long c = __ldcg(a.cached + r), f = __ldcg(a.fresh + r);
-    if (c < 0 || f < 0 || c + f > 0x7fffffffll) {
-      bad |= GSI_PLAN_BAD_LENGTH;
-    } else {
-      const long long held = (c + page - 1) >> shift, want = (c + f + page - 1) >> shift;
-      if (want > a.width) bad |= GSI_PLAN_TABLE_FULL;
-      sum.fresh += f;
-      sum.pages += want - held;
+  PlanSums all, at;
+  if (one_chunk) {
+    load(0);
+    at = plan_scan(sums(), s_warp, &all);
+  } else {
+    PlanSums mine{0, 0, 0};
+    for (int r = tid; r < a.n_req; r += kPlanThreads) {
+      const PlanSums q = plan_request(a, __ldcg(a.cached + r), __ldcg(a.fresh + r));
+      mine.fresh += q.fresh, mine.pages += q.pages, mine.bad |= q.bad;
     }
+    plan_scan(mine, s_warp, &all);
   }
-  PlanSums all;
-  plan_scan(sum, s_warp, &all);
-  bad = __reduce_or_sync(0xffffffffu, bad);
-  bad = unsigned(__syncthreads_or(bad & GSI_PLAN_BAD_LENGTH) ? GSI_PLAN_BAD_LENGTH : 0) |
-        unsigned(__syncthreads_or(bad & GSI_PLAN_TABLE_FULL) ? GSI_PLAN_TABLE_FULL : 0);
+  unsigned bad = all.bad;
   if (n_free < 0 || n_free > a.capacity || all.pages > n_free) bad |= GSI_PLAN_NO_PAGES;
   if (all.fresh > a.n_tokens) bad |= GSI_PLAN_TOO_MANY_TOKENS;
 
@@ -109,26 +141,14 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanArgs a) {
   }
 
   // 2. the requests, a chunk at a time
-  PlanSums base{0, 0};
+  PlanSums base{0, 0, 0};
   for (int c0 = 0; c0 < a.n_req; c0 += kPlanChunk) {
     const int n = min(kPlanChunk, a.n_req - c0);
-    int f[kPlanItems], p[kPlanItems];
-    PlanSums mine{0, 0};
-#pragma unroll
-    for (int i = 0; i < kPlanItems; ++i) {
-      const int r = tid * kPlanItems + i;
-      f[i] = p[i] = 0;
-      if (r < n) {
-        const int c = __ldcg(a.cached + c0 + r);
-        f[i] = __ldcg(a.fresh + c0 + r);
-        p[i] = int(((long long)c + f[i] + page - 1) >> shift) - int((c + page - 1) >> shift);
-        if (blockIdx.x == 0) a.kv_len[c0 + r] = c + f[i];
-      }
-      mine.fresh += f[i];
-      mine.pages += p[i];
+    PlanSums chunk = all;
+    if (!one_chunk) {
+      load(c0);
+      at = plan_scan(sums(), s_warp, &chunk);
     }
-    PlanSums chunk;
-    PlanSums at = plan_scan(mine, s_warp, &chunk);
     int s = int(base.fresh + at.fresh), q = int(base.pages + at.pages);
 #pragma unroll
     for (int i = 0; i < kPlanItems; ++i) {
@@ -136,10 +156,14 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanArgs a) {
       if (r < n) {
         s_start[r] = s;
         s_pages[r] = q;
-        if (blockIdx.x == 0) a.q_start[c0 + r] = s;
+        s_cached[r] = c[i];
+        if (blockIdx.x == 0) {
+          a.q_start[c0 + r] = s;
+          a.kv_len[c0 + r] = c[i] + f[i];
+        }
       }
       s += f[i];
-      q += p[i];
+      q += ((c[i] + f[i] + round) >> shift) - ((c[i] + round) >> shift);
     }
     const int first = int(base.fresh), end = int(base.fresh + chunk.fresh);
     if (tid == 0) s_start[n] = end;
@@ -150,19 +174,18 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanArgs a) {
         const int mid = (lo + hi) >> 1;
         if (s_start[mid] <= t) lo = mid; else hi = mid;
       }
-      const int r = c0 + lo;
-      const int c = __ldcg(a.cached + r);
-      const int pos = c + t - s_start[lo];
-      const int held = int((c + page - 1) >> shift), j = pos >> shift;
+      const int64_t r = c0 + lo;
+      const int cached = s_cached[lo], pos = cached + t - s_start[lo];
+      const int held = (cached + round) >> shift, j = pos >> shift;
       int id;
       if (j >= held) {
         id = __ldcg(a.free_pages + (n_free - 1 - (s_pages[lo] + j - held)));
-        if ((pos & int(page - 1)) == 0) a.table[r * a.width + j] = id;
+        if ((pos & round) == 0) a.table[r * a.width + j] = id;
       } else {
         id = __ldcg(a.table + r * a.width + j);
       }
-      a.slots[t] = id < 0 ? -1 : (long long)id * page + (pos & int(page - 1));
-      a.token_req[t] = r;
+      a.slots[t] = id < 0 ? -1 : ((long long)id << shift) + (pos & round);
+      a.token_req[t] = int(r);
       a.positions[t] = pos;
     }
     base.fresh += chunk.fresh;
@@ -172,10 +195,13 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanArgs a) {
 }
 
 cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t s) {
-  const int ctas = max(1, min(152, a.n_tokens / kPlanTokens));
+  static const cudaError_t ready =
+      cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlanSmem);
+  if (ready != cudaSuccess) return ready;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas);
+  cfg.gridDim = dim3(max(1, min(sm_count(), a.n_tokens / kPlanTokens)));
   cfg.blockDim = dim3(kPlanThreads);
+  cfg.dynamicSmemBytes = kPlanSmem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
