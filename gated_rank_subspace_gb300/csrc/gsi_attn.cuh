@@ -51,41 +51,122 @@ __device__ __forceinline__ void attn_tiles(const AttnArgs& a, const AttnReq& q, 
   n = max(0, (lim + kt - 1) / kt - t0);
 }
 
-// Cost of a request's units under one head: its tiles, and `extra` more a unit.
-__device__ __forceinline__ long long attn_head_cost(const AttnArgs& a, const AttnReq& q, int ut, int kt, int extra) {
-  long long s = 0;
-  for (int u = 0; u * ut < q.q_len; ++u) {
-    int t0, n;
-    attn_tiles(a, q, u, ut, kt, t0, n);
-    s += max(1, n) + extra;
-  }
-  return s;
-}
-
 // Whole quotient of a by b > 0 (in 32 bits, a fifth of the time, where they suffice).
 __device__ __forceinline__ long long attn_div(long long a, long long b) {
   if (((a | b) >> 31) == 0) return int(a) / int(b);
   return a / b;
 }
 
+// sum of floor((x i + y) / m) for i = 0 .. n - 1, x, y >= 0 (by Euclid's algorithm on x and m).
+__device__ __forceinline__ long long attn_floor_sum(long long n, long long m, long long x, long long y) {
+  long long s = 0;
+  while (n > 0) {
+    if (x >= m) {
+      const long long q = attn_div(x, m);
+      s += (n - 1) * n / 2 * q;
+      x -= q * m;
+    }
+    if (y >= m) {
+      const long long q = attn_div(y, m);
+      s += n * q;
+      y -= q * m;
+    }
+    const long long top = x * n + y;
+    if (top < m) break;
+    n = attn_div(top, m);
+    y = top - n * m;
+    const long long z = m;
+    m = x;
+    x = z;
+  }
+  return s;
+}
+
+// Tiles of the first u units (all of them whole) of a request under one head.
+// Few units are counted one by one (~30 cycles each); for more, in closed form
+// (~300 cycles a sum): unit v ends at the limit base + (v + 1) ut of its last
+// token, and begins, under a window, window - 1 keys before that of its first.
+// (Not inlined, like what calls it below: this runs once a CTA, and then its
+// time is that of fetching its instructions.)
+constexpr int kAttnCount = 64;
+static __device__ __noinline__ long long attn_prefix_tiles(const AttnArgs& a, AttnReq q, int u, int ut, int kt) {
+  const long long n = u;
+  if (u <= kAttnCount) {
+    int tiles = 0;
+#pragma unroll 1
+    for (int v = 0; v < u; ++v) {
+      int t0, c;
+      attn_tiles(a, q, v, ut, kt, t0, c);
+      tiles += max(1, c);
+    }
+    return tiles;
+  }
+  if (!a.causal) return n * max(1, (q.len + kt - 1) / kt);
+  const long long base = q.len - q.q_len;
+  const long long none = base < 0 ? min(n, attn_div(-base, ut)) : 0;  // units that see no key
+  long long s = none + attn_floor_sum(n - none, kt, ut, base + (none + 1) * ut + kt - 1);
+  if (a.window > 0) {
+    const long long first = base + 1 - a.window;  // where unit 0 begins
+    const long long skip = first < 0 ? min(n, attn_div(-first + ut - 1, ut)) : 0;
+    s -= attn_floor_sum(n - skip, kt, ut, first + skip * ut);
+  }
+  return s;
+}
+
+__device__ __forceinline__ int attn_units(const AttnReq& q, int ut) { return q.q_len > 0 ? (q.q_len - 1) / ut + 1 : 0; }
+
+// Tiles of all units of a request under one head.
+__device__ __forceinline__ long long attn_head_tiles(const AttnArgs& a, const AttnReq& q, int ut, int kt) {
+  const int units = attn_units(q, ut);
+  if (units == 0) return 0;
+  int t0, n;
+  attn_tiles(a, q, units - 1, ut, kt, t0, n);  // the last unit may be a part of one
+  return (units > 1 ? attn_prefix_tiles(a, q, units - 1, ut, kt) : 0) + max(1, n);
+}
+
 // A place on the line: `off` tiles into unit u of head h of request r.
 struct AttnPlace {
   AttnReq q;
   int r, h, u;
-  long long per_head, off;
+  long long off;
+  // the beginning of the first request from r_ on that has tokens (there is one)
+  __device__ __forceinline__ void start(const AttnArgs& a, int r_) {
+    for (r = r_;; ++r) {
+      q = attn_request(a, r);
+      if (q.q_len > 0) break;
+    }
+    h = u = 0;
+    off = 0;
+  }
   // `at` tiles behind the first one of request r, whose lengths are q (there are tiles beyond)
-  __device__ __forceinline__ void set(const AttnArgs& a, int r_, const AttnReq& q_, long long at, int ut, int kt, int extra) {
+  __device__ __noinline__ void set(const AttnArgs& a, int r_, AttnReq q_, long long at, int ut, int kt, int extra) {
     r = r_;
     q = q_;
+    long long per_head;
     for (;;) {
-      per_head = attn_head_cost(a, q, ut, kt, extra);
+      per_head = attn_head_tiles(a, q, ut, kt) + (long long)extra * attn_units(q, ut);
       if (at < per_head * a.hkv) break;
       at -= per_head * a.hkv;
       q = attn_request(a, ++r);
     }
     h = int(attn_div(at, per_head));
     off = at - h * per_head;
-    for (u = 0;; ++u) {
+    // the last unit that begins at or before `off`: by bisection to kAttnCount units, then one by one
+    int past = attn_units(q, ut);
+    long long before = 0;
+    for (u = 0; past - u > kAttnCount;) {
+      const int mid = (u + past) >> 1;
+      const long long c = attn_prefix_tiles(a, q, mid, ut, kt) + (long long)extra * mid;
+      if (c <= off) {
+        u = mid;
+        before = c;
+      } else {
+        past = mid;
+      }
+    }
+    off -= before;
+#pragma unroll 1
+    for (;; ++u) {
       int t0, n;
       attn_tiles(a, q, u, ut, kt, t0, n);
       if (off < max(1, n) + extra) break;
@@ -107,70 +188,67 @@ struct AttnShare {
 };
 
 // The share of CTA blockIdx.x and where it begins; all NT threads of the block.
+// Each half of the block goes over the requests, and finds one of the two cuts.
 template <int NT>
 __device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, int ut, int kt, int extra, AttnPlace& begin) {
-  __shared__ long long s_sum[NT / 32], s_cut[2];
-  __shared__ int s_tiles[NT / 32];
+  constexpr int NH = NT / 2, NW = NH / 32;
+  static_assert(NT % 64 == 0, "halves of whole warps");
+  __shared__ long long s_tiles[2 * NW], s_units[2 * NW], s_cut[2];
   __shared__ AttnPlace s_begin;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int r0 = int((long long)a.n_req * tid / NT), r1 = int((long long)a.n_req * (tid + 1) / NT);
-  AttnShare s;
-  s.extra = 0;
-  if (extra > 0) {  // shares of fewer than 4 extra tiles are cut where they fall
-    int tiles = 0;
-    const int enough = 4 * extra * int(gridDim.x);
-    for (int r = r0; r < r1 && tiles < enough; ++r) {
-      const long long c = attn_head_cost(a, attn_request(a, r), ut, kt, 0) * a.hkv;
-      tiles += int(c < enough ? c : enough);
-    }
-    tiles = __reduce_add_sync(0xffffffffu, min(tiles, enough));
-    if (lane == 0) s_tiles[warp] = min(tiles, enough);
-    __syncthreads();
-    tiles = 0;
-#pragma unroll
-    for (int w = 0; w < NT / 32; ++w) tiles += s_tiles[w];
-    if (tiles >= enough) s.extra = extra;
-  }
-  long long mine = 0;
-  AttnReq q{};  // of request r1 - 1
-  for (int r = r0; r < r1; ++r) {
+  const int tid = threadIdx.x, lane = tid & 31, half = tid / NH, warp = (tid >> 5) - half * NW;
+  const int ht = tid - half * NH;
+  const int r0 = int((long long)a.n_req * ht / NH), r1 = int((long long)a.n_req * (ht + 1) / NH);
+  long long tiles = 0, units = 0;
+  AttnReq q{};  // of request r0
+#pragma unroll 1
+  for (int r = r1 - 1; r >= r0; --r) {
     q = attn_request(a, r);
-    mine += attn_head_cost(a, q, ut, kt, s.extra) * a.hkv;
+    tiles += attn_head_tiles(a, q, ut, kt) * a.hkv;
+    units += (long long)attn_units(q, ut) * a.hkv;
   }
-  long long inc = mine;
+  long long it = tiles, iu = units;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += v;
+    const long long x = __shfl_up_sync(0xffffffffu, it, o), y = __shfl_up_sync(0xffffffffu, iu, o);
+    if (lane >= o) it += x, iu += y;
   }
-  if (lane == 31) s_sum[warp] = inc;
+  if (lane == 31) {
+    s_tiles[half * NW + warp] = it;
+    s_units[half * NW + warp] = iu;
+  }
   __syncthreads();
-  long long before = inc - mine, total = 0;
+  it -= tiles;
+  iu -= units;
+  long long total = 0, total_units = 0;
 #pragma unroll
-  for (int w = 0; w < NT / 32; ++w) {
-    if (w < warp) before += s_sum[w];
-    total += s_sum[w];
+  for (int w = 0; w < NW; ++w) {
+    if (w < warp) it += s_tiles[half * NW + w], iu += s_units[half * NW + w];
+    total += s_tiles[w];
+    total_units += s_units[w];
   }
+  AttnShare s;
+  s.extra = total >= 4ll * extra * gridDim.x ? extra : 0;  // shares of fewer than 4 extra tiles are cut where they fall
+  total += s.extra * total_units;
+  const long long before = it + s.extra * iu, mine = tiles + s.extra * units;
   s.total = total;
   s.grid = int(total < (long long)gridDim.x ? total : (long long)gridDim.x);
   s.pos = s.end = 0;
   const bool some = int(blockIdx.x) < s.grid;
   if (some) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const long long cut = attn_div(total * (blockIdx.x + i), s.grid);
-      if (before <= cut && cut < before + mine) {
-        long long at = cut - before;
-        if (r1 - r0 > 1) q = attn_request(a, r0);
-        AttnPlace p;
-        if (i == 0 || s.extra > 0) p.set(a, r0, q, at, ut, kt, s.extra);
-        const int move = s.extra > 0 ? p.snap(a, ut, kt, s.extra) : 0;
-        s_cut[i] = cut + move;
-        if (i == 0) {
-          if (move > 0 && cut + move < total) p.set(a, r0, r1 - r0 > 1 ? attn_request(a, r0) : q, at + move, ut, kt, s.extra);
-          if (move < 0) p.off += move;
-          s_begin = p;
-        }
+    const long long cut = attn_div(total * (blockIdx.x + half), s.grid);
+    if (before <= cut && cut < before + mine) {
+      AttnPlace p;
+      int move = 0;
+      if (half == 0 || s.extra > 0) {
+        p.set(a, r0, q, cut - before, ut, kt, s.extra);
+        if (s.extra > 0) move = p.snap(a, ut, kt, s.extra);
+      }
+      s_cut[half] = cut + move;
+      if (half == 0) {
+        // (a cut at a unit's end is the next one's beginning, or that of the next head or request)
+        if (move > 0 && cut + move < total) p.set(a, r0, q, cut - before + move, ut, kt, s.extra);
+        if (move < 0) p.off += move;
+        s_begin = p;
       }
     }
   }
@@ -220,7 +298,7 @@ struct AttnWalk {
         p.u = 0;
         ++p.h;
       } else {
-        p.set(a, p.r + 1, attn_request(a, p.r + 1), 0, ut, kt, s.extra);
+        p.start(a, p.r + 1);
       }
     }
     return true;
@@ -379,7 +457,7 @@ __device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnSeg& g, i
 // with it is what the definition gives.  Tiles [t0 + a, t0 + b) of kt keys;
 // the value of column c for a row that sees [lo, lim).
 template <class T>
-__device__ __noinline__ float attn_nonfinite(const AttnArgs& a, const AttnSeg& g, int kt, int lo, int lim, int lo_all,
+static __device__ __noinline__ float attn_nonfinite(const AttnArgs& a, const AttnSeg& g, int kt, int lo, int lim, int lo_all,
                                              int lim_all, int c, float o) {
   for (int t = g.t0 + g.a; t < g.t0 + g.b; ++t) {
     if (t * kt >= lo_all && (t + 1) * kt <= lim_all) continue;  // every row sees this tile: nothing was taken out
