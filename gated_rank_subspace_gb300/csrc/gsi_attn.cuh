@@ -57,9 +57,19 @@ __device__ __forceinline__ long long attn_div(long long a, long long b) {
   return a / b;
 }
 
-// sum of floor((x i + y) / m) for i = 0 .. n - 1, x, y >= 0 (by Euclid's algorithm on x and m).
-__device__ __forceinline__ long long attn_floor_sum(long long n, long long m, long long x, long long y) {
-  long long s = 0;
+// sum of floor((x i + y) / m) for i = 0 .. n - 1; x > 0, y >= 0, m a power of
+// two.  Where x is one too (as many heads a group) in a few steps, else by
+// Euclid's algorithm on x and m.
+__device__ __forceinline__ long long attn_floor_sum(long long n, int m_, int x_, long long y) {
+  if ((x_ & (x_ - 1)) == 0) {
+    const int ms = __ffs(m_) - 1, xs = __ffs(x_) - 1;
+    if (xs >= ms) return n * (y >> ms) + ((n * (n - 1) / 2) << (xs - ms));
+    // floor((i + z) / 2^d) from z on
+    const int d = ms - xs;
+    const long long z = y >> xs, a = (n + z) >> d, b = z >> d;
+    return ((a * (a - 1) / 2) << d) + a * (n + z - (a << d)) - ((b * (b - 1) / 2) << d) - b * (z - (b << d));
+  }
+  long long s = 0, m = m_, x = x_;
   while (n > 0) {
     if (x >= m) {
       const long long q = attn_div(x, m);
@@ -83,12 +93,12 @@ __device__ __forceinline__ long long attn_floor_sum(long long n, long long m, lo
 }
 
 // Tiles of the first u units (all of them whole) of a request under one head.
-// Few units are counted one by one (~30 cycles each); for more, in closed form
-// (~300 cycles a sum): unit v ends at the limit base + (v + 1) ut of its last
-// token, and begins, under a window, window - 1 keys before that of its first.
-// (Not inlined, like what calls it below: this runs once a CTA, and then its
-// time is that of fetching its instructions.)
-constexpr int kAttnCount = 64;
+// Two are counted one by one (~200 cycles each, a chain of dependent integer
+// steps); more in closed form: unit v ends at the limit base + (v + 1) ut of its
+// last token, and begins, under a window, window - 1 keys before that of its
+// first.  (Not inlined: this runs once a CTA, and then its time is that of
+// fetching its instructions.)
+constexpr int kAttnCount = 2;
 static __device__ __noinline__ long long attn_prefix_tiles(const AttnArgs& a, AttnReq q, int u, int ut, int kt) {
   const long long n = u;
   if (u <= kAttnCount) {
@@ -138,11 +148,14 @@ struct AttnPlace {
     h = u = 0;
     off = 0;
   }
-  // `at` tiles behind the first one of request r, whose lengths are q (there are tiles beyond)
+  // `at` tiles behind the first one of request r, whose lengths are q (there are tiles beyond); the 32 lanes of a warp,
+  // alike: each counts a unit
   __device__ __noinline__ void set(const AttnArgs& a, int r_, AttnReq q_, long long at, int ut, int kt, int extra) {
+    const int lane = threadIdx.x & 31;
     r = r_;
     q = q_;
     long long per_head;
+#pragma unroll 1
     for (;;) {
       per_head = attn_head_tiles(a, q, ut, kt) + (long long)extra * attn_units(q, ut);
       if (at < per_head * a.hkv) break;
@@ -151,10 +164,13 @@ struct AttnPlace {
     }
     h = int(attn_div(at, per_head));
     off = at - h * per_head;
-    // the last unit that begins at or before `off`: by bisection to kAttnCount units, then one by one
-    int past = attn_units(q, ut);
+    // the last unit that begins at or before `off`: by bisection to a warp's units, then a lane each
+    const int units = attn_units(q, ut);
+    int past = units;
     long long before = 0;
-    for (u = 0; past - u > kAttnCount;) {
+    u = 0;
+#pragma unroll 1
+    while (past - u > 32) {
       const int mid = (u + past) >> 1;
       const long long c = attn_prefix_tiles(a, q, mid, ut, kt) + (long long)extra * mid;
       if (c <= off) {
@@ -165,12 +181,31 @@ struct AttnPlace {
       }
     }
     off -= before;
-#pragma unroll 1
-    for (;; ++u) {
-      int t0, n;
-      attn_tiles(a, q, u, ut, kt, t0, n);
-      if (off < max(1, n) + extra) break;
-      off -= max(1, n) + extra;
+    int t0, n = 0, c = 0;
+    if (u + lane < units) {
+      attn_tiles(a, q, u + lane, ut, kt, t0, n);
+      c = max(1, n) + extra;
+    }
+    long long inc = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    const int skip = __popc(__ballot_sync(0xffffffffu, u + lane < units && inc <= off));
+    if (skip > 0) off -= __shfl_sync(0xffffffffu, inc, skip - 1);
+    u += skip;
+  }
+  // the beginning of the next unit (there is one)
+  __device__ __forceinline__ void next_unit(const AttnArgs& a, int ut) {
+    off = 0;
+    if ((u + 1) * ut < q.q_len) {
+      ++u;
+    } else if (h + 1 < a.hkv) {
+      u = 0;
+      ++h;
+    } else {
+      start(a, r + 1);
     }
   }
   // tiles by which a cut here is moved
@@ -236,20 +271,23 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, int ut, int k
   const bool some = int(blockIdx.x) < s.grid;
   if (some) {
     const long long cut = attn_div(total * (blockIdx.x + half), s.grid);
-    if (before <= cut && cut < before + mine) {
+    const unsigned hit = __ballot_sync(0xffffffffu, before <= cut && cut < before + mine);
+    if (hit && (half == 0 || s.extra > 0)) {
+      const int from = __ffs(hit) - 1;
+      q.q0 = __shfl_sync(0xffffffffu, q.q0, from);
+      q.q_len = __shfl_sync(0xffffffffu, q.q_len, from);
+      q.len = __shfl_sync(0xffffffffu, q.len, from);
       AttnPlace p;
-      int move = 0;
-      if (half == 0 || s.extra > 0) {
-        p.set(a, r0, q, cut - before, ut, kt, s.extra);
-        if (s.extra > 0) move = p.snap(a, ut, kt, s.extra);
-      }
-      s_cut[half] = cut + move;
+      p.set(a, __shfl_sync(0xffffffffu, r0, from), q, __shfl_sync(0xffffffffu, cut - before, from), ut, kt, s.extra);
+      const int move = s.extra > 0 ? p.snap(a, ut, kt, s.extra) : 0;
       if (half == 0) {
-        // (a cut at a unit's end is the next one's beginning, or that of the next head or request)
-        if (move > 0 && cut + move < total) p.set(a, r0, q, cut - before + move, ut, kt, s.extra);
+        if (move > 0 && cut + move < total) p.next_unit(a, ut);
         if (move < 0) p.off += move;
-        s_begin = p;
+        if (lane == 0) s_begin = p;
       }
+      if (lane == 0) s_cut[half] = cut + move;
+    } else if (hit && lane == 0) {
+      s_cut[half] = cut;
     }
   }
   __syncthreads();
@@ -290,17 +328,7 @@ struct AttnWalk {
     g.b = min(g.n, max(0, int(p.off + take) - s.extra));
     s.pos += take;
     p.off += take;
-    if (p.off == cost && s.pos < s.end) {
-      p.off = 0;
-      if ((p.u + 1) * ut < p.q.q_len) {
-        ++p.u;
-      } else if (p.h + 1 < a.hkv) {
-        p.u = 0;
-        ++p.h;
-      } else {
-        p.start(a, p.r + 1);
-      }
-    }
+    if (p.off == cost && s.pos < s.end) p.next_unit(a, ut);
     return true;
   }
   // The CTAs that hold parts of a unit: the cuts inside it, beyond what is moved to its ends, are those of the CTAs
