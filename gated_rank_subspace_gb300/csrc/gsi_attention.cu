@@ -150,13 +150,14 @@ size_t attention_work_bytes(gsi_dtype dt, int dim, int group) {
   return dt == GSI_BF16 ? attn_tiles_work_bytes(dim) : attn_work_bytes(2 * kAttnCtas, 64, dim);
 }
 
-// Few query rows of a request under one key/value head go to the kernels of 16
-// (or 8) rows, which the bytes bound; more to the row tiles.  At 16 rows and
-// 8000 keys of 128 columns the bf16 row tiles take TILES16 us, the kernel of 16
-// rows ROWS16.
+// Few query rows of a request under one key/value head go to the kernels of 8
+// (float32: 16) rows, which the bytes bound; more to the row tiles.  Both sides,
+// us: bf16, 8 heads that share one of 8 key/value heads of 128 columns, 2000 keys
+// 14.4 (row tiles 14.8), 8 requests of 8000 keys 41 (44); 16 heads 19 (16) and 53
+// (45).  float32, 16 rows over 2000 keys of 8 x 64: 31 (44); 32 rows 43 (47).
 cudaError_t launch_paged_attention(const AttnArgs& a, gsi_dtype dt, int64_t max_q, cudaStream_t s) {
   const int64_t most = max_q * a.group;
-  if (dt == GSI_BF16) return most <= 16 ? launch_attn_rows(a, most <= 8, s) : launch_attn_tiles(a, s);
+  if (dt == GSI_BF16) return most <= 8 ? launch_attn_rows(a, s) : launch_attn_tiles(a, s);
   if (a.group <= 64) return launch_attn_f32(a, most <= 16, s);
   const int64_t rows = int64_t(a.N) * a.hkv * a.group;
   cudaLaunchConfig_t cfg{};

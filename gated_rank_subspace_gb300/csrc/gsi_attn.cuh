@@ -467,9 +467,8 @@ template <class T, bool kRowMajor, int CW>
 __device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnSeg& g, int b0, int b1, int tiles, int tile,
                                           int rows, int n_rows, int tok0, int tid, int nt) {
   const int per = (a.dim + CW - 1) / CW;
-  for (int e = tid; e < (kRowMajor ? n_rows : rows) * per; e += nt) {
-    const int row = kRowMajor ? e / per : e % rows, c = (kRowMajor ? e % per : e / rows) * CW;
-    if (row >= n_rows) continue;
+  for (int e = tid; e < n_rows * per; e += nt) {
+    const int row = kRowMajor ? e / per : e % n_rows, c = (kRowMajor ? e % per : e / n_rows) * CW;
     float m = -INFINITY, l = 0.f, o[CW];
 #pragma unroll
     for (int i = 0; i < CW; ++i) o[i] = 0.f;
@@ -529,8 +528,8 @@ inline cudaError_t attn_prepare_kernel(K kern, size_t smem, int threads, int reg
 // Map of the query rows: (column, head, token) boxes of 64 x box_heads x box_tokens.
 cudaError_t attn_query_map(CUtensorMap* m, const AttnArgs& a, int box_heads, int box_tokens);
 
-// Units of at most 16 query rows (half: 8).
-cudaError_t launch_attn_rows(const AttnArgs& a, bool half, cudaStream_t s);
+// Units of at most 8 query rows.
+cudaError_t launch_attn_rows(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_attn_tiles(const AttnArgs& a, cudaStream_t s);
 // A float32 cache: units of 64 query rows (few: 16).
 cudaError_t launch_attn_f32(const AttnArgs& a, bool few, cudaStream_t s);

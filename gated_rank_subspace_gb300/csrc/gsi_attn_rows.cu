@@ -1,14 +1,18 @@
-// Attention of few query rows (decode): all rows of a unit in one tensor-core
-// tile of 8 or 16 rows, the keys and values streamed once.
+// Attention of few query rows (decode): a unit's at most 8 rows in one
+// tensor-core tile, the keys and values streamed once.
 
 #include "gsi_attn.cuh"
 
 namespace gsi {
 
-// With G = group query heads a key/value head and ut = floor(R / G) tokens a
-// unit, S = Q K^T and O = P V have at most R = 8 or 16 rows: 16 FLOP a byte of
-// cache at most, far below what the warp-level tensor products sustain, so the
-// bytes bound the kernel and its work is to keep them coming.  One CTA an SM;
+// With G = group query heads a key/value head and ut = floor(8 / G) tokens a
+// unit, S = Q K^T and O = P V have at most 8 rows: 8 FLOP a byte of cache, far
+// below what the warp-level tensor products sustain, so the bytes bound the
+// kernel and its work is to keep them coming (16 requests of up to 8191 keys, 40
+// x 128: 247 us, 6.2 TB/s; 260001 keys of 8 x 128: 165 us, 6.45 TB/s).  More
+// rows go to the row tiles: a form of this kernel with all 16 rows of a fragment
+// was slower than they are from 2000 keys on (19 against 16 us for 16 heads that
+// share one of 8 key/value heads, 53 against 45 us at 8 x 8000 keys).  One CTA an SM;
 // copy warps keep a ring of 192 KB filled (64 or 128 keys and their values a stage,
 // one TMA box a page and 64 columns, each lane issuing its own box); eight warps
 // take every stage, one to each 16 keys with a softmax of its own (running
@@ -18,9 +22,8 @@ namespace gsi {
 // them, which both form the scores and each half of the output's columns.  The
 // warps' parts are joined when the CTA's part of a unit ends.  The scores'
 // fragment of m16n8k16 is the next product's left operand as it stands, so P
-// never leaves the registers.  Up to 8 rows the lower half of the fragments is
-// neither kept nor scaled.
-template <int NS, bool HALF>  // 64-column slabs of a row; at most 8 rows
+// never leaves the registers.
+template <int NS>  // 64-column slabs of a row
 struct RowsCfg {
   static constexpr int kWarps = 8;                       // compute warps
   static constexpr int kKeyWarps = NS <= 2 ? 8 : 4;      // 16 keys of a stage each
@@ -28,12 +31,12 @@ struct RowsCfg {
   static constexpr int kKt = 16 * kKeyWarps;             // keys a stage
   // three warpgroups: the copy warps' hands registers to the others
   static constexpr int kThreads = 384;
-  static constexpr int kRows = HALF ? 8 : 16;
+  static constexpr int kRows = 8, kShared = 16;          // query rows; output rows in shared memory
   static constexpr int kSlab = kKt * 128;                // bytes
   static constexpr int kStage = 2 * NS * kSlab;          // K slabs, then V slabs
   static constexpr int kStages = 196608 / kStage;        // 192 KB
   static constexpr int kDim = NS * 64;
-  static constexpr size_t kSmem = 1024 + size_t(kStages) * kStage + 16 * kDim * 4 + kKeyWarps * 32 * 4 + 2 * kStages * 8 + 16;
+  static constexpr size_t kSmem = 1024 + size_t(kStages) * kStage + kShared * kDim * 4 + kKeyWarps * 32 * 4 + 2 * kStages * 8 + 16;
 };
 
 __device__ __forceinline__ void rows_ldsm(uint32_t addr, uint32_t (&r)[4]) {
@@ -46,19 +49,12 @@ __device__ __forceinline__ void rows_ldsm_t(uint32_t addr, uint32_t (&r)[4]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr));
 }
-// c += a b; with 8 rows only the upper half (c[0], c[1] from a[0], a[2]).
-template <int NC>
-__device__ __forceinline__ void rows_mma(float (&c)[NC], const uint32_t (&a)[NC], uint32_t b0, uint32_t b1) {
-  if constexpr (NC == 4) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  } else {
-    float x, y;
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %8, %5, %8}, {%6, %7}, {%0, %1, %9, %9};"
-        : "+f"(c[0]), "+f"(c[1]), "=f"(x), "=f"(y)
-        : "r"(a[0]), "r"(a[1]), "r"(b0), "r"(b1), "r"(0u), "f"(0.f));
-  }
+// c += a b, the upper 8 rows of the 16 (the lower ones are zeros that go nowhere).
+__device__ __forceinline__ void rows_mma(float (&c)[2], const uint32_t (&a)[2], uint32_t b0, uint32_t b1) {
+  float x, y;
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %8, %5, %8}, {%6, %7}, {%0, %1, %9, %9};"
+      : "+f"(c[0]), "+f"(c[1]), "=f"(x), "=f"(y)
+      : "r"(a[0]), "r"(a[1]), "r"(b0), "r"(b1), "r"(0u), "f"(0.f));
 }
 // The compute warps only.
 template <int N>
@@ -77,17 +73,17 @@ __device__ __forceinline__ uint32_t rows_clean(uint32_t v, int j, int lo, int li
   return v & keep;
 }
 
-template <int NS, bool HALF>
-__global__ void __launch_bounds__(RowsCfg<NS, HALF>::kThreads, 1)
+template <int NS>
+__global__ void __launch_bounds__(RowsCfg<NS>::kThreads, 1)
     attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                      const __grid_constant__ AttnArgs a) {
-  using C = RowsCfg<NS, HALF>;
-  constexpr int NW = C::kWarps, NC = HALF ? 2 : 4, NY = NC / 2;  // values of a fragment a lane keeps; its rows
+  using C = RowsCfg<NS>;
+  constexpr int NW = C::kWarps;
   constexpr int KW = C::kKeyWarps, NO = 8 * NS / C::kColWarps;  // 8-column pieces of the output a warp holds
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* s_o = reinterpret_cast<float*>(ring + size_t(C::kStages) * C::kStage);  // [16][kDim]
-  float* s_ml = s_o + 16 * C::kDim;                                            // [keys' warp][m: 16, l: 16]
+  float* s_ml = s_o + C::kShared * C::kDim;                                            // [keys' warp][m: 16, l: 16]
   uint64_t* full = reinterpret_cast<uint64_t*>(s_ml + KW * 32);
   uint64_t* empty = full + C::kStages;
   int* s_flag = reinterpret_cast<int*>(empty + C::kStages);
@@ -167,37 +163,25 @@ __global__ void __launch_bounds__(RowsCfg<NS, HALF>::kThreads, 1)
   bool ok = true;
   while (walk.next(a, g)) {  // after a wait that gave up too: the warps meet at barriers
     const int tok0 = g.u * ut, n_tok = min(ut, g.q.q_len - tok0), n_rows = n_tok * a.group;
-    int lim[NY], lo[NY];
-    uint32_t q[4 * NS][NC];
+    uint32_t q[4 * NS][2];
+    const int tok = r0 / a.group;
+    const bool there = r0 < n_rows;
+    const int lim = there ? attn_lim(a, g.q, tok0 + tok) : 0, lo = attn_lo(a, lim);
+    const uint16_t* src = static_cast<const uint16_t*>(a.Q) + int64_t(g.q.q0 + tok0 + tok) * a.q_stride +
+                          int64_t(g.h * a.group + r0 - tok * a.group) * a.dim;
 #pragma unroll
-    for (int i = 0; i < NY; ++i) {
-      const int row = r0 + 8 * i, tok = row / a.group;
-      const bool there = row < n_rows;
-      lim[i] = there ? attn_lim(a, g.q, tok0 + tok) : 0;
-      lo[i] = attn_lo(a, lim[i]);
-      const uint16_t* src = static_cast<const uint16_t*>(a.Q) + int64_t(g.q.q0 + tok0 + tok) * a.q_stride +
-                            int64_t(g.h * a.group + row - tok * a.group) * a.dim;
+    for (int k = 0; k < 4 * NS; ++k)
 #pragma unroll
-      for (int k = 0; k < 4 * NS; ++k)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int c = k * 16 + x * 8 + c0;
-          q[k][NY * x + i] = there && c < a.dim ? __ldcg(reinterpret_cast<const uint32_t*>(src + c)) : 0u;
-        }
-    }
+      for (int x = 0; x < 2; ++x) {
+        const int c = k * 16 + x * 8 + c0;
+        q[k][x] = there && c < a.dim ? __ldcg(reinterpret_cast<const uint32_t*>(src + c)) : 0u;
+      }
     const int lim_all = attn_lim(a, g.q, tok0 + n_tok - 1), lim_min = attn_lim(a, g.q, tok0);  // last and first token's
     const int lo_all = attn_lo(a, lim_min), lo_max = attn_lo(a, lim_all);
-    float m[NY], l[NY];
+    float m = -INFINITY, l = 0.f;
+    float o[NO][2];
 #pragma unroll
-    for (int y = 0; y < NY; ++y) {
-      m[y] = -INFINITY;
-      l[y] = 0.f;
-    }
-    float o[NO][NC];
-#pragma unroll
-    for (int n = 0; n < NO; ++n)
-#pragma unroll
-      for (int x = 0; x < NC; ++x) o[n][x] = 0.f;
+    for (int n = 0; n < NO; ++n) o[n][0] = o[n][1] = 0.f;
     bool found = false;
 
     for (int i = g.a; i < g.b; ++i, ++it) {
@@ -209,9 +193,9 @@ __global__ void __launch_bounds__(RowsCfg<NS, HALF>::kThreads, 1)
       const uint32_t kb = sa(ring + size_t(s) * C::kStage), vb = kb + NS * C::kSlab;
       // scores of this warp's 16 keys, in two chains of products; lane l addresses row l % 8 (+ 8 in lanes 16..31) of
       // the fragment
-      float sc[2][NC];
+      float sc[2][2];
       {
-        float part[2][2][NC] = {};
+        float part[2][2][2] = {};
         const int kr = kg * 16 + (lane & 7) + ((lane >> 4) << 3);
         const uint32_t base = kb + kr * 128;
         const int ch = (lane >> 3) & 1;
@@ -219,58 +203,44 @@ __global__ void __launch_bounds__(RowsCfg<NS, HALF>::kThreads, 1)
         for (int k = 0; k < 4 * NS; ++k) {
           uint32_t b[4];
           rows_ldsm(base + (k >> 2) * C::kSlab + ((((k & 3) * 2 + ch) ^ (kr & 7)) << 4), b);
-          rows_mma<NC>(part[k & 1][0], q[k], b[0], b[1]);
-          rows_mma<NC>(part[k & 1][1], q[k], b[2], b[3]);
+          rows_mma(part[k & 1][0], q[k], b[0], b[1]);
+          rows_mma(part[k & 1][1], q[k], b[2], b[3]);
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
-          for (int y = 0; y < NC; ++y) sc[x][y] = (part[0][x][y] + part[1][x][y]) * sl;
+          for (int y = 0; y < 2; ++y) sc[x][y] = (part[0][x][y] + part[1][x][y]) * sl;
       }
       const int j0 = tile + kg * 16 + c0;
       if (partial) {
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
-          for (int y = 0; y < NC; ++y) {
-            const int j = j0 + 8 * x + (y & 1);
-            if (j < lo[y >> 1] || j >= lim[y >> 1]) sc[x][y] = -INFINITY;
+          for (int y = 0; y < 2; ++y) {
+            const int j = j0 + 8 * x + y;
+            if (j < lo || j >= lim) sc[x][y] = -INFINITY;
           }
       }
-      float f[NY];
-      bool scale = false;
-#pragma unroll
-      for (int y = 0; y < NY; ++y) {
-        float mx = fmaxf(fmaxf(sc[0][2 * y], sc[0][2 * y + 1]), fmaxf(sc[1][2 * y], sc[1][2 * y + 1]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        mx = fmaxf(mx, m[y]);
-        f[y] = attn_scale(m[y], mx);
-        scale |= f[y] != 1.f;
-        m[y] = mx;
-        const float to = mx == -INFINITY ? 0.f : mx;
-        float sum = 0.f;
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            sc[x][2 * y + z] = ex2(sc[x][2 * y + z] - to);
-            sum += sc[x][2 * y + z];
-          }
-        l[y] = l[y] * f[y] + sum;  // this lane's keys; the lanes of a row are added at the end
-      }
-      if (__any_sync(0xffffffffu, scale)) {
-#pragma unroll
-        for (int n = 0; n < NO; ++n)
-#pragma unroll
-          for (int x = 0; x < NC; ++x) o[n][x] *= f[x >> 1];
-      }
-      // the weights enter the second product as bf16: 2^-8 of each at most, what rounding to the cache's type costs
-      uint32_t p[NC];
+      float mx = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      mx = fmaxf(mx, m);
+      const float f = attn_scale(m, mx), to = mx == -INFINITY ? 0.f : mx;
+      m = mx;
 #pragma unroll
       for (int x = 0; x < 2; ++x)
 #pragma unroll
-        for (int y = 0; y < NY; ++y) p[NY * x + y] = attn_pack(sc[x][2 * y], sc[x][2 * y + 1]);
+        for (int y = 0; y < 2; ++y) sc[x][y] = ex2(sc[x][y] - to);
+      l = l * f + ((sc[0][0] + sc[0][1]) + (sc[1][0] + sc[1][1]));  // this lane's keys; the lanes of a row are added at the end
+      if (__any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll
+        for (int n = 0; n < NO; ++n) {
+          o[n][0] *= f;
+          o[n][1] *= f;
+        }
+      }
+      // the weights enter the second product as bf16: 2^-8 of each at most, what rounding to the cache's type costs
+      const uint32_t p[2] = {attn_pack(sc[0][0], sc[0][1]), attn_pack(sc[1][0], sc[1][1])};
       {
         const int vr = kg * 16 + (lane & 15);
         const uint32_t base = vb + vr * 128;
@@ -283,8 +253,8 @@ __global__ void __launch_bounds__(RowsCfg<NS, HALF>::kThreads, 1)
 #pragma unroll
             for (int x = 0; x < 4; ++x) b[x] = rows_clean(b[x], j0 + 8 * (x & 1), lo_all, lim_all, found);
           }
-          rows_mma<NC>(o[2 * n], p, b[0], b[1]);
-          rows_mma<NC>(o[2 * n + 1], p, b[2], b[3]);
+          rows_mma(o[2 * n], p, b[0], b[1]);
+          rows_mma(o[2 * n + 1], p, b[2], b[3]);
         }
       }
       __syncwarp();
@@ -294,51 +264,41 @@ __global__ void __launch_bounds__(RowsCfg<NS, HALF>::kThreads, 1)
     // ---- the warps' parts of the segment: common maximum, one sum.  The shared rows hold 16 / n_rows copies of the
     // output; in each round the warps of that many 16 keys add to a copy each, in their order, and the
     // copies are added at the end.
-#pragma unroll
-    for (int y = 0; y < NY; ++y) {
-      l[y] += __shfl_xor_sync(0xffffffffu, l[y], 1);
-      l[y] += __shfl_xor_sync(0xffffffffu, l[y], 2);
-      if (dh == 0 && (lane & 3) == 0) {
-        s_ml[kg * 32 + r0 + 8 * y] = m[y];
-        s_ml[kg * 32 + 16 + r0 + 8 * y] = l[y];
-      }
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    if (dh == 0 && (lane & 3) == 0) {
+      s_ml[kg * 32 + r0] = m;
+      s_ml[kg * 32 + 16 + r0] = l;
     }
     if (found) s_flag[1] = 1;
     rows_sync<NW * 32>();
     const bool any = s_flag[1] != 0;
+    float mx = -INFINITY;
 #pragma unroll
-    for (int y = 0; y < NY; ++y) {
-      float mx = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < KW; ++w) mx = fmaxf(mx, s_ml[w * 32 + r0 + 8 * y]);
-      m[y] = attn_scale(m[y], mx);  // this warp's factor
-    }
-    const int copies = min(KW, 16 / n_rows), rounds = (KW + copies - 1) / copies;
+    for (int w = 0; w < KW; ++w) mx = fmaxf(mx, s_ml[w * 32 + r0]);
+    const float mine = attn_scale(m, mx);  // this warp's factor
+    const int copies = min(KW, C::kShared / n_rows), rounds = (KW + copies - 1) / copies;
     for (int round = 0; round < rounds; ++round) {
-      if (kg / copies == round) {
+      if (kg / copies == round && r0 < n_rows) {
+        float* row = s_o + ((kg % copies) * n_rows + r0) * C::kDim + dh * (NO * 8);
 #pragma unroll
-        for (int y = 0; y < NY; ++y)
-          if (r0 + 8 * y < n_rows) {
-            float* row = s_o + ((kg % copies) * n_rows + r0 + 8 * y) * C::kDim + dh * (NO * 8);
-#pragma unroll
-            for (int n = 0; n < NO; ++n) {
-              float2* dst = reinterpret_cast<float2*>(row + n * 8 + c0);
-              float2 v = make_float2(o[n][2 * y] * m[y], o[n][2 * y + 1] * m[y]);
-              if (round > 0) {
-                const float2 u = *dst;
-                v.x += u.x;
-                v.y += u.y;
-              }
-              *dst = v;
-            }
+        for (int n = 0; n < NO; ++n) {
+          float2* dst = reinterpret_cast<float2*>(row + n * 8 + c0);
+          float2 v = make_float2(o[n][0] * mine, o[n][1] * mine);
+          if (round > 0) {
+            const float2 u = *dst;
+            v.x += u.x;
+            v.y += u.y;
           }
+          *dst = v;
+        }
       }
       rows_sync<NW * 32>();
     }
     const bool whole = g.a == 0 && g.b == g.n;
     int b0, b1;
     walk.parts(g, b0, b1);
-    float* part = attn_part(a, 2 * int(blockIdx.x) + (int(blockIdx.x) == b0), 1, 0, 16);
+    float* part = attn_part(a, 2 * int(blockIdx.x) + (int(blockIdx.x) == b0), 1, 0, C::kRows);
     const int vec = a.dim / 8;
     for (int e = tid; e < n_rows * vec; e += NW * 32) {
       const int row = e / vec, c = (e - row * vec) * 8;
@@ -361,11 +321,11 @@ __global__ void __launch_bounds__(RowsCfg<NS, HALF>::kThreads, 1)
       if (whole) {
         attn_finish<BF16, 8>(a, attn_out_row(a, g, tok0, row) * a.dim + c, c, sum, v);
       } else {
-        *attn_piece<true>(part, 16, a.dim, row, c) = make_float4(v[0], v[1], v[2], v[3]);
-        *attn_piece<true>(part, 16, a.dim, row, c + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        *attn_piece<true>(part, C::kRows, a.dim, row, c) = make_float4(v[0], v[1], v[2], v[3]);
+        *attn_piece<true>(part, C::kRows, a.dim, row, c + 4) = make_float4(v[4], v[5], v[6], v[7]);
         if (c == 0) {
           part[row] = mx;
-          part[16 + row] = sum;
+          part[C::kRows + row] = sum;
         }
       }
     }
@@ -381,7 +341,7 @@ __global__ void __launch_bounds__(RowsCfg<NS, HALF>::kThreads, 1)
       rows_sync<NW * 32>();
       if (s_flag[0]) {
         __threadfence();
-        attn_join<BF16, true, 8>(a, g, b0, b1, 1, 0, 16, n_rows, tok0, tid, NW * 32);
+        attn_join<BF16, true, 8>(a, g, b0, b1, 1, 0, C::kRows, n_rows, tok0, tid, NW * 32);
       }
     }
     if (tid == 0) s_flag[1] = 0;
@@ -389,16 +349,16 @@ __global__ void __launch_bounds__(RowsCfg<NS, HALF>::kThreads, 1)
   }
 }
 
-template <int NS, bool HALF>
+template <int NS>
 static cudaError_t launch_rows(const AttnArgs& a, cudaStream_t s) {
-  using C = RowsCfg<NS, HALF>;
+  using C = RowsCfg<NS>;
   static_assert(C::kSmem + 512 <= 232448, "shared memory of an SM, some of it static");
   const int box = (1 << a.page_shift) < C::kKt ? (1 << a.page_shift) : C::kKt;
   CUtensorMap mk, mv;
   cudaError_t e = attn_page_map(&mk, a, a.K, box);
   if (e == cudaSuccess) e = attn_page_map(&mv, a, a.V, box);
   if (e != cudaSuccess) return e;
-  static const cudaError_t ready = attn_prepare_kernel(attn_rows_kernel<NS, HALF>, C::kSmem, C::kThreads, 72 * 128 + 216 * 256);
+  static const cudaError_t ready = attn_prepare_kernel(attn_rows_kernel<NS>, C::kSmem, C::kThreads, 72 * 128 + 216 * 256);
   if (ready != cudaSuccess) return ready;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(min(sm_count(), kAttnCtas));
@@ -410,15 +370,15 @@ static cudaError_t launch_rows(const AttnArgs& a, cudaStream_t s) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_rows_kernel<NS, HALF>, mk, mv, a);
+  return cudaLaunchKernelEx(&cfg, attn_rows_kernel<NS>, mk, mv, a);
 }
 
-cudaError_t launch_attn_rows(const AttnArgs& a, bool half, cudaStream_t s) {
+cudaError_t launch_attn_rows(const AttnArgs& a, cudaStream_t s) {
   switch ((a.dim + 63) / 64) {
-    case 1: return half ? launch_rows<1, true>(a, s) : launch_rows<1, false>(a, s);
-    case 2: return half ? launch_rows<2, true>(a, s) : launch_rows<2, false>(a, s);
-    case 3: return half ? launch_rows<3, true>(a, s) : launch_rows<3, false>(a, s);
-    default: return half ? launch_rows<4, true>(a, s) : launch_rows<4, false>(a, s);
+    case 1: return launch_rows<1>(a, s);
+    case 2: return launch_rows<2>(a, s);
+    case 3: return launch_rows<3>(a, s);
+    default: return launch_rows<4>(a, s);
   }
 }
 

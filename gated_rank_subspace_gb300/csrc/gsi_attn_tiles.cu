@@ -641,9 +641,10 @@ __global__ void __launch_bounds__(TilesCfg<NS>::kThreads, 1)
       const unsigned n_parts = unsigned(b1 - b0 + 1);
       auto wg_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory"); };
       // The part that begins a unit is the last thing its CTA does and the others' first, so they are there as a
-      // rule: then they are folded in here, and nothing of this one is written.
+      // rule: then they are folded in here, and nothing of this one is written.  (A thread folds its row's parts one
+      // after the other; many parts are joined faster by all threads.)
       bool fold = false;
-      if (!whole && b0 == int(blockIdx.x)) {
+      if (!whole && b0 == int(blockIdx.x) && n_parts <= 4) {
         if ((warp & 3) == 0 && lane == 0) {
           unsigned n;
           asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(n) : "l"(attn_counter(a, b0, q)) : "memory");
@@ -720,7 +721,11 @@ __global__ void __launch_bounds__(TilesCfg<NS>::kThreads, 1)
         const bool last = *reinterpret_cast<volatile int*>(&bars.last[q]) != 0;
         if (last) {
           __threadfence();
-          attn_join<BF16, false, 64>(a, g, b0, b1, NQ, q, 128, n_rows, tok0, row, 128);
+          // few rows: eight columns a thread, eight parts in flight
+          if (n_rows <= 32)
+            attn_join<BF16, false, 8>(a, g, b0, b1, NQ, q, 128, n_rows, tok0, row, 128);
+          else
+            attn_join<BF16, false, 64>(a, g, b0, b1, NQ, q, 128, n_rows, tok0, row, 128);
         }
         wg_sync();  // before the flag is written again
       }

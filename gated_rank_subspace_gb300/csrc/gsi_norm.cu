@@ -314,9 +314,9 @@ static cudaError_t launch_norm_types(const NormArgs& a, cudaStream_t s) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  // CTAs that stay pay from about two tokens an SM on
+  // CTAs that stay pay from the second token of an SM on (200 x 5120 LAYER: 5.8 us, a CTA a token 6.5; 303: 5.9 and 6.7)
   cudaError_t e;
-  if (a.T >= 2 * sm_count() && (launch_norm_rows<HT, YT, XT, true>(a, cfg, &e) || launch_norm_rows<HT, YT, XT, false>(a, cfg, &e)))
+  if (a.T > sm_count() && (launch_norm_rows<HT, YT, XT, true>(a, cfg, &e) || launch_norm_rows<HT, YT, XT, false>(a, cfg, &e)))
     return e;
   const int pieces = a.d / 4;
   const auto threads_for = [&](int vpt) { return ((pieces + vpt - 1) / vpt + 31) / 32 * 32; };
