@@ -15,7 +15,7 @@ namespace gsi {
 // next thread the next piece: a warp's 16-byte accesses cover whole lines (with
 // eight float32 values a thread every access touched half of twice the sectors).
 //
-// Few tokens are latency: a CTA a token.  Many are bytes, and a CTA a token
+// Few tokens are latency: a CTA a token (one of 4096: 2.5 us).  Many are bytes, and a CTA a token
 // waits for its first loads and its weights most of its life: there the CTAs
 // stay, keep the weights in shared memory and copy the rows to come ahead of
 // the one they work on, each thread its own pieces, so that no barrier guards
@@ -195,8 +195,10 @@ __global__ void __launch_bounds__(1024, 1) norm_token_kernel(const __grid_consta
 // one row, then kNormAhead + 1 rows' pieces, those of a thread written and read
 // by it alone.  The weights are in registers (REGS, two pieces a thread, up to
 // 5120 values), or, where wider rows leave no room for them, in shared memory
-// before the rows (four pieces a thread): 2049 x 5120 LAYER takes 26 us the
-// first way and 42 us the second, whose fewer warps wait on each other longer.
+// before the rows (four pieces a thread): 2049 x 5120 LAYER takes 36 us (4.1
+// TB/s) the first way and 42 us the second, whose fewer warps wait on each other
+// longer.  What is left is the row's own chain: up to four reductions of ~400
+// cycles, and ~460 instructions a warp.
 constexpr int kNormAhead = 3;
 template <bool REGS>
 struct NormRowsCfg {
