@@ -466,7 +466,13 @@ def _on_stream(stream):
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
-def _ints(name, t, n, dtype=torch.int32):
+# (The calls below take microseconds on the GPU: their checks are written for
+# the time they take here.)
+_I32, _I64 = torch.int32, torch.int64
+_DTYPES = {torch.float32: GSI_F32, torch.bfloat16: GSI_BF16}
+
+
+def _ints(name, t, n, dtype=_I32):
     """A contiguous integer CUDA tensor of n elements."""
     if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
         raise ValueError(f"{name} must be a contiguous CUDA tensor of {n} {dtype}, not {tuple(t.shape)} {t.dtype}")
@@ -474,9 +480,14 @@ def _ints(name, t, n, dtype=torch.int32):
 
 def _like(name, t, shape, dtype):
     """A contiguous CUDA tensor of this shape and type."""
-    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or t.shape != shape:
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor of {tuple(shape)} {dtype}, "
                          f"not {tuple(t.shape)} {t.dtype}")
+
+
+def _float_code(t) -> int:
+    code = _DTYPES.get(t.dtype)
+    return _dtype_code(t.dtype) if code is None else code
 
 
 @dataclass
@@ -494,13 +505,13 @@ class PagedCache:
 
     def desc(self) -> CacheDesc:
         K, V = self.K, self.V
-        st = K.stride()
-        if K.dim() != 4 or K.shape != V.shape or st != V.stride() or K.dtype is not V.dtype:
+        shape, st = K.shape, K.stride()
+        if len(shape) != 4 or V.shape != shape or V.stride() != st or V.dtype is not K.dtype:
             raise ValueError("K and V must be two (pages, heads, page_size, head_dim) tensors of one dtype and layout")
         if not K.is_cuda or not V.is_cuda or st[3] != 1:
             raise ValueError("K and V must be CUDA tensors with contiguous head_dim")
-        n, h, p, d = K.shape
-        return CacheDesc(n, p, h, d, _dtype_code(K.dtype), *st[:3], K.data_ptr(), V.data_ptr())
+        n, h, p, d = shape
+        return CacheDesc(n, p, h, d, _float_code(K), st[0], st[1], st[2], K.data_ptr(), V.data_ptr())
 
 
 @dataclass
@@ -545,22 +556,24 @@ def paged_plan(cached: torch.Tensor, fresh: torch.Tensor, table: torch.Tensor, f
     if table.dim() != 2 or table.shape[0] != R:
         raise ValueError(f"table must be ({R}, pages), not {tuple(table.shape)}")
     width = table.shape[1]
+    capacity = free_pages.numel()
+    q_start, kv_len, slots, req, pos, left, status = (plan.q_start, plan.kv_len, plan.slots, plan.token_req, plan.positions,
+                                                      plan.n_free, plan.status)
     _ints("cached", cached, R)
     _ints("fresh", fresh, R)
     _ints("table", table, R * width)
-    _ints("free_pages", free_pages, free_pages.numel())
+    _ints("free_pages", free_pages, capacity)
     _ints("n_free", n_free, 1)
-    _ints("plan.q_start", plan.q_start, R + 1)
-    _ints("plan.kv_len", plan.kv_len, R)
-    _ints("plan.slots", plan.slots, N, torch.int64)
-    _ints("plan.token_req", plan.token_req, N)
-    _ints("plan.positions", plan.positions, N)
-    _ints("plan.n_free", plan.n_free, 1)
-    _ints("plan.status", plan.status, 1)
+    _ints("plan.q_start", q_start, R + 1)
+    _ints("plan.kv_len", kv_len, R)
+    _ints("plan.slots", slots, N, _I64)
+    _ints("plan.token_req", req, N)
+    _ints("plan.positions", pos, N)
+    _ints("plan.n_free", left, 1)
+    _ints("plan.status", status, 1)
     _check(lib().gsi_paged_plan(cached.data_ptr(), fresh.data_ptr(), R, table.data_ptr(), width, free_pages.data_ptr(),
-                                free_pages.numel(), n_free.data_ptr(), page_size, N, plan.q_start.data_ptr(),
-                                plan.kv_len.data_ptr(), plan.slots.data_ptr(), plan.token_req.data_ptr(),
-                                plan.positions.data_ptr(), plan.n_free.data_ptr(), plan.status.data_ptr(),
+                                capacity, n_free.data_ptr(), page_size, N, q_start.data_ptr(), kv_len.data_ptr(),
+                                slots.data_ptr(), req.data_ptr(), pos.data_ptr(), left.data_ptr(), status.data_ptr(),
                                 _raw_stream(stream, cached)))
     return plan
 
@@ -571,18 +584,18 @@ def cache_append(cache: PagedCache, rows: torch.Tensor, slots: torch.Tensor, n_q
     (negative: padding), queries to Q (T, n_q_heads, head_dim), returned."""
     c = cache.desc()
     T = slots.numel()
-    if rows.dim() != 2 or not rows.is_cuda or rows.shape[0] != T or \
-            rows.shape[1] != (n_q_heads + 2 * c.n_heads) * c.head_dim or (rows.stride(1) != 1 and T):
-        raise ValueError(f"rows must be CUDA rows of ({T}, {(n_q_heads + 2 * c.n_heads) * c.head_dim}), "
-                         f"not {tuple(rows.shape)}")
-    _ints("slots", slots, T, torch.int64)
+    D = c.head_dim
+    st = rows.stride()
+    if rows.shape != (T, (n_q_heads + 2 * c.n_heads) * D) or not rows.is_cuda or (st[1] != 1 and T):
+        raise ValueError(f"rows must be CUDA rows of ({T}, {(n_q_heads + 2 * c.n_heads) * D}), not {tuple(rows.shape)}")
+    _ints("slots", slots, T, _I64)
     if Q is None:
         with _on_stream(stream):
-            Q = torch.empty(T, n_q_heads, c.head_dim, dtype=cache.K.dtype, device=rows.device)
+            Q = torch.empty(T, n_q_heads, D, dtype=cache.K.dtype, device=rows.device)
     else:
-        _like("Q", Q, (T, n_q_heads, c.head_dim), cache.K.dtype)
-    _check(lib().gsi_cache_append(ctypes.byref(c), rows.data_ptr(), _dtype_code(rows.dtype), rows.stride(0),
-                                  slots.data_ptr(), T, n_q_heads, Q.data_ptr(), _raw_stream(stream, rows)))
+        _like("Q", Q, (T, n_q_heads, D), cache.K.dtype)
+    _check(lib().gsi_cache_append(c, rows.data_ptr(), _float_code(rows), st[0], slots.data_ptr(), T, n_q_heads,
+                                  Q.data_ptr(), _raw_stream(stream, rows)))
     return Q
 
 
@@ -606,11 +619,11 @@ def paged_attention(cache: PagedCache, Q: torch.Tensor, q_start: torch.Tensor, k
     are not written.  max_q: a bound on a request's new tokens, for the choice
     of kernel.  scale defaults to head_dim ** -0.5."""
     c = cache.desc()
-    if Q.dim() != 3 or not Q.is_cuda or Q.dtype is not cache.K.dtype or Q.shape[2] != c.head_dim:
+    shape, st = Q.shape, Q.stride()
+    if len(shape) != 3 or not Q.is_cuda or Q.dtype is not cache.K.dtype or shape[2] != c.head_dim:
         raise ValueError(f"Q must be a (tokens, heads, {c.head_dim}) CUDA tensor of {cache.K.dtype}, "
-                         f"not {tuple(Q.shape)} {Q.dtype}")
-    N, H, D = Q.shape
-    st = Q.stride()
+                         f"not {tuple(shape)} {Q.dtype}")
+    N, H, D = shape
     if N and (st[2] != 1 or (H > 1 and st[1] != D)):
         raise ValueError("the heads of a token of Q must be contiguous")
     R = kv_len.numel()
@@ -624,11 +637,11 @@ def paged_attention(cache: PagedCache, Q: torch.Tensor, q_start: torch.Tensor, k
         with _on_stream(stream):
             out = torch.empty(N, H, D, dtype=Q.dtype, device=Q.device)
     else:
-        _like("out", out, Q.shape, Q.dtype)
+        _like("out", out, shape, Q.dtype)
     if workspace is None:
         with _on_stream(stream):
             workspace = new_workspace(paged_attention_workspace_size(cache, H), Q.device, stream)
-    _check(lib().gsi_paged_attention(ctypes.byref(c), Q.data_ptr(), st[0], N, H, q_start.data_ptr(), kv_len.data_ptr(),
+    _check(lib().gsi_paged_attention(c, Q.data_ptr(), st[0], N, H, q_start.data_ptr(), kv_len.data_ptr(),
                                      table.data_ptr(), width, R, N if max_q is None else max_q,
                                      D ** -0.5 if scale is None else scale, 1 if causal else 0, window, out.data_ptr(),
                                      workspace.data_ptr(), workspace.numel(), _raw_stream(stream, Q)))
@@ -660,10 +673,12 @@ def norm_residual(h: torch.Tensor, y: torch.Tensor = None, post: Norm = None, pr
     h, y, x: float32 or bfloat16.  gate: float32, (d,) for every token or
     (n, d) with gate_index (T int32) naming each token's row (a plan's
     token_req, for a gate per request).  h_out may be h."""
-    T, d = h.shape
-    _like("h", h, (T, d), h.dtype)
+    shape = h.shape
+    T, d = shape
+    if not h.is_cuda or not h.is_contiguous():
+        raise ValueError("h must be a contiguous CUDA tensor")
     if y is not None:
-        _like("y", y, (T, d), y.dtype)
+        _like("y", y, shape, y.dtype)
     rows = 0
     if gate is not None:
         rows = gate.numel() // d
@@ -676,17 +691,16 @@ def norm_residual(h: torch.Tensor, y: torch.Tensor = None, post: Norm = None, pr
         with _on_stream(stream):
             h_out = torch.empty_like(h)
     else:
-        _like("h_out", h_out, (T, d), h.dtype)
+        _like("h_out", h_out, shape, h.dtype)
     if x is None:
         with _on_stream(stream):
             x = torch.empty(T, d, dtype=x_dtype, device=h.device)
     else:
-        _like("x", x, (T, d), x.dtype)
-    _check(lib().gsi_norm_residual(h.data_ptr(), _dtype_code(h.dtype), None if y is None else y.data_ptr(),
-                                   0 if y is None else _dtype_code(y.dtype), T, d, alpha,
-                                   None if post is None else ctypes.byref(post.desc(d)),
-                                   None if gate is None else gate.data_ptr(), rows,
+        _like("x", x, shape, x.dtype)
+    _check(lib().gsi_norm_residual(h.data_ptr(), _float_code(h), None if y is None else y.data_ptr(),
+                                   0 if y is None else _float_code(y), T, d, alpha,
+                                   None if post is None else post.desc(d), None if gate is None else gate.data_ptr(), rows,
                                    None if gate_index is None else gate_index.data_ptr(),
-                                   None if pre is None else ctypes.byref(pre.desc(d)), h_out.data_ptr(), x.data_ptr(),
-                                   _dtype_code(x.dtype), _raw_stream(stream, h)))
+                                   None if pre is None else pre.desc(d), h_out.data_ptr(), x.data_ptr(), _float_code(x),
+                                   _raw_stream(stream, h)))
     return h_out, x

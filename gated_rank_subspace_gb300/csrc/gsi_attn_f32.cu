@@ -51,7 +51,8 @@ __global__ void __launch_bounds__(kF32Threads, BM == 16 || NC <= 2 ? 2 : 1) attn
   float* sv = sk + kF32Keys * DP;
   float* sp = sv + kF32Keys * DP;
   // the output's columns: CG lanes a row, the lanes left over take a part of the keys each
-  int cg = 1;
+  // (four keys at a time, so at least TK / 16 lanes a row)
+  int cg = TK / 16;
   while (cg < d4 && cg < TK) cg *= 2;
   const int kq = tk / cg, keys_each = kF32Keys * cg / TK, c0 = tk % cg;
 

@@ -51,10 +51,10 @@ __device__ __forceinline__ void rows_ldsm_t(uint32_t addr, uint32_t (&r)[4]) {
 }
 // c += a b, the upper 8 rows of the 16 (the lower ones are zeros that go nowhere).
 __device__ __forceinline__ void rows_mma(float (&c)[2], const uint32_t (&a)[2], uint32_t b0, uint32_t b1) {
-  float x, y;
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %8, %5, %8}, {%6, %7}, {%0, %1, %9, %9};"
-      : "+f"(c[0]), "+f"(c[1]), "=f"(x), "=f"(y)
-      : "r"(a[0]), "r"(a[1]), "r"(b0), "r"(b1), "r"(0u), "f"(0.f));
+  float x = 0.f, y = 0.f;
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %8, %5, %8}, {%6, %7}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(x), "+f"(y)
+      : "r"(a[0]), "r"(a[1]), "r"(b0), "r"(b1), "r"(0u));
 }
 // The compute warps only.
 template <int N>

@@ -58,9 +58,9 @@ static gsi_status check_cache(const gsi_cache_desc* c) {
     return refuse(GSI_ERR_UNSUPPORTED, "head_dim=%lld is above 256 or not a multiple of 16 bytes", (long long)c->head_dim);
   if (c->n_heads > 4096 || c->n_pages > (int64_t(1) << 31) - 1)
     return refuse(GSI_ERR_UNSUPPORTED, "more than 4096 heads or 2^31 pages");
-  const int64_t st[3] = {c->page_stride, c->head_stride, c->token_stride};
+  const int64_t st[3] = {c->page_stride, c->head_stride, c->token_stride}, n[3] = {c->n_pages, c->n_heads, c->page_size};
   for (int i = 0; i < 3; ++i) {
-    if (st[i] < 0) return refuse(GSI_ERR_INVALID_ARG, "negative cache stride");
+    if (st[i] < 0 || (st[i] == 0 && n[i] > 1)) return refuse(GSI_ERR_INVALID_ARG, "a cache stride is not positive");
     if ((st[i] * es) % 16) return refuse(GSI_ERR_UNSUPPORTED, "a cache stride is not a multiple of 16 bytes");
     if (st[i] >= int64_t(1) << 38) return refuse(GSI_ERR_UNSUPPORTED, "a cache stride is above 2^38");
   }
@@ -201,8 +201,8 @@ gsi_status gsi_paged_attention(const gsi_cache_desc* cache, const void* Q, int64
   if (window < 0 || (window > 0 && !causal))
     return refuse(GSI_ERR_INVALID_ARG, "window must be >= 0, and 0 where the attention is not causal");
   if (N > (int64_t(1) << 24) || n_req > (int64_t(1) << 20) ||
-      table_width >= (int64_t(1) << 31) / cache->page_size)
-    return refuse(GSI_ERR_UNSUPPORTED, "more than 2^24 tokens, 2^20 requests or 2^31 places of a request");
+      table_width > ((int64_t(1) << 31) - 512) / cache->page_size)  // a tile's end stays within 31 bits
+    return refuse(GSI_ERR_UNSUPPORTED, "more than 2^24 tokens, 2^20 requests or 2^31 - 512 places of a request");
   if (N == 0 || n_req == 0) return record_error(GSI_OK, "");
   const int64_t values = n_q_heads * cache->head_dim;
   if (q_stride < values && N > 1)

@@ -360,8 +360,9 @@ gsi_status gsi_linear_noalloc_status(uint32_t* code, void* stream);
  * the head_dim values of token o of page p under head h are contiguous at
  * element p * page_stride + h * head_stride + o * token_stride of either.
  * page_size is a power of two from 16 to 256; head_dim is at most 256;
- * head_dim and the strides are multiples of 16 bytes; the strides are
- * non-negative.  GSI_ERR_UNSUPPORTED otherwise. */
+ * head_dim and the strides are multiples of 16 bytes (GSI_ERR_UNSUPPORTED
+ * otherwise); a stride is positive where its dimension has more than one
+ * element (GSI_ERR_INVALID_ARG). */
 typedef struct gsi_cache_desc {
   int64_t n_pages;
   int64_t page_size;
@@ -433,7 +434,9 @@ gsi_status gsi_cache_append(const gsi_cache_desc* cache, const void* X, gsi_dtyp
  * O is N x n_q_heads x head_dim, of the cache's type like Q; its rows outside
  * every request are not written.  q_start must not decrease and stays within
  * N; kv_len stays within table_width * page_size (a longer one is cut there);
- * a table entry outside the cache reads as zeros.
+ * a table entry outside the cache reads as zeros.  N <= 2^24, n_req <= 2^20,
+ * table_width * page_size <= 2^31 - 512, at most 128 query heads a key/value
+ * head.
  * Softmax statistics and sums are float32; for GSI_BF16 the weights p enter
  * the second product as bf16.  max_q is the caller's bound on a request's
  * new tokens (it chooses the kernel; a wrong one costs time, not results).

@@ -217,6 +217,12 @@ def test_attention(gsi, lens, dt, hq, hkv, D, page):
     attention_case(gsi, dt, hq, hkv, D, page, lens)
 
 
+@pytest.mark.parametrize("dt,D", [(BF, 8), (BF, 16), (BF, 40), (BF, 136), (F, 4), (F, 8), (F, 20), (F, 100), (F, 252)])
+@pytest.mark.parametrize("lens", [[(1, 77), (1, 3)], [(3, 200), (1, 1)], [(70, 300)]], ids=str)
+def test_attention_odd_head_sizes(gsi, dt, D, lens):
+    attention_case(gsi, dt, 4, 2, D, 16, lens)
+
+
 @pytest.mark.parametrize("dt,D", [(BF, 128), (BF, 256), (F, 64)])
 @pytest.mark.parametrize("window", [1, 16, 100, 128, 1000])
 @pytest.mark.parametrize("lens", [[(1, 1), (1, 500), (2, 131)], [(150, 400), (3, 129)]], ids=str)
@@ -337,6 +343,27 @@ def test_attention_streams_from_memory(gsi, D, q, group):
         assert ((out[:, h].double() - want).abs() <= 1e-4 * A + 2**-8 * (A + want.abs())).all()
 
 
+@pytest.mark.parametrize("D,hq,hkv,q,k", [(256, 16, 16, 2048, 2048), (128, 32, 32, 1500, 1700), (64, 40, 8, 1900, 1900),
+                                           (192, 24, 24, 1601, 1601), (128, 48, 16, 1111, 1300)])
+def test_attention_of_one_prompt(gsi, D, hq, hkv, q, k):
+    # enough units of one causal request to be dealt out whole
+    page = 32
+    n = -(-k // page)
+    g = torch.Generator(device="cuda").manual_seed(D + q)
+    K, V = (torch.randn(n, hkv, page, D, device="cuda", generator=g, dtype=BF) for _ in range(2))
+    Q = 2 * torch.randn(q, hq, D, device="cuda", generator=g, dtype=BF)
+    table = torch.randperm(n, device="cuda", generator=g).int()[None]
+    ws = gsi.new_workspace(gsi.paged_attention_workspace_size(gsi.PagedCache(K, V), hq))
+    out = gsi.paged_attention(gsi.PagedCache(K, V), Q, i32([0, q]), i32([k]), table, workspace=ws)
+    assert gsi.workspace_status(ws) == 0
+    hidden = torch.arange(k, device="cuda") > torch.arange(k - q, k, device="cuda")[:, None]
+    for h in range(0, hq, 5):
+        ks, vs = (t[table[0].long(), h * hkv // hq].reshape(-1, D)[:k].double() for t in (K, V))
+        p = torch.softmax((Q[:, h].double() @ ks.T * D ** -0.5).masked_fill(hidden, -float("inf")), -1)
+        want, A = p @ vs, p @ vs.abs()
+        assert ((out[:, h].double() - want).abs() <= 1e-4 * A + 2**-8 * (A + want.abs())).all()
+
+
 def test_attention_offsets_beyond_32_bits(gsi):
     # a cache of more than 2^31 elements, the request's pages at its far end and at its beginning
     hkv, D, page, k = 8, 128, 64, 300
@@ -407,7 +434,8 @@ def test_attention_of_nothing(gsi):
 
 
 # ------------------------------------------------------------------ norm
-@pytest.mark.parametrize("T,d", [(1, 8), (3, 256), (5, 4096), (2, 5120), (17, 1032), (3, 16384), (2, 8200)])
+@pytest.mark.parametrize("T,d", [(1, 8), (3, 256), (5, 4096), (2, 5120), (17, 1032), (3, 16384), (2, 8200),
+                                 (153, 5120), (340, 1032), (170, 5128), (160, 8192), (700, 64)])
 @pytest.mark.parametrize("post,pre", [("rms", "rms"), ("layer", "layer"), ("none", "layer"), (None, "rms"), ("rms", None)])
 @pytest.mark.parametrize("gate", [None, "row", "index"])
 @pytest.mark.parametrize("hdt,ydt,xdt", [(F, F, BF), (BF, F, BF), (F, BF, F), (BF, BF, F)])

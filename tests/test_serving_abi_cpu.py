@@ -76,7 +76,7 @@ def test_nothing_to_do_is_no_launch():
 @pytest.mark.parametrize("kw,status,needle", [
     (dict(page=24), 2, "page_size"), (dict(page=8), 2, "page_size"), (dict(page=512), 2, "page_size"),
     (dict(dim=260), 2, "head_dim"), (dict(dim=62), 2, "head_dim"), (dict(dim=0), 1, "positive"),
-    (dict(dt=5), 1, "dtype"), (dict(ts=60), 2, "stride"), (dict(hs=-64), 1, "stride"), (dict(K=None), 1, "K is NULL"),
+    (dict(dt=5), 1, "dtype"), (dict(ts=60), 2, "stride"), (dict(hs=-64), 1, "stride"), (dict(hs=0), 1, "stride"), (dict(ps=0), 1, "stride"), (dict(K=None), 1, "K is NULL"),
     (dict(V=P + 8), 1, "aligned"), (dict(n_pages=-1), 1, "positive"), (dict(n_pages=1 << 31), 2, "pages"),
     (dict(ps=1 << 40), 2, "stride")])
 def test_cache_refusals(kw, status, needle):
@@ -91,7 +91,7 @@ def test_cache_refusals(kw, status, needle):
     (dict(window=4, causal=0), 1, "window"), (dict(q_stride=255), 1, "q_stride"), (dict(q_stride=260), 2, "q_stride"),
     (dict(Q=None), 1, "Q is NULL"), (dict(O=P + 4), 1, "aligned"), (dict(qs=None), 1, "q_start"), (dict(tb=None), 1, "table"),
     (dict(ws=None), 4, "NULL"), (dict(ws=P + 16), 4, "256-byte"), (dict(n=8), 4, "needed"), (dict(N=1 << 25), 2, "2^24"),
-    (dict(width=1 << 28), 2, "2^31"), (dict(ln=P + 2), 1, "aligned")])
+    (dict(width=1 << 28), 2, "2^31"), (dict(width=(1 << 27) - 31), 2, "2^31"), (dict(ln=P + 2), 1, "aligned")])
 def test_attention_refusals(kw, status, needle):
     refused(attention(**kw), status, needle)
 
