@@ -10,6 +10,8 @@
 
 namespace gsi {
 
+constexpr int kAttnCtas = 152;  // CTAs of a launch, at most: one an SM (two over a float32 cache)
+
 // ------------------------------------------------------------------ work
 // A unit is a block of `ut` consecutive new tokens of one request under one
 // key/value head (their ut * group query rows), over the tiles of `kt` keys
@@ -223,20 +225,25 @@ struct AttnShare {
   int dealt;                  // units dealt out whole instead (their number)
 };
 
-// One causal prompt alone has units that shrink with their place.  Where there
-// are enough of them, they are dealt out whole, the longest first, back and
-// forth over the CTAs: no unit is cut, and the shares differ by about a tile
-// (2048 tokens of 16 x 256: 16 tiles at most where 14.3 is the mean, and a cut
-// share costs about kAttnCut tiles more).  Long shares stay on the line: there
-// a cut is nothing, and neighbours read the same keys.
-constexpr int kAttnCut = 5, kAttnDealMost = 64;
+// One causal request alone has units that shrink with their place.  They are
+// dealt out whole, the longest first, back and forth over the CTAs, where the
+// longest hand is at most what the line's cuts cost (kAttnCut tiles, and an
+// eighth: neighbours on the line wait for each other's parts) above the mean: no
+// unit is cut then.  2048 tokens of 16 x 256 (16 tiles at most, 14.3 the mean):
+// 41 us, on the line 49; 4096 of 40 x 128 (90, 80) 162, on the line 175; 8192 of
+// 32 x 128 394, on the line 417; but 1000 behind 4000 of 40 x 128 (73, 39) 133,
+// on the line 93.
+constexpr int kAttnCut = 5, kAttnDealRows = 16;
+__device__ __forceinline__ int attn_dealt(int k, int cta, int n_cta) {  // a hand's k-th unit
+  return k * n_cta + (k & 1 ? n_cta - 1 - cta : cta);
+}
 
 // The share of CTA blockIdx.x and where it begins; all NT threads of the block.
 // Each half of the block goes over the requests, and finds one of the two cuts.
 template <int NT>
 __device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, int ut, int kt, int extra, AttnPlace& begin) {
   constexpr int NH = NT / 2, NW = NH / 32;
-  static_assert(NT % 64 == 0, "halves of whole warps");
+  static_assert(NT % 64 == 0 && NT >= kAttnCtas, "halves of whole warps; a thread a CTA");
   __shared__ long long s_tiles[2 * NW], s_units[2 * NW], s_cut[2];
   __shared__ AttnPlace s_begin;
   const int tid = threadIdx.x, lane = tid & 31, half = tid / NH, warp = (tid >> 5) - half * NW;
@@ -278,12 +285,28 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, int ut, int k
   s.grid = int(total < (long long)gridDim.x ? total : (long long)gridDim.x);
   s.pos = s.end = 0;
   s.dealt = 0;
-  if (s.extra > 0 && a.n_req == 1 && a.causal && a.window == 0 && total_units >= s.grid && total <= (long long)kAttnDealMost * s.grid) {
+  if (extra > 0 && a.n_req == 1 && a.causal && a.window == 0 && total_units >= gridDim.x && total_units < (1ll << 30)) {
     const AttnReq all = attn_request(a, 0);
-    int t0, n;
-    attn_tiles(a, all, attn_units(all, ut) - 1, ut, kt, t0, n);
-    if ((long long)(n + s.extra - kAttnCut) * s.grid <= total) {
-      s.dealt = int(total_units);
+    const int n_units = int(total_units), n_cta = int(gridDim.x), rows = (n_units + n_cta - 1) / n_cta;
+    bool deal;
+    if (rows > kAttnDealRows) {
+      deal = all.len == all.q_len;  // a whole prompt's last rows are its shortest units
+    } else {
+      int load = 0;  // of CTA tid
+      if (tid < n_cta)
+#pragma unroll 1
+        for (int k = 0; k < rows; ++k) {
+          const int i = attn_dealt(k, tid, n_cta);
+          if (i < n_units) {
+            int t0, n;
+            attn_tiles(a, all, attn_units(all, ut) - 1 - i / a.hkv, ut, kt, t0, n);
+            load += max(1, n) + s.extra;
+          }
+        }
+      deal = !__syncthreads_or((long long)(load - kAttnCut) * n_cta * 8 > total * 9);
+    }
+    if (deal) {
+      s.dealt = n_units;
       begin.q = all;
       begin.r = begin.h = begin.u = 0;
       begin.off = 0;  // units taken
@@ -337,8 +360,7 @@ struct AttnWalk {
 
   __device__ __forceinline__ bool next(const AttnArgs& a, AttnSeg& g) {
     if (s.dealt > 0) {
-      const int k = int(p.off), row = k * int(gridDim.x);
-      const int i = k & 1 ? row + int(gridDim.x) - 1 - int(blockIdx.x) : row + int(blockIdx.x);
+      const int i = attn_dealt(int(p.off), int(blockIdx.x), int(gridDim.x));
       if (i >= s.dealt) return false;
       ++p.off;
       g.q = p.q;
@@ -385,7 +407,6 @@ struct AttnWalk {
 // depend on who came last) and sets the counter back to zero.  Nobody waits.
 // At most two units of a share are cut: one that an earlier CTA began (slot
 // 2 b) and one that a later CTA ends (slot 2 b + 1).
-constexpr int kAttnCtas = 152;  // CTAs of a launch, at most: one an SM (two over a float32 cache)
 constexpr size_t kAttnCounterBytes = 4096;
 static_assert(2 * kAttnCtas * 2 * 4 <= int(kAttnCounterBytes), "two counters (row tiles) a CTA");
 
