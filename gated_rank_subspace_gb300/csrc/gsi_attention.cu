@@ -1,6 +1,8 @@
 // Attention of new tokens over a paged key/value cache: dispatch, and the
 // plain kernel.
 
+#include <algorithm>
+
 #include "gsi_attn.cuh"
 
 namespace gsi {
@@ -155,10 +157,18 @@ size_t attention_work_bytes(gsi_dtype dt, int dim, int group) {
 // us: bf16, 8 heads that share one of 8 key/value heads of 128 columns, 2000 keys
 // 14.4 (row tiles 14.8), 8 requests of 8000 keys 41 (44); 16 heads 19 (16) and 53
 // (45).  float32, 16 rows over 2000 keys of 8 x 64: 31 (44); 32 rows 43 (47).
+constexpr int64_t kF32FewTiles = 304;
 cudaError_t launch_paged_attention(const AttnArgs& a, gsi_dtype dt, int64_t max_q, cudaStream_t s) {
   const int64_t most = max_q * a.group;
   if (dt == GSI_BF16) return most <= 8 ? launch_attn_rows(a, s) : launch_attn_tiles(a, s);
-  if (a.group <= 64) return launch_attn_f32(a, most <= 16, s);
+  if (a.group <= 64) {
+    // 64-row units that do not fill the chip are too long a chain each (there are at most `tiles` of their tiles here):
+    // 64 tokens, window 128, 4 x 64 16 us with 16 rows, 24 with 64; 100 of 500, 4 requests of 4 x 64 25 and 28; but 100
+    // of 1000, 4 requests of 8 / 4 x 128 75 and 70, 128 of 1000, 8 requests of 8 x 64 86 and 62
+    const int64_t keys = std::min<int64_t>(a.width << a.page_shift, a.window > 0 ? a.window + 128 : int64_t(1) << 31);
+    const int64_t tiles = (int64_t(a.N) * a.group / 64 + 1) * a.hkv * (keys / 64 + 1);
+    return launch_attn_f32(a, most <= 16 || (a.group <= 16 && tiles < kF32FewTiles), s);
+  }
   const int64_t rows = int64_t(a.N) * a.hkv * a.group;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(unsigned((rows + kPlainWarps - 1) / kPlainWarps));

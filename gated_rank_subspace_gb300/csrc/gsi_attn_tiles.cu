@@ -25,8 +25,8 @@ namespace gsi {
 // What bounds it: up to 128 columns the chain of a row tile (S, its maximum, 128
 // exponentials a thread, then its two products, ~3000 cycles a tile of 256 rows
 // against 2048 of products); above, the reads of L2 (128 KB a tile of 128 rows,
-// ~10 TB/s over the SMs).  8192 tokens: 32 x 128 403 us (1.37 PFLOP/s), 16 x 256
-// 439 us (1.25), 32 x 64 339 us (0.81); 2048 tokens of 16 x 256 49 us.
+// ~10 TB/s over the SMs).  8192 tokens: 32 x 128 395 us (1.39 PFLOP/s), 16 x 256
+// 414 us (1.33), 32 x 64 341 us (0.81); 2048 tokens of 16 x 256 41 us.
 //
 // Masked tiles: S is masked in registers; a weight of 0 hides a number of V
 // but not an infinity or NaN, nor the ring's stale bytes where no page was
@@ -136,6 +136,13 @@ __device__ __forceinline__ void tl_st32(uint32_t t, const uint32_t* r) {
       "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
       ::"r"(t), GSI_W8(r, 0), GSI_W8(r, 8), GSI_W8(r, 16), GSI_W8(r, 24)
       : "memory");
+}
+
+// After tl_wait_ld(): nothing that uses these registers may move before it.
+#define GSI_H8(r, i) "+r"((r)[(i)]), "+r"((r)[(i) + 1]), "+r"((r)[(i) + 2]), "+r"((r)[(i) + 3]), "+r"((r)[(i) + 4]), \
+                     "+r"((r)[(i) + 5]), "+r"((r)[(i) + 6]), "+r"((r)[(i) + 7])
+__device__ __forceinline__ void tl_arrived32(uint32_t* r) {
+  asm volatile("" : GSI_H8(r, 0), GSI_H8(r, 8), GSI_H8(r, 16), GSI_H8(r, 24)::"memory");
 }
 
 // Shared-memory operand descriptors, 128-byte swizzle (version 1).  K-major
@@ -538,6 +545,8 @@ __global__ void __launch_bounds__(TilesCfg<NS>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) tl_ld32(s_at + 32 * i, sr + 32 * i);
         tl_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tl_arrived32(sr + 32 * i);
         const int tile = (g.t0 + j) * kTileKeys;
         if (neg) {
 #pragma unroll
@@ -578,6 +587,7 @@ __global__ void __launch_bounds__(TilesCfg<NS>::kThreads, 1)
               uint32_t r[32];
               tl_ld32(o_at + 32 * i, r);
               tl_wait_ld();
+              tl_arrived32(r);
 #pragma unroll
               for (int z = 0; z < 32; ++z) r[z] = __float_as_uint(__uint_as_float(r[z]) * f);
               tl_st32(o_at + 32 * i, r);
@@ -668,6 +678,7 @@ __global__ void __launch_bounds__(TilesCfg<NS>::kThreads, 1)
           __syncwarp();
           asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(x) : "r"(o_at + i));
           tl_wait_ld();
+          asm volatile("" : "+r"(x)::"memory");
           if (row < n_rows)
             x = __float_as_uint(attn_nonfinite<BF16>(a, g, kTileKeys, lo, lim, t.lo_max, t.lim_min, i, __uint_as_float(x)));
           __syncwarp();
@@ -685,6 +696,8 @@ __global__ void __launch_bounds__(TilesCfg<NS>::kThreads, 1)
           tl_ld32(o_at + 64 * i, r);
           tl_ld32(o_at + 64 * i + 32, r + 32);
           tl_wait_ld();
+          tl_arrived32(r);
+          tl_arrived32(r + 32);
         } else {
 #pragma unroll
           for (int z = 0; z < 64; ++z) r[z] = 0;
