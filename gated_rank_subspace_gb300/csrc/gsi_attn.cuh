@@ -283,6 +283,11 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, int ut, int k
   const long long before = it + s.extra * iu, mine = tiles + s.extra * units;
   s.total = total;
   s.grid = int(total < (long long)gridDim.x ? total : (long long)gridDim.x);
+  if (total > s.grid && total < 16 * s.grid) {
+    // as few CTAs as leave the longest share as it is: 512 tiles are 4 for 128 CTAs and for 152, with fewer parts to join
+    const unsigned tiles = unsigned(total), most = (tiles + s.grid - 1) / unsigned(s.grid);
+    s.grid = int((tiles + most - 1) / most);
+  }
   s.pos = s.end = 0;
   s.dealt = 0;
   if (extra > 0 && a.n_req == 1 && a.causal && a.window == 0 && total_units >= gridDim.x && total_units < (1ll << 30)) {
