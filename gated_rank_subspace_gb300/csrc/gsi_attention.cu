@@ -159,7 +159,9 @@ size_t attention_work_bytes(gsi_dtype dt, int dim, int group) {
 // (45).  float32, 16 rows over 2000 keys of 8 x 64: 31 (44); 32 rows 43 (47).
 constexpr int64_t kF32FewTiles = 304;
 cudaError_t launch_paged_attention(const AttnArgs& a, gsi_dtype dt, int64_t max_q, cudaStream_t s) {
-  const int64_t most = max_q * a.group;
+  // The hint is the caller's: a request that has tokens has at least one and no more than all of them, whatever it says
+  // (a unit of the few-row kernels has to hold a token's heads).
+  const int64_t most = std::clamp<int64_t>(max_q, 1, a.N) * a.group;
   if (dt == GSI_BF16) return most <= 8 ? launch_attn_rows(a, s) : launch_attn_tiles(a, s);
   if (a.group <= 64) {
     // 64-row units that do not fill the chip are too long a chain each (there are at most `tiles` of their tiles here):

@@ -433,6 +433,14 @@ def test_attention_of_nothing(gsi):
     assert (out == 0.0).all()
 
 
+@pytest.mark.parametrize("dt,group", [(BF, 8), (BF, 9), (BF, 16), (BF, 128), (F, 16), (F, 17), (F, 32), (F, 64), (F, 65)])
+def test_attention_any_hint(gsi, dt, group):
+    # no token, one, all of them and no bound: the hint chooses a kernel that holds a token's heads, or none would
+    for lens in ([(1, 70), (1, 9)], [(3, 40), (0, 8), (2, 2)]):
+        for max_q in (0, 1, sum(q for q, _ in lens), 2**62, 2**63 - 1):
+            attention_case(gsi, dt, 2 * group, 2, 64, 16, lens, max_q=max_q)
+
+
 # ------------------------------------------------------------------ norm
 @pytest.mark.parametrize("T,d", [(1, 8), (3, 256), (5, 4096), (2, 5120), (17, 1032), (3, 16384), (2, 8200),
                                  (153, 5120), (340, 1032), (170, 5128), (160, 8192), (700, 64)])

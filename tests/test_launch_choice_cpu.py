@@ -1,0 +1,77 @@
+"""Which kernel a serving call launches, and with what, without a GPU.
+
+A small C++ harness (fake_runtime.cpp) runs the built library against a fake of
+the runtime calls on a launch's path.  A kernel that is launched for a shape
+it has no unit for would only show on a GPU, as a fault.
+"""
+import json
+import os
+import shutil
+import subprocess
+
+import pytest
+
+import __graft_entry__
+
+__graft_entry__.build()
+from gated_rank_subspace_gb300 import _build  # noqa: E402
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+F32, BF16 = 0, 1
+
+
+@pytest.fixture(scope="module")
+def run(tmp_path_factory):
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("g++ is not available")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_build.nvcc())))
+    exe = str(tmp_path_factory.mktemp("fake") / "fake_runtime")
+    subprocess.run([gxx, "-std=c++17", "-O1", "-rdynamic", "-I", _build.INCLUDE, "-I", os.path.join(cuda, "include"),
+                    os.path.join(HERE, "fake_runtime.cpp"), _build.LIB, "-Wl,-rpath," + os.path.dirname(_build.LIB),
+                    "-Wl,-rpath," + os.path.join(cuda, "lib64"), "-L" + os.path.join(cuda, "lib64"), "-lcudart", "-ldl",
+                    "-o", exe], check=True)
+
+    def go(*commands):
+        r = subprocess.run([exe], input="\n".join(commands) + "\n", capture_output=True, text=True, check=True)
+        return [json.loads(x) for x in r.stdout.splitlines()]
+
+    return go
+
+
+def attention(dt, group, N, max_q, hkv=2, dim=64, n_req=1, width=8, page=16, window=0):
+    return f"attention {dt} {group} {hkv} {dim} {N} {max_q} {n_req} {width} {page} {window}"
+
+
+HINTS = [0, 1, 2, 5, 300, 2**31, 2**62, 2**63 - 1]
+
+
+@pytest.mark.parametrize("dim", [64, 256])
+@pytest.mark.parametrize("group", [1, 2, 8, 9, 16, 17, 32, 64, 65, 128])
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_attention_kernel_holds_a_token_of_the_group(run, dt, group, dim):
+    # a unit of the few-row kernels is 8 / group (float32: 16 / group) tokens: at least one, whatever the caller's hint says
+    N = 5
+    for hint, r in zip(HINTS, run(*[attention(dt, group, N, h, dim=dim) for h in HINTS])):
+        assert r["status"] == 0
+        (launch,) = r["launches"]
+        name = launch["kernel"]
+        if "attn_rows_kernel" in name:
+            assert group <= 8, (hint, name)
+        elif "attn_f32_kernelILi16" in name:
+            assert group <= 16, (hint, name)
+        elif "attn_f32_kernelILi64" in name:
+            assert group <= 64, (hint, name)
+        elif "attn_tiles_kernel" in name:
+            assert group <= 128
+        else:
+            assert "attn_plain_kernel" in name and dt == F32
+
+
+@pytest.mark.parametrize("group", [1, 4, 8, 9, 16, 64, 128])
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_attention_hint_beyond_the_tokens_is_their_number(run, dt, group):
+    # no hint below one token or above all of them can mean anything else
+    a = run(*[attention(dt, group, 300, h) for h in (0, 1, 300, 301, 2**31, 2**62, 2**63 - 1)])
+    names = [r["launches"][0]["kernel"] for r in a]
+    assert names[0] == names[1] and len(set(names[2:])) == 1
