@@ -496,10 +496,18 @@ __device__ __forceinline__ void attn_fold(const AttnArgs& a, int from, int to, i
   }
 }
 
-// Writes CW columns from c of a finished row: o / l.
+// 1 / l for a row of token tok.  A sum of 0 is that of a row without a key, whose output is zeros, or of one whose scores are
+// all -inf, which has no softmax (any other row's largest weight is about 1).
+__device__ __forceinline__ float attn_inverse(const AttnArgs& a, const AttnReq& q, int tok, float l) {
+  if (l != 0.f) return 1.f / l;
+  return attn_lim(a, q, tok) > 0 ? NAN : 0.f;
+}
+
+// Writes CW columns from c of a finished row of token tok: o / l.
 template <class T, int CW>
-__device__ __forceinline__ void attn_finish(const AttnArgs& a, int64_t at, int c, float l, const float (&o)[CW]) {
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+__device__ __forceinline__ void attn_finish(const AttnArgs& a, const AttnReq& q, int tok, int64_t at, int c, float l,
+                                            const float (&o)[CW]) {
+  const float inv = attn_inverse(a, q, tok, l);
   if constexpr (CW == 4) {
     static_assert(T::kBytes == 4, "pieces of four are float32's");
     *reinterpret_cast<float4*>(static_cast<float*>(a.O) + at) = make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
@@ -537,7 +545,7 @@ __device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnSeg& g, i
 #pragma unroll
     for (int i = 0; i < CW; ++i) o[i] = 0.f;
     attn_fold<kRowMajor, CW>(a, b0, b1, b0, tiles, tile, rows, row, c, m, l, o);
-    attn_finish<T, CW>(a, attn_out_row(a, g, tok0, row) * a.dim + c, c, l, o);
+    attn_finish<T, CW>(a, g.q, tok0 + row / a.group, attn_out_row(a, g, tok0, row) * a.dim + c, c, l, o);
   }
 }
 

@@ -709,7 +709,7 @@ __global__ void __launch_bounds__(TilesCfg<NS>::kThreads, 1)
           if (whole || fold) {
             float fm = ml, fl = l;
             if (fold) attn_fold<false, 64>(a, b0 + 1, b1, b0, NQ, q, 128, row, 64 * i, fm, fl, v);
-            attn_finish<BF16, 64>(a, out + 64 * i, 64 * i, fl, v);
+            attn_finish<BF16, 64>(a, g.q, my_tok, out + 64 * i, 64 * i, fl, v);
           } else {
 #pragma unroll
             for (int z = 0; z < 64; z += 4)

@@ -428,8 +428,9 @@ gsi_status gsi_cache_append(const gsi_cache_desc* cache, const void* X, gsi_dtyp
  *   not causal: all kv_len keys (window must be 0) -- the cross attention of
  *               a chunk to states of another length.
  * O[i] = sum_j p_j v_j with p = softmax(scale * q_i . k_j) over those keys;
- * a row that sees none gives zeros.  Values outside a row's keys (stale
- * slots, other tokens, whatever they hold) do not reach it.  Q rows are
+ * a row that sees none gives zeros, and one whose scores are all -inf (a key
+ * holds an infinity) gives NaN.  Values outside a row's keys (stale slots,
+ * other tokens, whatever they hold) do not reach it.  Q rows are
  * q_stride elements apart (n_q_heads x head_dim values each, 16-byte aligned);
  * O is N x n_q_heads x head_dim, of the cache's type like Q; its rows outside
  * every request are not written.  q_start must not decrease and stays within

@@ -299,6 +299,29 @@ def test_attention_nonfinite_token_reaches_only_who_sees_it(gsi, dt, D, lens, ba
         assert torch.isfinite(out[first:first + before].float()).all()
 
 
+@pytest.mark.parametrize("dt,hq,D", [(BF, 4, 64), (BF, 4, 128), (BF, 4, 256), (F, 4, 64), (F, 130, 32)])
+@pytest.mark.parametrize("value", [float("inf"), -float("inf")])
+@pytest.mark.parametrize("lens,bad", [([(9, 40)], 36), ([(150, 300)], 200), ([(1, 500), (3, 20)], 18), ([(40, 40)], 0)], ids=str)
+def test_attention_infinite_key(gsi, dt, hq, D, lens, bad, value):
+    # scores of both infinities: a row is NaN where the largest one is, and loses the key where it is the smallest
+    def touch(Q, K, V, table, key_at):
+        pg, o = key_at(len(lens) - 1, bad)
+        K[pg, :, o, 3] = value
+    attention_case(gsi, dt, hq, 2, D, 16, lens, touch=touch)
+
+
+@pytest.mark.parametrize("dt,hq,D", [(BF, 4, 64), (BF, 4, 128), (BF, 4, 256), (F, 4, 64), (F, 130, 32)])
+@pytest.mark.parametrize("window", [0, 20])
+@pytest.mark.parametrize("lens", [[(1, 1)], [(1, 3000), (2, 50)], [(70, 70), (3, 0)], [(300, 900)]], ids=str)
+def test_attention_scores_all_lowest(gsi, dt, hq, D, lens, window):
+    # every score of every second head is -inf, which is no softmax; a row without a key is zeros all the same
+    def touch(Q, K, V, table, key_at):
+        K[..., 3] = float("inf")
+        Q[:, :, 3] = 1.0
+        Q[:, 1::2, 3] = -1.0
+    attention_case(gsi, dt, hq, 2, D, 16, lens, window=window, touch=touch)
+
+
 @pytest.mark.parametrize("dt", [BF, F])
 def test_attention_extreme_scores(gsi, dt):
     # scores of +-1e4: the running maximum grows from tile to tile; scores that fall; all equal
