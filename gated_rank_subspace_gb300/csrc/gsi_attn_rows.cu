@@ -231,6 +231,11 @@ __global__ void __launch_bounds__(RowsCfg<NS>::kThreads, 1)
       for (int x = 0; x < 2; ++x)
 #pragma unroll
         for (int y = 0; y < 2; ++y) sc[x][y] = ex2(sc[x][y] - to);
+      // the weights enter the second product as bf16: 2^-8 of each at most, what rounding to the cache's type costs; what
+      // enters it is what is summed, so that the output is a mean of the values for any rounding
+      const uint32_t p[2] = {attn_pack(sc[0][0], sc[0][1]), attn_pack(sc[1][0], sc[1][1])};
+#pragma unroll
+      for (int x = 0; x < 2; ++x) BF16::unpack2(p[x], sc[x][0], sc[x][1]);
       l = l * f + ((sc[0][0] + sc[0][1]) + (sc[1][0] + sc[1][1]));  // this lane's keys; the lanes of a row are added at the end
       if (__any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll
@@ -239,8 +244,6 @@ __global__ void __launch_bounds__(RowsCfg<NS>::kThreads, 1)
           o[n][1] *= f;
         }
       }
-      // the weights enter the second product as bf16: 2^-8 of each at most, what rounding to the cache's type costs
-      const uint32_t p[2] = {attn_pack(sc[0][0], sc[0][1]), attn_pack(sc[1][0], sc[1][1])};
       {
         const int vr = kg * 16 + (lane & 15);
         const uint32_t base = vb + vr * 128;

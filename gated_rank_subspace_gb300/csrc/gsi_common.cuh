@@ -37,6 +37,10 @@ __device__ __forceinline__ unsigned long long f2_add(unsigned long long a, unsig
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+// a += the lower bf16 of v, b += the upper one, in float32 (where the program says so: not moved across other volatile code).
+__device__ __forceinline__ void add_bf16x2(float& a, float& b, unsigned v) {
+  asm volatile("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tadd.rn.f32.bf16 %0, l, %0;\n\tadd.rn.f32.bf16 %1, h, %1;\n\t}" : "+f"(a), "+f"(b) : "r"(v));
+}
 // The largest of three (NaN is dropped where another is a number, as by fmaxf).
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;

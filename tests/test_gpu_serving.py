@@ -322,6 +322,26 @@ def test_attention_scores_all_lowest(gsi, dt, hq, D, lens, window):
     attention_case(gsi, dt, hq, 2, D, 16, lens, window=window, touch=touch)
 
 
+@pytest.mark.parametrize("D", [64, 128, 192, 256])
+@pytest.mark.parametrize("lens,window", [([(1, 16)], 0), ([(1, 160), (2, 40)], 0), ([(1, 5000), (1, 7)], 0), ([(150, 150)], 0),
+                                         ([(300, 2000), (20, 50)], 0), ([(200, 700)], 100)], ids=str)
+@pytest.mark.parametrize("weight", [0.5 * (1 + 0.98 * 2**-8), 0.5 * (1 + 1.02 * 2**-8), 1 + 0.98 * 2**-8, 1 + 1.02 * 2**-8])
+def test_attention_of_equal_values_is_the_value(gsi, D, lens, window, weight):
+    # A weighted mean of one value is the value.  Most keys have a weight half way between two bf16 values, so all of them
+    # are rounded one way for the product over a bf16 cache: the rounded weights have to be the ones that are summed.
+    # What is left is the float32 rounding of both sums (under 1e-4), far below that of the result.
+    def touch(Q, K, V, table, key_at):
+        V[:] = torch.linspace(1.0, 2.0 - 2**-7, D, device="cuda").to(BF)
+        Q[:], K[:] = 0, 0
+        Q[:, :, 0] = 1.0
+        for r, (_, k) in enumerate(lens):
+            for j in range(0, k, 16):
+                K[key_at(r, j)[0], :, :, 0] = 1.0 if weight < 1 or j >= 128 else 0.0
+                K[key_at(r, j)[0], :, 5, 0] = 0.0 if weight < 1 or j < 128 else 1.0
+    out, O = attention_case(gsi, BF, 4, 2, D, 16, lens, window=window, touch=touch, scale=float(np.log(weight)))
+    assert np.array_equal(f64(out), f64(torch.tensor(O).to(BF)))
+
+
 @pytest.mark.parametrize("dt", [BF, F])
 def test_attention_extreme_scores(gsi, dt):
     # scores of +-1e4: the running maximum grows from tile to tile; scores that fall; all equal
