@@ -89,7 +89,8 @@ struct NormRegs {
 };
 
 // A thread's pieces: their columns (those beyond the row stand on column 0 and
-// count 0 in one[]; their values never leave the thread).
+// count 0 in one[]; their values, which may be those of column 0's weight, bias
+// and gate, never leave the thread).
 template <int VPT>
 struct NormRow {
   int c[VPT];
@@ -158,7 +159,7 @@ __device__ __forceinline__ void norm_token(const NormArgs& a, const NormRow<VPT>
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) h[i][e] = fmaf(a.alpha, h[i][e], y[i][e]) * k.one[i];
+    for (int e = 0; e < 4; ++e) h[i][e] = k.in(i) ? fmaf(a.alpha, h[i][e], y[i][e]) : 0.f;  // (an infinity times 0 is none)
   if (a.H_out) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i)

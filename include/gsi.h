@@ -439,8 +439,9 @@ gsi_status gsi_cache_append(const gsi_cache_desc* cache, const void* X, gsi_dtyp
  * table_width * page_size <= 2^31 - 512, at most 128 query heads a key/value
  * head.
  * Softmax statistics and sums are float32; for GSI_BF16 the weights p enter
- * the second product as bf16, and their sum as they enter it.  max_q is the caller's bound on a request's
- * new tokens (it chooses the kernel; a wrong one costs time, not results).
+ * the second product as bf16, and their sum as they enter it.  max_q is the
+ * caller's bound on a request's new tokens (it chooses the kernel; a wrong one
+ * costs time, not results).
  * workspace: zeroed once (gsi_workspace_init), one stream at a time, at least
  * gsi_paged_attention_workspace_size bytes. */
 size_t gsi_paged_attention_workspace_size(const gsi_cache_desc* cache, int64_t n_q_heads);

@@ -515,6 +515,25 @@ def test_norm(gsi, T, d, post, pre, gate, hdt, ydt, xdt):
     assert ho.dtype == hdt and x.dtype == xdt
 
 
+@pytest.mark.parametrize("T,d", [(1, 8), (3, 1032), (2, 4096), (2, 8200), (700, 64), (340, 1032), (170, 5128), (160, 8192)])
+@pytest.mark.parametrize("from_gate", [False, True])
+def test_norm_infinity_stays_in_its_column(gsi, T, d, from_gate):
+    # an infinite bias or gate of the first column: an RMS norm of the row is 0 elsewhere, whatever the row's length leaves
+    # of the last threads without a value
+    h, y = torch.randn(T, d, device="cuda"), torch.rand(T, d, device="cuda") + 1
+    w, b, gate = torch.ones(d, device="cuda"), torch.randn(d, device="cuda"), torch.ones(d, device="cuda")
+    bad = b.clone()
+    (gate if from_gate else bad)[0] = float("inf")
+    post = None if from_gate else gsi.Norm("rms", w, bad)
+    ho, x = gsi.norm_residual(h, y, post=post, gate=gate, pre=gsi.Norm("rms", w, b), x_dtype=F)
+    with np.errstate(all="ignore"):
+        H, X = so.norm_residual(f64(h), f64(y), 1.0, ("rms", f64(w), f64(bad)) if post else None, f64(gate)[None], None,
+                                ("rms", f64(w), f64(b)))
+    assert np.isinf(H[:, 0]).all() and np.isnan(X[:, 0]).all() and np.isfinite(X[:, 1:]).all()
+    for got, want in ((ho, H), (x, X)):
+        assert np.allclose(f64(got), want, rtol=2e-5, atol=2e-5, equal_nan=True)
+
+
 def test_norm_forms(gsi):
     h = torch.randn(4, 512, device="cuda")
     w = torch.rand(512, device="cuda")
