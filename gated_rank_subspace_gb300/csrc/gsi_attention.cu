@@ -139,13 +139,13 @@ cudaError_t attn_query_map(CUtensorMap* m, const AttnArgs& a, int box_heads, int
 }
 
 int sm_count() {
-  static const int n = [] {
-    int dev = 0, v = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-      return kAttnCtas;
-    return v;
-  }();
-  return n;
+  static std::atomic<int> counts[64];
+  int dev = 0, v = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return kAttnCtas;
+  if ((v = counts[dev].load(std::memory_order_relaxed)) > 0) return v;
+  if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return kAttnCtas;
+  counts[dev].store(v, std::memory_order_relaxed);
+  return v;
 }
 
 size_t attention_work_bytes(gsi_dtype dt, int dim, int group) {

@@ -270,8 +270,9 @@ __global__ void __launch_bounds__(kF32Threads, BM == 16 || NC <= 2 ? 2 : 1) attn
 
 template <int BM, int NC>
 static cudaError_t launch_f32(const AttnArgs& a, cudaStream_t s) {
-  static const cudaError_t ready = attn_prepare_kernel(attn_f32_kernel<BM, NC>, F32Cfg<BM>::smem(256), kF32Threads, 0);
-  if (ready != cudaSuccess) return ready;
+  static OnEveryDevice ready;
+  const cudaError_t e = ready([] { return attn_prepare_kernel(attn_f32_kernel<BM, NC>, F32Cfg<BM>::smem(256), kF32Threads, 0); });
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   const size_t smem = F32Cfg<BM>::smem(a.dim);
   const int per_sm = (BM == 16 || NC <= 2) && 2 * (smem + 2048) <= 233472 ? 2 : 1;  // CTAs that an SM holds

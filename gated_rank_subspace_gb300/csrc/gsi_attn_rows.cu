@@ -361,8 +361,9 @@ static cudaError_t launch_rows(const AttnArgs& a, cudaStream_t s) {
   cudaError_t e = attn_page_map(&mk, a, a.K, box);
   if (e == cudaSuccess) e = attn_page_map(&mv, a, a.V, box);
   if (e != cudaSuccess) return e;
-  static const cudaError_t ready = attn_prepare_kernel(attn_rows_kernel<NS>, C::kSmem, C::kThreads, 72 * 128 + 216 * 256);
-  if (ready != cudaSuccess) return ready;
+  static OnEveryDevice ready;
+  e = ready([] { return attn_prepare_kernel(attn_rows_kernel<NS>, C::kSmem, C::kThreads, 72 * 128 + 216 * 256); });
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(min(sm_count(), kAttnCtas));
   cfg.blockDim = dim3(C::kThreads);

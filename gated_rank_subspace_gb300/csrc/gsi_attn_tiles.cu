@@ -774,8 +774,11 @@ static cudaError_t launch_tiles(const AttnArgs& a, cudaStream_t s) {
   if (e == cudaSuccess) e = attn_page_map(&mk, a, a.K, page < kTileKeys ? page : kTileKeys);
   if (e == cudaSuccess) e = attn_page_map(&mv, a, a.V, page < C::kVK ? page : C::kVK);
   if (e != cudaSuccess) return e;
-  static const cudaError_t ready = attn_prepare_kernel(attn_tiles_kernel<NS>, C::kSmem, C::kThreads, C::kNQ == 2 ? 104 * 128 + 200 * 256 : 0);
-  if (ready != cudaSuccess) return ready;
+  static OnEveryDevice ready;
+  e = ready([] {
+    return attn_prepare_kernel(attn_tiles_kernel<NS>, C::kSmem, C::kThreads, C::kNQ == 2 ? 104 * 128 + 200 * 256 : 0);
+  });
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(min(sm_count(), kAttnCtas));
   cfg.blockDim = dim3(C::kThreads);

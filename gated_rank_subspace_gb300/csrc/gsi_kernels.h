@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/gsi.h"
 #include "gsi_plan.h"
 
@@ -254,9 +256,26 @@ cudaError_t launch_residual_check(const void* X, const void* V, const float* G, 
 cudaError_t launch_image(const void* W, const void* V, void* M, float* gram, int64_t d,
                          int64_t d_out, int64_t k, gsi_dtype dt, cudaStream_t s);
 
-
-// SMs of the current device.
+// SMs of the current device (of the first 64; on another one, or where it cannot be asked, those of a whole GB300).
 int sm_count();
+
+// What a kernel needs once on every device it runs on (its limits belong to a device): calls f on the current device
+// until it has succeeded there.  A failure is returned and not kept.  (Two threads may both call f: it does no harm twice.)
+class OnEveryDevice {
+  std::atomic<uint64_t> done_{0};
+
+ public:
+  template <class F>
+  cudaError_t operator()(F f) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t(1) << dev : 0;
+    if (done_.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    if ((e = f()) == cudaSuccess) done_.fetch_or(bit, std::memory_order_release);
+    return e;
+  }
+};
 
 // Serving operators (see gsi_paged.cu, gsi_norm.cu, gsi_attention.cu).
 struct PlanArgs {

@@ -295,10 +295,11 @@ static bool launch_norm_rows(const NormArgs& a, cudaLaunchConfig_t cfg, cudaErro
   const size_t smem = size_t(params) * a.d * 4 + size_t(kNormAhead + 1) * C::kVpt * threads * 4 * (HT::kBytes + YT::kBytes);
   constexpr size_t kMost = 232448 - 1024;
   if (threads > C::kThreads || smem > kMost) return false;
-  static const cudaError_t ready = cudaFuncSetAttribute(norm_rows_kernel<HT, YT, XT, REGS>,
-                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMost));
-  *e = ready;
-  if (ready != cudaSuccess) return true;
+  static OnEveryDevice ready;
+  *e = ready([] {
+    return cudaFuncSetAttribute(norm_rows_kernel<HT, YT, XT, REGS>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMost));
+  });
+  if (*e != cudaSuccess) return true;
   // CTAs of an SM: what its registers and shared memory hold
   const int per_sm = max(1, min(C::kThreads / threads, int(kMost / (smem + 2048))));
   cfg.gridDim = dim3(min(a.T, sm_count() * per_sm));

@@ -196,9 +196,10 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
 }
 
 cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t s) {
-  static const cudaError_t ready =
-      cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlanSmem);
-  if (ready != cudaSuccess) return ready;
+  static OnEveryDevice ready;
+  const cudaError_t e =
+      ready([] { return cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlanSmem); });
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(max(1, min(sm_count(), a.n_tokens / kPlanTokens)));
   cfg.blockDim = dim3(kPlanThreads);

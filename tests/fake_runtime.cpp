@@ -8,7 +8,7 @@
 //   fail N              the next N cudaFuncSetAttribute calls fail
 //   attention DT GROUP HKV DIM N MAX_Q N_REQ WIDTH PAGE WINDOW
 //   plan N_REQ N_TOKENS
-//   norm T D            (float32 throughout, LAYER / LAYER)
+//   norm T D            (float32 throughout, RMS / RMS)
 // Output, a line a command: {"status": .., "launches": [{"kernel": mangled name,
 // "grid": .., "smem": .., "allowed": the dynamic shared memory that the current device lets that kernel have}]}
 #include <cuda_runtime_api.h>
@@ -95,7 +95,7 @@ static int plan(long long n_req, long long n_tokens) {
                         static_cast<int32_t*>(at(128)), i, nullptr);
 }
 static int norm(long long T, long long d) {
-  const gsi_norm n{GSI_NORM_LAYER, 1e-5f, static_cast<const float*>(P), static_cast<const float*>(P)};
+  const gsi_norm n{GSI_NORM_RMS, 1e-5f, static_cast<const float*>(P), nullptr};
   return gsi_norm_residual(P, GSI_F32, P, GSI_F32, T, d, 1.f, &n, nullptr, 0, nullptr, &n, P, P, GSI_F32, nullptr);
 }
 

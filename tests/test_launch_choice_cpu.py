@@ -75,3 +75,34 @@ def test_attention_hint_beyond_the_tokens_is_their_number(run, dt, group):
     a = run(*[attention(dt, group, 300, h) for h in (0, 1, 300, 301, 2**31, 2**62, 2**63 - 1)])
     names = [r["launches"][0]["kernel"] for r in a]
     assert names[0] == names[1] and len(set(names[2:])) == 1
+
+
+CALLS = {"rows": attention(BF16, 1, 4, 1), "rows, 256 columns": attention(BF16, 1, 4, 1, dim=256),
+         "tiles": attention(BF16, 1, 600, 600), "tiles, 256 columns": attention(BF16, 4, 600, 600, dim=256),
+         "float32, few rows": attention(F32, 1, 4, 1, dim=256), "float32": attention(F32, 1, 6000, 6000, dim=128, width=512),
+         "plan": "plan 40 40000", "norm, registers": "norm 4000 5120", "norm, shared memory": "norm 4000 5128"}
+
+
+@pytest.mark.parametrize("call", CALLS.values(), ids=CALLS)
+def test_every_device_is_set_up(run, call):
+    # what a kernel may have of shared memory, and the number of SMs, belong to the device that is current
+    first, again, _, other, _, back = run(call, call, "device 1", call, "device 0", call)
+    for r in (first, again, other, back):
+        assert r["status"] == 0
+        (launch,) = r["launches"]
+        assert launch["smem"] <= launch["allowed"]
+    grids = [r["launches"][0]["grid"] for r in (first, other, back)]
+    assert grids[0] == grids[2] and grids[0] % 152 == 0 or "plan" in call and grids[0] == 78
+    assert grids[1] % 100 == 0 or "plan" in call and grids[1] == 78
+
+
+@pytest.mark.parametrize("call", CALLS.values(), ids=CALLS)
+def test_a_failed_set_up_is_tried_again(run, call):
+    _, failed, after = run("fail 1", call, call)
+    assert failed["status"] == 3 and not failed["launches"]
+    assert after["status"] == 0 and after["launches"][0]["smem"] <= after["launches"][0]["allowed"]
+
+
+def test_plan_takes_the_device_it_runs_on(run):
+    a, _, b = run("plan 40 1000000", "device 1", "plan 40 1000000")
+    assert a["launches"][0]["grid"] == 152 and b["launches"][0]["grid"] == 100
