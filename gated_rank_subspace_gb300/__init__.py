@@ -472,17 +472,26 @@ _I32, _I64 = torch.int32, torch.int64
 _DTYPES = {torch.float32: GSI_F32, torch.bfloat16: GSI_BF16}
 
 
-def _ints(name, t, n, dtype=_I32):
-    """A contiguous integer CUDA tensor of n elements."""
-    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
-        raise ValueError(f"{name} must be a contiguous CUDA tensor of {n} {dtype}, not {tuple(t.shape)} {t.dtype}")
+def _device(name, t) -> int:
+    """The device of a call's tensors: kernels run on the current one, and only there are its pointers good."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} must be a tensor of the current CUDA device, not of {t.device}")
+    return dev
 
 
-def _like(name, t, shape, dtype):
-    """A contiguous CUDA tensor of this shape and type."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor of {tuple(shape)} {dtype}, "
-                         f"not {tuple(t.shape)} {t.dtype}")
+def _ints(name, t, n, dev, dtype=_I32):
+    """A contiguous integer tensor of n elements on this device."""
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{name} must be a contiguous tensor of {n} {dtype} on cuda:{dev}, "
+                         f"not {tuple(t.shape)} {t.dtype} on {t.device}")
+
+
+def _like(name, t, shape, dtype, dev):
+    """A contiguous tensor of this shape and type on this device."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of {tuple(shape)} {dtype} on cuda:{dev}, "
+                         f"not {tuple(t.shape)} {t.dtype} on {t.device}")
 
 
 def _float_code(t) -> int:
@@ -508,8 +517,8 @@ class PagedCache:
         shape, st = K.shape, K.stride()
         if len(shape) != 4 or V.shape != shape or V.stride() != st or V.dtype is not K.dtype:
             raise ValueError("K and V must be two (pages, heads, page_size, head_dim) tensors of one dtype and layout")
-        if not K.is_cuda or not V.is_cuda or st[3] != 1:
-            raise ValueError("K and V must be CUDA tensors with contiguous head_dim")
+        if not K.is_cuda or V.get_device() != K.get_device() or st[3] != 1:
+            raise ValueError("K and V must be tensors of one CUDA device with contiguous head_dim")
         n, h, p, d = shape
         return CacheDesc(n, p, h, d, _float_code(K), st[0], st[1], st[2], K.data_ptr(), V.data_ptr())
 
@@ -559,18 +568,19 @@ def paged_plan(cached: torch.Tensor, fresh: torch.Tensor, table: torch.Tensor, f
     capacity = free_pages.numel()
     q_start, kv_len, slots, req, pos, left, status = (plan.q_start, plan.kv_len, plan.slots, plan.token_req, plan.positions,
                                                       plan.n_free, plan.status)
-    _ints("cached", cached, R)
-    _ints("fresh", fresh, R)
-    _ints("table", table, R * width)
-    _ints("free_pages", free_pages, capacity)
-    _ints("n_free", n_free, 1)
-    _ints("plan.q_start", q_start, R + 1)
-    _ints("plan.kv_len", kv_len, R)
-    _ints("plan.slots", slots, N, _I64)
-    _ints("plan.token_req", req, N)
-    _ints("plan.positions", pos, N)
-    _ints("plan.n_free", left, 1)
-    _ints("plan.status", status, 1)
+    dev = _device("cached", cached)
+    _ints("cached", cached, R, dev)
+    _ints("fresh", fresh, R, dev)
+    _ints("table", table, R * width, dev)
+    _ints("free_pages", free_pages, capacity, dev)
+    _ints("n_free", n_free, 1, dev)
+    _ints("plan.q_start", q_start, R + 1, dev)
+    _ints("plan.kv_len", kv_len, R, dev)
+    _ints("plan.slots", slots, N, dev, _I64)
+    _ints("plan.token_req", req, N, dev)
+    _ints("plan.positions", pos, N, dev)
+    _ints("plan.n_free", left, 1, dev)
+    _ints("plan.status", status, 1, dev)
     _check(lib().gsi_paged_plan(cached.data_ptr(), fresh.data_ptr(), R, table.data_ptr(), width, free_pages.data_ptr(),
                                 capacity, n_free.data_ptr(), page_size, N, q_start.data_ptr(), kv_len.data_ptr(),
                                 slots.data_ptr(), req.data_ptr(), pos.data_ptr(), left.data_ptr(), status.data_ptr(),
@@ -583,17 +593,19 @@ def cache_append(cache: PagedCache, rows: torch.Tensor, slots: torch.Tensor, n_q
     bfloat16, rows contiguous): keys and values into the cache at `slots`
     (negative: padding), queries to Q (T, n_q_heads, head_dim), returned."""
     c = cache.desc()
+    dev = _device("the cache", cache.K)
     T = slots.numel()
     D = c.head_dim
     st = rows.stride()
-    if rows.shape != (T, (n_q_heads + 2 * c.n_heads) * D) or not rows.is_cuda or (st[1] != 1 and T):
-        raise ValueError(f"rows must be CUDA rows of ({T}, {(n_q_heads + 2 * c.n_heads) * D}), not {tuple(rows.shape)}")
-    _ints("slots", slots, T, _I64)
+    if rows.shape != (T, (n_q_heads + 2 * c.n_heads) * D) or rows.get_device() != dev or (st[1] != 1 and T):
+        raise ValueError(f"rows must be rows of ({T}, {(n_q_heads + 2 * c.n_heads) * D}) on the cache's device, "
+                         f"not {tuple(rows.shape)} on {rows.device}")
+    _ints("slots", slots, T, dev, _I64)
     if Q is None:
         with _on_stream(stream):
             Q = torch.empty(T, n_q_heads, D, dtype=cache.K.dtype, device=rows.device)
     else:
-        _like("Q", Q, (T, n_q_heads, D), cache.K.dtype)
+        _like("Q", Q, (T, n_q_heads, D), cache.K.dtype, dev)
     _check(lib().gsi_cache_append(c, rows.data_ptr(), _float_code(rows), st[0], slots.data_ptr(), T, n_q_heads,
                                   Q.data_ptr(), _raw_stream(stream, rows)))
     return Q
@@ -619,10 +631,11 @@ def paged_attention(cache: PagedCache, Q: torch.Tensor, q_start: torch.Tensor, k
     are not written.  max_q: a bound on a request's new tokens, for the choice
     of kernel.  scale defaults to head_dim ** -0.5."""
     c = cache.desc()
+    dev = _device("the cache", cache.K)
     shape, st = Q.shape, Q.stride()
-    if len(shape) != 3 or not Q.is_cuda or Q.dtype is not cache.K.dtype or shape[2] != c.head_dim:
-        raise ValueError(f"Q must be a (tokens, heads, {c.head_dim}) CUDA tensor of {cache.K.dtype}, "
-                         f"not {tuple(shape)} {Q.dtype}")
+    if len(shape) != 3 or Q.get_device() != dev or Q.dtype is not cache.K.dtype or shape[2] != c.head_dim:
+        raise ValueError(f"Q must be a (tokens, heads, {c.head_dim}) tensor of {cache.K.dtype} on cuda:{dev}, "
+                         f"not {tuple(shape)} {Q.dtype} on {Q.device}")
     N, H, D = shape
     if N and (st[2] != 1 or (H > 1 and st[1] != D)):
         raise ValueError("the heads of a token of Q must be contiguous")
@@ -630,17 +643,19 @@ def paged_attention(cache: PagedCache, Q: torch.Tensor, q_start: torch.Tensor, k
     if table.dim() != 2 or table.shape[0] != R:
         raise ValueError(f"table must be ({R}, pages), not {tuple(table.shape)}")
     width = table.shape[1]
-    _ints("table", table, R * width)
-    _ints("q_start", q_start, R + 1)
-    _ints("kv_len", kv_len, R)
+    _ints("table", table, R * width, dev)
+    _ints("q_start", q_start, R + 1, dev)
+    _ints("kv_len", kv_len, R, dev)
     if out is None:
         with _on_stream(stream):
             out = torch.empty(N, H, D, dtype=Q.dtype, device=Q.device)
     else:
-        _like("out", out, shape, Q.dtype)
+        _like("out", out, shape, Q.dtype, dev)
     if workspace is None:
         with _on_stream(stream):
             workspace = new_workspace(paged_attention_workspace_size(cache, H), Q.device, stream)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}, not on {workspace.device}")
     _check(lib().gsi_paged_attention(c, Q.data_ptr(), st[0], N, H, q_start.data_ptr(), kv_len.data_ptr(),
                                      table.data_ptr(), width, R, N if max_q is None else max_q,
                                      D ** -0.5 if scale is None else scale, 1 if causal else 0, window, out.data_ptr(),
@@ -656,12 +671,12 @@ class Norm:
     bias: torch.Tensor = None
     eps: float = 1e-5
 
-    def desc(self, d: int) -> NormDesc:
+    def desc(self, d: int, dev: int = None) -> NormDesc:
         w, b = self.weight, self.bias
         if w is not None:
-            _like("norm weight", w, (d,), torch.float32)
+            _like("norm weight", w, (d,), torch.float32, max(w.get_device(), 0) if dev is None else dev)
         if b is not None:
-            _like("norm bias", b, (d,), torch.float32)
+            _like("norm bias", b, (d,), torch.float32, max(b.get_device(), 0) if dev is None else dev)
         return NormDesc(NORMS[self.kind], self.eps, None if w is None else w.data_ptr(),
                         None if b is None else b.data_ptr())
 
@@ -675,32 +690,33 @@ def norm_residual(h: torch.Tensor, y: torch.Tensor = None, post: Norm = None, pr
     token_req, for a gate per request).  h_out may be h."""
     shape = h.shape
     T, d = shape
-    if not h.is_cuda or not h.is_contiguous():
-        raise ValueError("h must be a contiguous CUDA tensor")
+    dev = _device("h", h)
+    if not h.is_contiguous():
+        raise ValueError("h must be contiguous")
     if y is not None:
-        _like("y", y, shape, y.dtype)
+        _like("y", y, shape, y.dtype, dev)
     rows = 0
     if gate is not None:
         rows = gate.numel() // d
-        _like("gate", gate, gate.shape[:-1] + (d,), torch.float32)
+        _like("gate", gate, gate.shape[:-1] + (d,), torch.float32, dev)
         if gate_index is not None:
-            _ints("gate_index", gate_index, T)
+            _ints("gate_index", gate_index, T, dev)
         elif rows != 1:
             raise ValueError("a gate of several rows needs gate_index")
     if h_out is None:
         with _on_stream(stream):
             h_out = torch.empty_like(h)
     else:
-        _like("h_out", h_out, shape, h.dtype)
+        _like("h_out", h_out, shape, h.dtype, dev)
     if x is None:
         with _on_stream(stream):
             x = torch.empty(T, d, dtype=x_dtype, device=h.device)
     else:
-        _like("x", x, shape, x.dtype)
+        _like("x", x, shape, x.dtype, dev)
     _check(lib().gsi_norm_residual(h.data_ptr(), _float_code(h), None if y is None else y.data_ptr(),
                                    0 if y is None else _float_code(y), T, d, alpha,
-                                   None if post is None else post.desc(d), None if gate is None else gate.data_ptr(), rows,
+                                   None if post is None else post.desc(d, dev), None if gate is None else gate.data_ptr(), rows,
                                    None if gate_index is None else gate_index.data_ptr(),
-                                   None if pre is None else pre.desc(d), h_out.data_ptr(), x.data_ptr(), _float_code(x),
+                                   None if pre is None else pre.desc(d, dev), h_out.data_ptr(), x.data_ptr(), _float_code(x),
                                    _raw_stream(stream, h)))
     return h_out, x

@@ -3,6 +3,7 @@
 import ctypes
 
 import pytest
+import torch
 
 import __graft_entry__
 
@@ -127,3 +128,89 @@ def test_workspace_size_is_host_arithmetic():
         n = L.gsi_paged_attention_workspace_size(ctypes.byref(cache(**kw)), 4)
         assert 256 <= n <= 96 << 20 and n % 256 == 0
     assert L.gsi_paged_attention_workspace_size(ctypes.byref(cache()), 3) == 0
+
+
+# ------------------------------------------------------------------ devices
+class On:
+    """A tensor that says it lies on a GPU (its data is never read: the injected fault stops every call)."""
+
+    def __init__(self, device, *shape, dtype=torch.int32):
+        self.t, self.device_no = torch.zeros(*shape, dtype=dtype), device
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    is_cuda = property(lambda self: self.device_no >= 0)
+    device = property(lambda self: torch.device("cuda", self.device_no) if self.device_no >= 0 else torch.device("cpu"))
+
+    def get_device(self):
+        return self.device_no
+
+    def data_ptr(self):
+        return P
+
+
+@pytest.fixture
+def current(monkeypatch):
+    """Makes a device current."""
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0, raising=False)
+    return lambda device: monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: device, raising=False)
+
+
+BF, I64 = torch.bfloat16, torch.int64
+SHAPES = {
+    "plan": dict(cached=(2,), fresh=(2,), table=(2, 3), free=(9,), n_free=(1,), q_start=(3,), kv_len=(2,), slots=(4, I64),
+                 token_req=(4,), positions=(4,), left=(1,), status=(1,)),
+    "append": dict(K=(8, 2, 16, 64, BF), V=(8, 2, 16, 64, BF), rows=(4, 512, torch.float32), slots=(4, I64), Q=(4, 4, 64, BF)),
+    "attention": dict(K=(8, 2, 16, 64, BF), V=(8, 2, 16, 64, BF), Q=(4, 4, 64, BF), q_start=(3,), kv_len=(2,), table=(2, 3),
+                      out=(4, 4, 64, BF), workspace=(64 << 20, torch.uint8)),
+    "norm": dict(h=(4, 64, torch.float32), y=(4, 64, torch.float32), w0=(64, torch.float32), b0=(64, torch.float32),
+                 w1=(64, torch.float32), b1=(64, torch.float32), gate=(3, 64, torch.float32), index=(4,),
+                 h_out=(4, 64, torch.float32), x=(4, 64, BF)),
+}
+
+
+def call(op, t):
+    if op == "plan":
+        plan = gsi.PagedPlan(t["q_start"], t["kv_len"], t["slots"], t["token_req"], t["positions"], t["left"], t["status"])
+        plan.kv_len.data_ptr = plan.n_free.data_ptr = lambda: P + 64
+        gsi.paged_plan(t["cached"], t["fresh"], t["table"], t["free"], t["n_free"], 16, plan=plan)
+    elif op == "append":
+        gsi.cache_append(gsi.PagedCache(t["K"], t["V"]), t["rows"], t["slots"], 4, Q=t["Q"])
+    elif op == "attention":
+        gsi.paged_attention(gsi.PagedCache(t["K"], t["V"]), t["Q"], t["q_start"], t["kv_len"], t["table"], out=t["out"],
+                            workspace=t["workspace"])
+    else:
+        gsi.norm_residual(t["h"], t["y"], post=gsi.Norm("layer", t["w0"], t["b0"]), pre=gsi.Norm("layer", t["w1"], t["b1"]),
+                          gate=t["gate"], gate_index=t["index"], h_out=t["h_out"], x=t["x"])
+
+
+def tensors(op, device):
+    made = {}
+    for name, shape in SHAPES[op].items():
+        dtype = shape[-1] if isinstance(shape[-1], torch.dtype) else torch.int32
+        made[name] = On(device, *(s for s in shape if not isinstance(s, torch.dtype)), dtype=dtype)
+    return made
+
+
+@pytest.mark.parametrize("op,name,elsewhere", [(op, name, d) for op in SHAPES for name in [None, *SHAPES[op]]
+                                               for d in ([1] if name is None else [1, -1])])
+def test_tensors_lie_on_the_current_device(current, op, name, elsewhere):
+    # a kernel runs on the device that is current: pointers of another one, or of the host, would fault there
+    made = tensors(op, 0)
+    L.gsi_debug_fail_after(1)
+    try:
+        current(0)
+        if name is None:
+            with pytest.raises(gsi.GsiError, match="injected"):  # all on the current device: reaches the launch
+                call(op, made)
+            L.gsi_debug_fail_after(1)
+            current(elsewhere)
+            with pytest.raises(ValueError, match="device"):
+                call(op, made)
+        else:
+            made[name].device_no = elsewhere
+            with pytest.raises(ValueError):
+                call(op, made)
+    finally:
+        L.gsi_debug_fail_after(0)
