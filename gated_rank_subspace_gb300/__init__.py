@@ -703,6 +703,8 @@ def norm_residual(h: torch.Tensor, y: torch.Tensor = None, post: Norm = None, pr
             _ints("gate_index", gate_index, T, dev)
         elif rows != 1:
             raise ValueError("a gate of several rows needs gate_index")
+        if rows == 0 and T:
+            raise ValueError("a gate needs a row")
     if h_out is None:
         with _on_stream(stream):
             h_out = torch.empty_like(h)

@@ -147,7 +147,7 @@ class On:
         return self.device_no
 
     def data_ptr(self):
-        return P
+        return P if self.t.numel() else 0
 
 
 @pytest.fixture
@@ -214,3 +214,21 @@ def test_tensors_lie_on_the_current_device(current, op, name, elsewhere):
                 call(op, made)
     finally:
         L.gsi_debug_fail_after(0)
+
+
+def test_a_gate_of_no_rows_is_not_no_gate(current):
+    # an empty tensor has no address, which to the library is "no gate": a gate of 1, where no index is right
+    current(0)
+    made = tensors("norm", 0)
+    made["gate"] = On(0, 0, 64, dtype=torch.float32)
+    L.gsi_debug_fail_after(1)
+    try:
+        with pytest.raises(ValueError, match="gate"):
+            call("norm", made)
+    finally:
+        L.gsi_debug_fail_after(0)
+    # no tokens ask for no rows
+    for name, shape in SHAPES["norm"].items():
+        if shape[0] == 4:
+            made[name] = On(0, 0, *(s for s in shape[1:-1]), dtype=shape[-1]) if len(shape) > 1 else On(0, 0)
+    call("norm", made)
