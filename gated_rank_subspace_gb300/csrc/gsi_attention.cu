@@ -129,8 +129,7 @@ cudaError_t attn_query_map(CUtensorMap* m, const AttnArgs& a, int box_heads, int
   const AttnEncodeFn fn = attn_encode_fn();
   if (!fn) return cudaErrorNotSupported;
   const cuuint64_t dim[3] = {cuuint64_t(a.dim), cuuint64_t(a.hkv) * a.group, cuuint64_t(a.N)};
-  const int64_t row = a.N > 1 ? a.q_stride : int64_t(a.dim) * a.hkv * a.group;
-  const cuuint64_t bytes[2] = {cuuint64_t(a.dim) * 2, cuuint64_t(row) * 2};
+  const cuuint64_t bytes[2] = {cuuint64_t(a.dim) * 2, cuuint64_t(a.q_stride) * 2};
   const cuuint32_t box[3] = {64, cuuint32_t(box_heads), cuuint32_t(box_tokens)}, es[3] = {1, 1, 1};
   const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.Q), dim, bytes, box, es,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

@@ -151,6 +151,7 @@ gsi_status gsi_cache_append(const gsi_cache_desc* cache, const void* X, gsi_dtyp
     return refuse(GSI_ERR_UNSUPPORTED, "more than 2^24 tokens or 4096 heads");
   if (T == 0) return record_error(GSI_OK, "");
   const int64_t values = (n_q_heads + 2 * cache->n_heads) * cache->head_dim;
+  if (T == 1) row_stride = 0;  // there is no next row
   if (row_stride < values && T > 1)
     return refuse(GSI_ERR_INVALID_ARG, "row_stride=%lld is below the row's %lld values", (long long)row_stride, (long long)values);
   if ((row_stride * elem(xdt)) % 16) return refuse(GSI_ERR_UNSUPPORTED, "row_stride is not a multiple of 16 bytes");
@@ -205,7 +206,8 @@ gsi_status gsi_paged_attention(const gsi_cache_desc* cache, const void* Q, int64
     return refuse(GSI_ERR_UNSUPPORTED, "more than 2^24 tokens, 2^20 requests or 2^31 - 512 places of a request");
   if (N == 0 || n_req == 0) return record_error(GSI_OK, "");
   const int64_t values = n_q_heads * cache->head_dim;
-  if (q_stride < values && N > 1)
+  if (N == 1) q_stride = values;  // there is no next row
+  if (q_stride < values)
     return refuse(GSI_ERR_INVALID_ARG, "q_stride=%lld is below the row's %lld values", (long long)q_stride, (long long)values);
   if ((q_stride * elem(cache->dtype)) % 16) return refuse(GSI_ERR_UNSUPPORTED, "q_stride is not a multiple of 16 bytes");
   if (q_stride >= int64_t(1) << 38) return refuse(GSI_ERR_UNSUPPORTED, "q_stride is above 2^38");

@@ -408,11 +408,11 @@ gsi_status gsi_paged_plan(const int32_t* cached, const int32_t* fresh, int64_t n
                           int32_t* token_req, int32_t* positions, int32_t* n_free_out, int32_t* status, void* stream);
 
 /* The rows of a qkv map (gsi_linear's Y, or any T x (n_q_heads + 2 n_heads) *
- * head_dim rows of type xdt, row_stride elements apart): the first n_q_heads *
- * head_dim values of a row are its queries and go to Q (T x n_q_heads x
- * head_dim, the cache's type; Q may be NULL, then they are left out), the
- * next n_heads * head_dim its keys and the last its values, which go to the
- * cache at slots[t].  float32 rows are rounded to nearest even into a bf16
+ * head_dim rows of type xdt, row_stride elements apart, a multiple of 16 bytes
+ * where there are several): the first n_q_heads * head_dim values of a row are
+ * its queries and go to Q (T x n_q_heads x head_dim, the cache's type; Q may
+ * be NULL, then they are left out), the next n_heads * head_dim its keys and
+ * the last its values, which go to the cache at slots[t].  float32 rows are rounded to nearest even into a bf16
  * cache.  Tokens whose slot lies outside the cache (negative: padding) leave
  * the cache as it is; their queries are still written.  Slots are distinct. */
 gsi_status gsi_cache_append(const gsi_cache_desc* cache, const void* X, gsi_dtype xdt, int64_t row_stride,
@@ -431,7 +431,8 @@ gsi_status gsi_cache_append(const gsi_cache_desc* cache, const void* X, gsi_dtyp
  * a row that sees none gives zeros, and one whose scores are all -inf (a key
  * holds an infinity) gives NaN.  Values outside a row's keys (stale slots,
  * other tokens, whatever they hold) do not reach it.  Q rows are
- * q_stride elements apart (n_q_heads x head_dim values each, 16-byte aligned);
+ * q_stride elements apart (n_q_heads x head_dim values each, 16-byte aligned;
+ * of a single row q_stride means nothing);
  * O is N x n_q_heads x head_dim, of the cache's type like Q; its rows outside
  * every request are not written.  q_start must not decrease and stays within
  * N; kv_len stays within table_width * page_size (a longer one is cut there);

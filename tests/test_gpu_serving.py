@@ -484,6 +484,20 @@ def test_attention_any_hint(gsi, dt, group):
             attention_case(gsi, dt, 2 * group, 2, 64, 16, lens, max_q=max_q)
 
 
+@pytest.mark.parametrize("dt,hq", [(BF, 4), (BF, 32), (F, 4), (F, 130)])
+def test_one_row_of_any_stride(gsi, dt, hq):
+    # a view of one row: its stride, that of a matrix of odd width, is never used
+    cache = gsi.PagedCache(*(torch.randn(3, 2, 16, 32, device="cuda").to(dt) for _ in range(2)))
+    wide = torch.randn((hq + 4) * 32 + 3, device="cuda")
+    rows = wide.as_strided((1, (hq + 4) * 32), ((hq + 4) * 32 + 3, 1))
+    slots = torch.tensor([20], device="cuda")
+    Q = gsi.cache_append(cache, rows, slots, hq)
+    assert torch.equal(cache.K[1, :, 4], rows[0, hq * 32:(hq + 2) * 32].view(2, 32).to(dt))
+    args = i32([0, 1]), i32([40]), i32([[2, 1, 0]])
+    odd = torch.empty(hq * 32 + 1, dtype=dt, device="cuda")[:hq * 32].copy_(Q.view(-1)).as_strided((1, hq, 32), (hq * 32 + 1, 32, 1))
+    assert torch.equal(gsi.paged_attention(cache, odd, *args), gsi.paged_attention(cache, Q, *args))
+
+
 # ------------------------------------------------------------------ norm
 @pytest.mark.parametrize("T,d", [(1, 8), (3, 256), (5, 4096), (2, 5120), (17, 1032), (3, 16384), (2, 8200),
                                  (153, 5120), (340, 1032), (170, 5128), (160, 8192), (700, 64)])

@@ -232,3 +232,11 @@ def test_a_gate_of_no_rows_is_not_no_gate(current):
         if shape[0] == 4:
             made[name] = On(0, 0, *(s for s in shape[1:-1]), dtype=shape[-1]) if len(shape) > 1 else On(0, 0)
     call("norm", made)
+
+
+def test_the_stride_of_one_row_means_nothing():
+    # a single row has no next one: whatever its stride says, as of a view's row
+    for stride in (0, 1, 513, -8, 1 << 40):
+        reaches_launch(append, T=1, stride=stride)
+        reaches_launch(attention, N=1, q_stride=stride)
+        reaches_launch(attention, c=cache(dt=0), N=1, q_stride=stride)
