@@ -71,6 +71,14 @@ static gsi_status check_cache(const gsi_cache_desc* c) {
   return GSI_OK;
 }
 
+static gsi_status check_heads(const gsi_cache_desc* c, int64_t n_q_heads) {
+  if (n_q_heads <= 0 || n_q_heads % c->n_heads)
+    return refuse(GSI_ERR_INVALID_ARG, "n_q_heads=%lld is not a multiple of the cache's %lld heads", (long long)n_q_heads,
+                  (long long)c->n_heads);
+  if (n_q_heads / c->n_heads > 128) return refuse(GSI_ERR_UNSUPPORTED, "more than 128 query heads share a key/value head");
+  return GSI_OK;
+}
+
 static gsi_status check_norm(const gsi_norm* n, const char* name) {
   if (!n) return GSI_OK;
   if (n->kind != GSI_NORM_NONE && n->kind != GSI_NORM_RMS && n->kind != GSI_NORM_LAYER)
@@ -180,7 +188,8 @@ gsi_status gsi_cache_append(const gsi_cache_desc* cache, const void* X, gsi_dtyp
 }
 
 size_t gsi_paged_attention_workspace_size(const gsi_cache_desc* cache, int64_t n_q_heads) {
-  if (check_cache(cache) != GSI_OK || n_q_heads <= 0 || n_q_heads % cache->n_heads) return 0;
+  if (check_cache(cache) != GSI_OK || check_heads(cache, n_q_heads) != GSI_OK) return 0;
+  record_error(GSI_OK, "");
   return attention_work_bytes(cache->dtype, int(cache->head_dim), int(n_q_heads / cache->n_heads));
 }
 
@@ -193,11 +202,7 @@ gsi_status gsi_paged_attention(const gsi_cache_desc* cache, const void* Q, int64
   if (N < 0 || n_req < 0 || table_width < 0 || max_q < 0)
     return refuse(GSI_ERR_INVALID_ARG, "a size is negative (N=%lld n_req=%lld table_width=%lld max_q=%lld)", (long long)N,
                   (long long)n_req, (long long)table_width, (long long)max_q);
-  if (n_q_heads <= 0 || n_q_heads % cache->n_heads)
-    return refuse(GSI_ERR_INVALID_ARG, "n_q_heads=%lld is not a multiple of the cache's %lld heads", (long long)n_q_heads,
-                  (long long)cache->n_heads);
-  if (n_q_heads / cache->n_heads > 128)
-    return refuse(GSI_ERR_UNSUPPORTED, "more than 128 query heads share a key/value head");
+  if ((s = check_heads(cache, n_q_heads)) != GSI_OK) return s;
   if (!std::isfinite(scale)) return refuse(GSI_ERR_INVALID_ARG, "scale must be finite");
   if (window < 0 || (window > 0 && !causal))
     return refuse(GSI_ERR_INVALID_ARG, "window must be >= 0, and 0 where the attention is not causal");

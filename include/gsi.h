@@ -444,7 +444,8 @@ gsi_status gsi_cache_append(const gsi_cache_desc* cache, const void* X, gsi_dtyp
  * caller's bound on a request's new tokens (it chooses the kernel; a wrong one
  * costs time, not results).
  * workspace: zeroed once (gsi_workspace_init), one stream at a time, at least
- * gsi_paged_attention_workspace_size bytes. */
+ * gsi_paged_attention_workspace_size bytes (0, and a message, where the
+ * attention would refuse the cache or the heads). */
 size_t gsi_paged_attention_workspace_size(const gsi_cache_desc* cache, int64_t n_q_heads);
 gsi_status gsi_paged_attention(const gsi_cache_desc* cache, const void* Q, int64_t q_stride, int64_t N,
                                int64_t n_q_heads, const int32_t* q_start, const int32_t* kv_len,

@@ -240,3 +240,11 @@ def test_the_stride_of_one_row_means_nothing():
         reaches_launch(append, T=1, stride=stride)
         reaches_launch(attention, N=1, q_stride=stride)
         reaches_launch(attention, c=cache(dt=0), N=1, q_stride=stride)
+
+
+@pytest.mark.parametrize("heads,needle", [(3, "multiple"), (0, "multiple"), (-2, "multiple"), (258, "128"), (2 << 32, "128")])
+def test_workspace_of_a_refused_shape_says_why(heads, needle):
+    attention(scale=NAN)  # an earlier error is not this one
+    n = L.gsi_paged_attention_workspace_size(ctypes.byref(cache()), heads)
+    refused(1 if n == 0 else 0, 1, needle)
+    assert L.gsi_paged_attention_workspace_size(ctypes.byref(cache()), 4) > 0 and L.gsi_last_error() == b""
