@@ -166,7 +166,7 @@ cudaError_t launch_paged_attention(const AttnArgs& a, gsi_dtype dt, int64_t max_
     // 64-row units that do not fill the chip are too long a chain each (there are at most `tiles` of their tiles here):
     // 64 tokens, window 128, 4 x 64 16 us with 16 rows, 24 with 64; 100 of 500, 4 requests of 4 x 64 25 and 28; but 100
     // of 1000, 4 requests of 8 / 4 x 128 75 and 70, 128 of 1000, 8 requests of 8 x 64 86 and 62
-    const int64_t keys = std::min<int64_t>(a.width << a.page_shift, a.window > 0 ? a.window + 128 : int64_t(1) << 31);
+    const int64_t keys = std::min<int64_t>(a.width << a.page_shift, a.window > 0 ? int64_t(a.window) + 128 : int64_t(1) << 31);
     const int64_t tiles = (int64_t(a.N) * a.group / 64 + 1) * a.hkv * (keys / 64 + 1);
     return launch_attn_f32(a, most <= 16 || (a.group <= 16 && tiles < kF32FewTiles), s);
   }

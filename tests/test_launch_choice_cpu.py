@@ -106,3 +106,10 @@ def test_a_failed_set_up_is_tried_again(run, call):
 def test_plan_takes_the_device_it_runs_on(run):
     a, _, b = run("plan 40 1000000", "device 1", "plan 40 1000000")
     assert a["launches"][0]["grid"] == 152 and b["launches"][0]["grid"] == 100
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_a_window_that_hides_nothing_changes_nothing(run, dt):
+    # 2^31 - 1 keys are more than a request can have
+    a, *b = run(*[attention(dt, 1, 6000, 6000, dim=128, width=512, window=w) for w in (0, 2**31 - 129, 2**31 - 128, 2**31 - 1, 2**31)])
+    assert all(r["launches"][0]["kernel"] == a["launches"][0]["kernel"] for r in b)
