@@ -163,9 +163,12 @@ cudaError_t launch_paged_attention(const AttnArgs& a, gsi_dtype dt, int64_t max_
   const int64_t most = std::clamp<int64_t>(max_q, 1, a.N) * a.group;
   if (dt == GSI_BF16) return most <= 8 ? launch_attn_rows(a, s) : launch_attn_tiles(a, s);
   if (a.group <= 64) {
-    // 64-row units that do not fill the chip are too long a chain each (there are at most `tiles` of their tiles here):
-    // 64 tokens, window 128, 4 x 64 16 us with 16 rows, 24 with 64; 100 of 500, 4 requests of 4 x 64 25 and 28; but 100
-    // of 1000, 4 requests of 8 / 4 x 128 75 and 70, 128 of 1000, 8 requests of 8 x 64 86 and 62
+    // 64-row units that do not fill the chip are too long a chain each.  `tiles` is what their tiles would be if rows filled
+    // them: an estimate, which leaves out each request's part of a unit (whose empty rows the 16-row units save).  16 and 64
+    // rows, us: 64 tokens, window 128, 4 x 64 16 and 24; 100 of 500, 4 requests of 4 x 64 27 and 29; 17 of 500, 100 requests of
+    // 1 x 64 26 and 36; 17 of 2000, 24 requests 26 and 35; but 17 of 500, 60 requests 25 and 22; and beyond the rule's bound
+    // 100 of 1000, 4 requests of 8 / 4 x 128 77 and 71, 128 of 1000, 8 requests of 8 x 64 90 and 62, 60 of 800, 6 requests of
+    // 8 / 2 x 32 33 and 22, 64 of 500, 16 requests of 4 / 2 x 128 43 and 47
     const int64_t keys = std::min<int64_t>(a.width << a.page_shift, a.window > 0 ? int64_t(a.window) + 128 : int64_t(1) << 31);
     const int64_t tiles = (int64_t(a.N) * a.group / 64 + 1) * a.hkv * (keys / 64 + 1);
     return launch_attn_f32(a, most <= 16 || (a.group <= 16 && tiles < kF32FewTiles), s);
