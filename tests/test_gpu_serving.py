@@ -529,6 +529,31 @@ def test_norm(gsi, T, d, post, pre, gate, hdt, ydt, xdt):
     assert ho.dtype == hdt and x.dtype == xdt
 
 
+@pytest.mark.parametrize("T,d,hdt,ydt,xdt", [(1500, 5120, F, F, BF), (1500, 5120, BF, BF, F), (1525, 4104, F, BF, BF), (27400, 64, F, F, F),
+                                             (4000, 1032, BF, F, BF), (1400, 5128, BF, F, BF), (1400, 5128, F, F, F),
+                                             (1400, 8192, BF, BF, BF)])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("gate", ["row", "index"])
+def test_norm_many_rows_a_cta(gsi, T, d, hdt, ydt, xdt, kind, gate):
+    # CTAs that stay copy three rows ahead into a ring of four: nine rows and more of each, so that every slot is filled
+    # and read again, with the weights in registers and, above 5120 values, in shared memory; the residual in place
+    g = torch.Generator(device="cuda").manual_seed(d + T)
+    r = lambda *s: torch.randn(*s, device="cuda", generator=g)  # noqa: E731
+    h, y = (r(T, d) + 0.5).to(hdt), (2 * r(T, d) - 3.0).to(ydt)
+    w, b = [1 + 0.2 * r(d), 1 + 0.2 * r(d)], [None, None] if kind == "rms" else [r(d), r(d)]
+    gates = r(d) if gate == "row" else r(T // 7, d)
+    index = None if gate == "row" else torch.randint(-1, T // 7 + 1, (T,), device="cuda", generator=g).int()
+    H, X = so.norm_residual(f64(h), f64(y), 0.75, (kind, f64(w[0]), None if b[0] is None else f64(b[0]), 1e-5),
+                            f64(gates).reshape(-1, d), None if index is None else index.tolist(),
+                            (kind, f64(w[1]), None if b[1] is None else f64(b[1]), 1e-5))
+    ho, x = gsi.norm_residual(h, y, post=gsi.Norm(kind, w[0], b[0]), pre=gsi.Norm(kind, w[1], b[1]), gate=gates, gate_index=index,
+                              alpha=0.75, h_out=h, x_dtype=xdt)
+    assert ho.data_ptr() == h.data_ptr()
+    for got, want in ((ho, H), (x, X)):
+        tol = 2e-5 * (1 + np.abs(want)) + (2**-8 * np.abs(want) if got.dtype == BF else 0)
+        assert (np.abs(f64(got) - want) <= tol).all()
+
+
 @pytest.mark.parametrize("T,d", [(1, 8), (3, 1032), (2, 4096), (2, 8200), (700, 64), (340, 1032), (170, 5128), (160, 8192)])
 @pytest.mark.parametrize("from_gate", [False, True])
 def test_norm_infinity_stays_in_its_column(gsi, T, d, from_gate):
