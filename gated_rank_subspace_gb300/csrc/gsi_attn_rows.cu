@@ -36,7 +36,7 @@ struct RowsCfg {
   static constexpr int kStage = 2 * NS * kSlab;          // K slabs, then V slabs
   static constexpr int kStages = 196608 / kStage;        // 192 KB
   static constexpr int kDim = NS * 64;
-  static constexpr size_t kSmem = 1024 + size_t(kStages) * kStage + kShared * kDim * 4 + kKeyWarps * 32 * 4 + 2 * kStages * 8 + 16;
+  static constexpr size_t kSmem = 1024 + size_t(kStages) * kStage + kShared * kDim * 4 + kKeyWarps * 16 * 4 + 2 * kStages * 8 + 16;
 };
 
 __device__ __forceinline__ void rows_ldsm(uint32_t addr, uint32_t (&r)[4]) {
@@ -83,8 +83,8 @@ __global__ void __launch_bounds__(RowsCfg<NS>::kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* s_o = reinterpret_cast<float*>(ring + size_t(C::kStages) * C::kStage);  // [16][kDim]
-  float* s_ml = s_o + C::kShared * C::kDim;                                            // [keys' warp][m: 16, l: 16]
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_ml + KW * 32);
+  float* s_ml = s_o + C::kShared * C::kDim;                                      // [keys' warp][m: 8, l: 8]
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_ml + KW * 16);
   uint64_t* empty = full + C::kStages;
   int* s_flag = reinterpret_cast<int*>(empty + C::kStages);
 
@@ -270,15 +270,15 @@ __global__ void __launch_bounds__(RowsCfg<NS>::kThreads, 1)
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
     if (dh == 0 && (lane & 3) == 0) {
-      s_ml[kg * 32 + r0] = m;
-      s_ml[kg * 32 + 16 + r0] = l;
+      s_ml[kg * 16 + r0] = m;
+      s_ml[kg * 16 + 8 + r0] = l;
     }
     if (found) s_flag[1] = 1;
     rows_sync<NW * 32>();
     const bool any = s_flag[1] != 0;
     float mx = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < KW; ++w) mx = fmaxf(mx, s_ml[w * 32 + r0]);
+    for (int w = 0; w < KW; ++w) mx = fmaxf(mx, s_ml[w * 16 + r0]);
     const float mine = attn_scale(m, mx);  // this warp's factor
     const int copies = min(KW, C::kShared / n_rows), rounds = (KW + copies - 1) / copies;
     for (int round = 0; round < rounds; ++round) {
@@ -307,9 +307,9 @@ __global__ void __launch_bounds__(RowsCfg<NS>::kThreads, 1)
       const int row = e / vec, c = (e - row * vec) * 8;
       float mx = -INFINITY, sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < KW; ++w) mx = fmaxf(mx, s_ml[w * 32 + row]);
+      for (int w = 0; w < KW; ++w) mx = fmaxf(mx, s_ml[w * 16 + row]);
 #pragma unroll
-      for (int w = 0; w < KW; ++w) sum += s_ml[w * 32 + 16 + row] * attn_scale(s_ml[w * 32 + row], mx);
+      for (int w = 0; w < KW; ++w) sum += s_ml[w * 16 + 8 + row] * attn_scale(s_ml[w * 16 + row], mx);
       float v[8];
 #pragma unroll
       for (int x = 0; x < 8; ++x) v[x] = s_o[row * C::kDim + c + x];
