@@ -456,6 +456,7 @@ def stack_raw(args, n, T, eps, workspace, stream=None, mode: str = "auto"):
 # step's tokens, the paged key/value cache, attention over it, and the norms
 # with gate and residual.  Outputs and workspaces may be passed in (a serving
 # loop keeps them); what is not passed is allocated by PyTorch on `stream`.
+# All tensors of a call lie on the current CUDA device.
 
 PLAN_BAD_LENGTH, PLAN_TABLE_FULL, PLAN_NO_PAGES, PLAN_TOO_MANY_TOKENS = 1, 2, 4, 8
 NORMS = {"none": 0, "rms": 1, "layer": 2}
@@ -627,9 +628,12 @@ def paged_attention(cache: PagedCache, Q: torch.Tensor, q_start: torch.Tensor, k
     by paged_plan; returns out (N, heads, head_dim).  causal: the new tokens are
     the last ones of the request's kv_len keys; window > 0: a token sees only
     that many keys, its own the last.  causal=False: every key (cross attention
-    to cached states).  A row that sees no key gives zeros; rows of no request
-    are not written.  max_q: a bound on a request's new tokens, for the choice
-    of kernel.  scale defaults to head_dim ** -0.5."""
+    to cached states).  A row that sees no key gives zeros (one whose scores are
+    all -inf NaN); rows of no request are not written.  max_q: a bound on a
+    request's new tokens, for the choice of kernel (a wrong one costs time, not
+    results).  scale defaults to head_dim ** -0.5.  Without a workspace every
+    call allocates and zeroes one (some 40 MB at 128 columns): a serving loop
+    keeps one, of paged_attention_workspace_size bytes from new_workspace."""
     c = cache.desc()
     dev = _device("the cache", cache.K)
     shape, st = Q.shape, Q.stride()

@@ -228,8 +228,8 @@ struct AttnShare {
 // One causal request alone has units that shrink with their place.  They are
 // dealt out whole, the longest first, back and forth over the CTAs, where the
 // longest hand is at most what the line's cuts cost (kAttnCut tiles, and an
-// eighth: neighbours on the line wait for each other's parts) above the mean: no
-// unit is cut then.  2048 tokens of 16 x 256 (16 tiles at most, 14.3 the mean):
+// eighth: parts are written, read and folded) above the mean: no unit is cut
+// then.  2048 tokens of 16 x 256 (16 tiles at most, 14.3 the mean):
 // 41 us, on the line 49; 4096 of 40 x 128 (90, 80) 162, on the line 175; 8192 of
 // 32 x 128 394, on the line 417; but 1000 behind 4000 of 40 x 128 (73, 39) 133,
 // on the line 93.
@@ -284,7 +284,13 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, int ut, int k
   s.total = total;
   s.grid = int(total < (long long)gridDim.x ? total : (long long)gridDim.x);
   if (total > s.grid && total < 16 * s.grid) {
-    // as few CTAs as leave the longest share as it is: 512 tiles are 4 for 128 CTAs and for 152, with fewer parts to join
+    // As few CTAs as leave the longest share as it is (512 tiles are 4 for 128 CTAs and for 152): fewer parts to join, and
+    // shares that often end where units do.  Without and with, us: one token over 2048 keys of 16 x 256 17.4 and 14.6, over
+    // 3000 of 16 x 128 20.0 and 13.9, 5000 21.4 and 15.5, 2500 of 40 x 128 24.5 and 21.5, 8000 of 32 x 128 35.3 and 34.2;
+    // 128 tokens over 4000 keys of 8 x 256 79 and 69; float32, 100 of 900 keys, 2 requests of 8 / 4 x 128 63.7 and 61.8.
+    // But 10,000 keys of 8 x 64 14.2 and 16.7, 20,000 16.5 and 19.0, and 200 tokens of 1500 keys, 2 requests of 32 / 8 x
+    // 128, 33.5 and 40.3 (row tiles' parts that all end at once are not there when the first one looks for them).  From 16
+    // tiles a share on the longest is within a sixteenth of the mean.
     const unsigned tiles = unsigned(total), most = (tiles + s.grid - 1) / unsigned(s.grid);
     s.grid = int((tiles + most - 1) / most);
   }

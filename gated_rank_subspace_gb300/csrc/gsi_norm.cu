@@ -17,9 +17,9 @@ namespace gsi {
 //
 // Few tokens are latency: a CTA a token (one of 4096: 2.5 us).  Many are bytes, and a CTA a token
 // waits for its first loads and its weights most of its life: there the CTAs
-// stay, keep the weights in shared memory and copy the rows to come ahead of
-// the one they work on, each thread its own pieces, so that no barrier guards
-// them.
+// stay, keep the weights (in registers, or for wider rows in shared memory) and
+// copy the rows to come ahead of the one they work on, each thread its own
+// pieces, so that no barrier guards them.
 __device__ __forceinline__ float norm_block_sum(float v, float* red) {
   v = warp_sum(v);
   const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
@@ -198,8 +198,13 @@ __global__ void __launch_bounds__(1024, 1) norm_token_kernel(const __grid_consta
 // 5120 values), or, where wider rows leave no room for them, in shared memory
 // before the rows (four pieces a thread): 2049 x 5120 LAYER takes 36 us (4.1
 // TB/s) the first way and 42 us the second, whose fewer warps wait on each other
-// longer.  What is left is the row's own chain: up to four reductions of ~400
-// cycles, and ~460 instructions a warp.
+// longer.  What is left is the row's own chain, with one row in work a CTA: up to
+// four reductions of ~400 cycles, and ~460 instructions a warp.  Staying CTAs and
+// a CTA a token, us: 2049 x 5120 LAYER 37 and 56, RMS 33 and 44 (a gate a
+// request each), 2049 x 5128 RMS (shared memory) 30 and 41, 2048 x 4096 LAYER 29
+// and 52, 2048 x 6144 LAYER of bf16 rows 38 and 61.  Rows that neither form
+// holds take a CTA a token: 2048 x 8192 LAYER 77, 2048 x 16384 125 (of 35 and 69
+// us of bytes).
 constexpr int kNormAhead = 3;
 template <bool REGS>
 struct NormRowsCfg {
