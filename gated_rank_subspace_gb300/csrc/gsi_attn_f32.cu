@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kF32Threads, BM == 16 || NC <= 2 ? 2 : 1) attn
       for (int i = 0; i < RM; ++i) {
         const int row = tr * RM + i;
         if (row >= n_rows) continue;
-        const float inv = !whole ? 1.f : attn_inverse(a, g.q, tok0 + row / a.group, l[i]);
+        const float inv = !whole ? 1.f : l[i] != 0.f ? 1.f / l[i] : lim[i] > 0 ? NAN : 0.f;  // as attn_inverse
         if (!whole && c0 == 0) {
           part[row] = m[i] == -INFINITY ? m[i] : m[i] * c;
           part[BM + row] = l[i];
