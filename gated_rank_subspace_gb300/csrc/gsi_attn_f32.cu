@@ -16,8 +16,8 @@ namespace gsi {
 // Values a masked tile hides are set to zero in shared memory as they arrive
 // where no row sees their key, and where they are not finite (added at the end
 // for the rows that do see them).
-// 2048 tokens of 16 x 64: 325 us, 26 TFLOP/s of what the mask leaves; one token
-// over 100,000 keys of 8 x 128: 376 us, 2.2 TB/s (the shared-memory loads of 2 x 2
+// 2048 tokens of 16 x 64: 317 us, 27 TFLOP/s of what the mask leaves; one token
+// over 100,000 keys of 8 x 128: 372 us, 2.2 TB/s (the shared-memory loads of 2 x 2
 // tiles).
 constexpr int kF32Keys = 64, kF32Threads = 256;
 

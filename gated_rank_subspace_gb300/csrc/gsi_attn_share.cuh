@@ -226,10 +226,10 @@ struct AttnShare {
 // dealt out whole, the longest first, back and forth over the CTAs, where the
 // longest hand is at most what the line's cuts cost (kAttnCut tiles, and an
 // eighth: parts are written, read and folded) above the mean: no unit is cut
-// then.  2048 tokens of 16 x 256 (16 tiles at most, 14.3 the mean):
-// 41 us, on the line 49; 4096 of 40 x 128 (90, 80) 162, on the line 175; 8192 of
-// 32 x 128 394, on the line 417; but 1000 behind 4000 of 40 x 128 (73, 39) 133,
-// on the line 93.
+// then.  2048 tokens of 16 x 256 (16 tiles at most, 14.3 the mean): 42 us, on the
+// line 52; 4096 of 40 x 128 (90, 80) 159, on the line 176; 8192 of 32 x 128 401, on
+// the line 429, of 16 x 256 422 and 448, but of 32 x 64 364 and 356; 1000 behind
+// 4000 of 40 x 128 (73, 39), left on the line, 91, dealt out 122.
 constexpr int kAttnCut = 5, kAttnDealRows = 16;
 __device__ __forceinline__ int attn_dealt(int k, int cta, int n_cta) {  // a hand's k-th unit
   return k * n_cta + (k & 1 ? n_cta - 1 - cta : cta);
