@@ -523,6 +523,12 @@ __global__ void __launch_bounds__(TilesCfg<NS>::kThreads, 1)
     const uint32_t o_at = tmem + lanes + C::kOCol + q * 128;
     int ks = 0, seg = 0;
     uint32_t ph_pv = 0;  // two row tiles: the segments that ended
+    // One row tile: the product of the tile before number ks is done.  A parity tells one phase from its neighbours only,
+    // so every phase is seen: a tile's weights are handed over whole (its own product cannot end before) after the
+    // product of the tile before, and at the segment's end just the last one is out.
+    auto product_before = [&]() {
+      return ks == 0 || __all_sync(0xffffffffu, bar_wait(&bars.pv_done[0], uint32_t(ks - 1) & 1u, err));
+    };
     while (walk.next(a, g)) {  // after a wait that gave up too: the warps of a row tile meet at barriers
       t.set(a, g, tpt);
       const int this_seg = seg++;
@@ -578,7 +584,7 @@ __global__ void __launch_bounds__(TilesCfg<NS>::kThreads, 1)
           if (j > ja) {
             // O has to be complete up to the tile before.  With two row tiles this S was made after that product.
             if constexpr (NQ == 1) {
-              ok = __all_sync(0xffffffffu, bar_wait(&bars.pv_done[0], uint32_t(ks - 1) & 1u, err));
+              ok = product_before();
               if (!ok) continue;
               tl_fence_after();
             }
@@ -630,6 +636,10 @@ __global__ void __launch_bounds__(TilesCfg<NS>::kThreads, 1)
         give(&bars.p_half[buf]);
         weights(96, 32, pr2 + 16);
         tl_st32(s_at + 32, pr2);
+        if constexpr (NQ == 1) {
+          ok = product_before();
+          if (!ok) continue;
+        }
         give(&bars.p_full[buf]);
         // The weights that entered the product are summed behind their hand-over: the chain up to it is what bounds a tile.
         // Against a sum of the weights before their rounding this costs, us: 5 chunks of 509 tokens over 8003 keys 146
@@ -651,9 +661,7 @@ __global__ void __launch_bounds__(TilesCfg<NS>::kThreads, 1)
           ok = __all_sync(0xffffffffu, bar_wait(&bars.pv_done[q], ph_pv, err));
           ph_pv ^= 1;
         } else {
-          // only the product before the last but one is known to be done here: a parity wait must not skip a phase
-          if (ks > 1) bar_wait(&bars.pv_done[0], uint32_t(ks - 2) & 1u, err);
-          ok = __all_sync(0xffffffffu, bar_wait(&bars.pv_done[0], uint32_t(ks - 1) & 1u, err));
+          ok = product_before();
         }
         tl_fence_after();
       }

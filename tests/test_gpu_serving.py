@@ -407,6 +407,35 @@ def test_attention_of_one_prompt(gsi, D, hq, hkv, q, k):
         assert ((out[:, h].double() - want).abs() <= 1e-4 * A + 2**-8 * (A + want.abs())).all()
 
 
+@pytest.mark.parametrize("D", [64, 128, 192, 256])
+def test_attention_units_end_in_step(gsi, D):
+    # many short units a CTA, whose last product may end before or after the rows' threads ask for it: no wait gives up,
+    # and every run gives the same
+    hq, hkv, page, lens = 64, 8, 32, [287, 191, 95, 250, 154, 58, 213]
+    g = torch.Generator(device="cuda").manual_seed(D)
+    table, n = pages_for([(k, k) for k in lens], page, 9, 1)
+    cache = gsi.PagedCache(*(torch.randn(n, hkv, page, D, device="cuda", generator=g, dtype=BF) for _ in range(2)))
+    q_start = np.cumsum([0] + lens)
+    ws = gsi.new_workspace(gsi.paged_attention_workspace_size(cache, hq))
+    for _ in range(12):
+        Q = 2 * torch.randn(int(q_start[-1]), hq, D, device="cuda", generator=g, dtype=BF)
+        first = None
+        for _ in range(8):
+            out = gsi.paged_attention(cache, Q, i32(q_start), i32(lens), i32(table), max_q=max(lens), workspace=ws)
+            first = out if first is None else first
+            assert torch.equal(out, first)
+        assert gsi.workspace_status(ws) == 0
+    for r, k in enumerate(lens):  # the last ones, against the definition
+        pg = torch.tensor(table[r, :-(-k // page)], device="cuda").long()
+        hidden = torch.ones(k, k, dtype=torch.bool, device="cuda").triu(1)
+        for h in (0, 13, 63):
+            ks, vs = (t[pg, h // 8].reshape(-1, D)[:k].double() for t in (cache.K, cache.V))
+            p = torch.softmax((Q[q_start[r]:q_start[r + 1], h].double() @ ks.T * D ** -0.5).masked_fill(hidden, -float("inf")), -1)
+            want, A = p @ vs, p @ vs.abs()
+            got = out[q_start[r]:q_start[r + 1], h].double()
+            assert ((got - want).abs() <= 1e-4 * A + 2**-8 * (A + want.abs())).all()
+
+
 def test_attention_offsets_beyond_32_bits(gsi):
     # a cache of more than 2^31 elements, the request's pages at its far end and at its beginning
     hkv, D, page, k = 8, 128, 64, 300
