@@ -26,7 +26,7 @@ namespace gsi {
 // exponentials a thread, then its two products, ~3000 cycles a tile of 256 rows
 // against 2048 of products); above, the reads of L2 (128 KB a tile of 128 rows,
 // ~10 TB/s over the SMs).  8192 tokens: 32 x 128 403 us (1.36 PFLOP/s), 16 x 256
-// 425 us (1.29), 32 x 64 364 us (0.76); 2048 tokens of 16 x 256 42 us.
+// 422 us (1.30), 32 x 64 364 us (0.76); 2048 tokens of 16 x 256 42 us.
 //
 // Masked tiles: S is masked in registers; a weight of 0 hides a number of V
 // but not an infinity or NaN, nor the ring's stale bytes where no page was
