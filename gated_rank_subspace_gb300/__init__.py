@@ -56,6 +56,14 @@ class NormDesc(ctypes.Structure):
                 ("bias", ctypes.c_void_p)]
 
 
+class RotaryDesc(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int64), ("layout", ctypes.c_int), ("scale", ctypes.c_float), ("phases", ctypes.c_void_p)]
+
+
+class MarksDesc(ctypes.Structure):
+    _fields_ = [("weight", ctypes.c_void_p), ("place", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -68,7 +76,7 @@ def lib() -> ctypes.CDLL:
         raise ImportError(f"{LIB_PATH} is missing: build it with __graft_entry__.build() "
                           "(or python -m gated_rank_subspace_gb300._build)")
     L = ctypes.CDLL(LIB_PATH)
-    i64, vp, f32, sz = ctypes.c_int64, ctypes.c_void_p, ctypes.c_float, ctypes.c_size_t
+    i64, vp, f32, f64, sz = ctypes.c_int64, ctypes.c_void_p, ctypes.c_float, ctypes.c_double, ctypes.c_size_t
     P = ctypes.POINTER
     sig = {
         "gsi_build_image": [vp, vp, vp, vp, i64, i64, i64, ctypes.c_int, vp],
@@ -95,6 +103,16 @@ def lib() -> ctypes.CDLL:
         "gsi_cache_append": [P(CacheDesc), vp, ctypes.c_int, i64, vp, i64, i64, vp, vp],
         "gsi_paged_attention": [P(CacheDesc), vp, i64, i64, i64, vp, vp, vp, i64, i64, i64, f32, ctypes.c_int, i64, vp,
                                 vp, sz, vp],
+        "gsi_paged_attention_lse": [P(CacheDesc), vp, i64, i64, i64, vp, vp, vp, i64, i64, i64, f32, ctypes.c_int, i64, vp,
+                                    vp, vp, sz, vp],
+        "gsi_paged_trim": [vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp],
+        "gsi_rotary_rates": [i64, f64, ctypes.c_int, f64, f64, f64, f64, P(f64), P(f32)],
+        "gsi_rotary_phases": [P(f64), i64, P(ctypes.c_uint64)],
+        "gsi_rotary_append": [P(CacheDesc), vp, ctypes.c_int, i64, vp, vp, vp, vp, i64, i64, i64, P(RotaryDesc), vp, vp],
+        "gsi_key_weights": [P(CacheDesc), vp, i64, i64, i64, vp, vp, vp, vp, vp, vp, i64, i64, i64, f32, ctypes.c_int,
+                            P(MarksDesc), vp, sz, vp],
+        "gsi_cache_evict": [P(CacheDesc), vp, vp, i64, i64, P(MarksDesc), i64, i64, i64, vp, vp, vp, vp, sz, vp],
+        "gsi_verify_drafts": [vp, ctypes.c_int, i64, vp, ctypes.c_int, i64, i64, i64, vp, vp, vp, vp, vp, i64, vp, vp, vp, vp],
         "gsi_norm_residual": [vp, ctypes.c_int, vp, ctypes.c_int, i64, i64, f32, P(NormDesc), vp, i64, vp, P(NormDesc),
                               vp, vp, ctypes.c_int, vp],
     }
@@ -110,6 +128,10 @@ def lib() -> ctypes.CDLL:
     L.gsi_basis_step_work_bytes.restype = sz
     L.gsi_paged_attention_workspace_size.argtypes = [P(CacheDesc), i64]
     L.gsi_paged_attention_workspace_size.restype = sz
+    L.gsi_key_weights_workspace_size.argtypes = []
+    L.gsi_key_weights_workspace_size.restype = sz
+    L.gsi_cache_evict_workspace_size.argtypes = [P(CacheDesc), i64, i64]
+    L.gsi_cache_evict_workspace_size.restype = sz
     L.gsi_last_error.argtypes = []
     L.gsi_last_error.restype = ctypes.c_char_p
     L.gsi_debug_fail_after.argtypes = [ctypes.c_int]
@@ -622,7 +644,7 @@ def paged_attention_workspace_size(cache: PagedCache, n_q_heads: int) -> int:
 
 def paged_attention(cache: PagedCache, Q: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor,
                     table: torch.Tensor, max_q: int = None, scale: float = None, causal: bool = True, window: int = 0,
-                    out=None, workspace=None, stream=None):
+                    out=None, workspace=None, stream=None, lse=None):
     """Attention of every request's new tokens Q (N, heads, head_dim; rows of the
     cache's dtype, any stride between tokens) over its cached keys, as planned
     by paged_plan; returns out (N, heads, head_dim).  causal: the new tokens are
@@ -633,7 +655,9 @@ def paged_attention(cache: PagedCache, Q: torch.Tensor, q_start: torch.Tensor, k
     request's new tokens, for the choice of kernel (a wrong one costs time, not
     results).  scale defaults to head_dim ** -0.5.  Without a workspace every
     call allocates and zeroes one (some 40 MB at 128 columns): a serving loop
-    keeps one, of paged_attention_workspace_size bytes from new_workspace."""
+    keeps one, of paged_attention_workspace_size bytes from new_workspace.
+    lse: float32 (N, heads) to write the logarithm of each row's sum of weights
+    to, for key_weights."""
     c = cache.desc()
     dev = _device("the cache", cache.K)
     shape, st = Q.shape, Q.stride()
@@ -660,10 +684,13 @@ def paged_attention(cache: PagedCache, Q: torch.Tensor, q_start: torch.Tensor, k
             workspace = new_workspace(paged_attention_workspace_size(cache, H), Q.device, stream)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}, not on {workspace.device}")
-    _check(lib().gsi_paged_attention(c, Q.data_ptr(), st[0], N, H, q_start.data_ptr(), kv_len.data_ptr(),
-                                     table.data_ptr(), width, R, N if max_q is None else max_q,
-                                     D ** -0.5 if scale is None else scale, 1 if causal else 0, window, out.data_ptr(),
-                                     workspace.data_ptr(), workspace.numel(), _raw_stream(stream, Q)))
+    if lse is not None:
+        _like("lse", lse, (N, H), torch.float32, dev)
+    _check(lib().gsi_paged_attention_lse(c, Q.data_ptr(), st[0], N, H, q_start.data_ptr(), kv_len.data_ptr(),
+                                         table.data_ptr(), width, R, N if max_q is None else max_q,
+                                         D ** -0.5 if scale is None else scale, 1 if causal else 0, window, out.data_ptr(),
+                                         None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                         _raw_stream(stream, Q)))
     return out
 
 
@@ -726,3 +753,283 @@ def norm_residual(h: torch.Tensor, y: torch.Tensor = None, post: Norm = None, pr
                                    None if pre is None else pre.desc(d, dev), h_out.data_ptr(), x.data_ptr(), _float_code(x),
                                    _raw_stream(stream, h)))
     return h_out, x
+
+
+ROTARY_LAYOUTS = {"half": 0, "pairs": 1}
+ROTARY_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
+
+
+@dataclass
+class Rotary:
+    """The positions' angles: the first dim values of a head are turned, pair i
+    being values i and dim / 2 + i (layout "half") or 2 i and 2 i + 1 ("pairs"),
+    by position * w_i, and multiplied by scale.  phases: the w_i in units of
+    2^-64 of a turn, int64 (dim / 2) on the device."""
+    dim: int
+    phases: torch.Tensor
+    layout: str = "half"
+    scale: float = 1.0
+
+    @classmethod
+    def from_rates(cls, rates, layout: str = "half", scale: float = 1.0, device="cuda"):
+        """From the w_i in radians a position (numbers, kept in 64 bits)."""
+        n = len(rates)
+        w, out = (ctypes.c_double * n)(*[float(r) for r in rates]), (ctypes.c_uint64 * n)()
+        _check(lib().gsi_rotary_phases(w, n, out))
+        phases = torch.tensor([p - 2 ** 64 if p >= 2 ** 63 else p for p in out], dtype=torch.int64, device=device)
+        return cls(2 * n, phases, layout, scale)
+
+    @classmethod
+    def make(cls, dim: int, base: float = 10000.0, layout: str = "half", scaling: str = "none", factor: float = 1.0,
+             context: float = 0.0, fast: float = 0.0, slow: float = 0.0, device="cuda"):
+        """w_i = base ** (-2 i / dim), scaled for contexts longer than `context` (include/gsi.h has the forms):
+        "linear", "ntk", "yarn" (fast, slow: turns within the context; 32 and 1 by default) or "bands" (4 and 1)."""
+        rates, scale = cls.rates(dim, base, scaling, factor, context, fast, slow)
+        return cls.from_rates(rates, layout, scale, device)
+
+    @staticmethod
+    def rates(dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0, context: float = 0.0,
+              fast: float = 0.0, slow: float = 0.0):
+        """The w_i (radians a position) and the scale of `make`."""
+        default = {"yarn": (32.0, 1.0), "bands": (4.0, 1.0)}.get(scaling, (0.0, 0.0))
+        out, scale = (ctypes.c_double * max(dim // 2, 1))(), ctypes.c_float()
+        _check(lib().gsi_rotary_rates(dim, base, ROTARY_SCALINGS[scaling], factor, context, fast or default[0],
+                                      slow or default[1], out, ctypes.byref(scale)))
+        return list(out), scale.value
+
+    def desc(self, dev: int) -> RotaryDesc:
+        _ints("rotary.phases", self.phases, self.dim // 2, dev, _I64)
+        return RotaryDesc(self.dim, ROTARY_LAYOUTS[self.layout], self.scale, self.phases.data_ptr())
+
+
+def rotary_append(cache: PagedCache, rows: torch.Tensor, slots: torch.Tensor, positions: torch.Tensor, n_q_heads: int,
+                  rotary: Rotary, token_req=None, offsets=None, Q=None, stream=None):
+    """cache_append with queries and keys turned by their positions (int32, one a
+    token), plus offsets[token_req] where a request's places have moved
+    (cache_evict's offsets_out and a plan's token_req)."""
+    c = cache.desc()
+    dev = _device("the cache", cache.K)
+    T = slots.numel()
+    D = c.head_dim
+    st = rows.stride()
+    if rows.shape != (T, (n_q_heads + 2 * c.n_heads) * D) or rows.get_device() != dev or (st[1] != 1 and T):
+        raise ValueError(f"rows must be rows of ({T}, {(n_q_heads + 2 * c.n_heads) * D}) on the cache's device, "
+                         f"not {tuple(rows.shape)} on {rows.device}")
+    _ints("slots", slots, T, dev, _I64)
+    _ints("positions", positions, T, dev)
+    R = 0
+    if offsets is not None:
+        R = offsets.numel()
+        _ints("offsets", offsets, R, dev)
+        if token_req is not None:
+            _ints("token_req", token_req, T, dev)
+        elif R != 1:
+            raise ValueError("offsets of several requests need token_req")
+    if Q is None:
+        with _on_stream(stream):
+            Q = torch.empty(T, n_q_heads, D, dtype=cache.K.dtype, device=rows.device)
+    else:
+        _like("Q", Q, (T, n_q_heads, D), cache.K.dtype, dev)
+    _check(lib().gsi_rotary_append(c, rows.data_ptr(), _float_code(rows), st[0], slots.data_ptr(), positions.data_ptr(),
+                                   None if token_req is None else token_req.data_ptr(),
+                                   None if offsets is None else offsets.data_ptr(), R, T, n_q_heads, rotary.desc(dev),
+                                   Q.data_ptr(), _raw_stream(stream, rows)))
+    return Q
+
+
+@dataclass
+class KeyMarks:
+    """What eviction goes by: for every page, head and token of a cache the
+    attention weight that the key has gathered (float32) and its position in
+    the sequence (int32), two dense (pages, heads, page_size) tensors."""
+    weight: torch.Tensor
+    place: torch.Tensor
+
+    @classmethod
+    def empty(cls, cache: PagedCache):
+        """Marks of a cache's shape (what they hold means nothing until key_weights has written it)."""
+        shape, dev = cache.K.shape[:3], cache.K.device
+        return cls(torch.empty(shape, dtype=torch.float32, device=dev), torch.empty(shape, dtype=torch.int32, device=dev))
+
+    def desc(self, cache: PagedCache, dev: int) -> MarksDesc:
+        _like("marks.weight", self.weight, cache.K.shape[:3], torch.float32, dev)
+        _like("marks.place", self.place, cache.K.shape[:3], _I32, dev)
+        return MarksDesc(self.weight.data_ptr(), self.place.data_ptr())
+
+
+def key_weights_workspace_size() -> int:
+    return int(lib().gsi_key_weights_workspace_size())
+
+
+def key_weights(cache: PagedCache, Q: torch.Tensor, lse: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor,
+                table: torch.Tensor, marks: KeyMarks, held=None, offsets=None, max_q: int = None, scale: float = None,
+                causal: bool = True, workspace=None, stream=None) -> KeyMarks:
+    """The attention weight that every key receives from the tokens Q, whose
+    attention left lse (paged_attention's, the same Q, q_start, kv_len, table,
+    scale and causal): added to the marks of the first held[r] keys of request r
+    (a plan's cached lengths), the beginning of the others', which get the
+    position place + offsets[r] (cache_evict's offsets_out).  held None: no key
+    has marks yet.  Q may be the last tokens only of those that came in."""
+    c = cache.desc()
+    dev = _device("the cache", cache.K)
+    shape, st = Q.shape, Q.stride()
+    if len(shape) != 3 or Q.get_device() != dev or Q.dtype is not cache.K.dtype or shape[2] != c.head_dim:
+        raise ValueError(f"Q must be a (tokens, heads, {c.head_dim}) tensor of {cache.K.dtype} on cuda:{dev}, "
+                         f"not {tuple(shape)} {Q.dtype} on {Q.device}")
+    N, H, D = shape
+    if N and (st[2] != 1 or (H > 1 and st[1] != D)):
+        raise ValueError("the heads of a token of Q must be contiguous")
+    R = kv_len.numel()
+    if table.dim() != 2 or table.shape[0] != R:
+        raise ValueError(f"table must be ({R}, pages), not {tuple(table.shape)}")
+    width = table.shape[1]
+    _like("lse", lse, (N, H), torch.float32, dev)
+    _ints("table", table, R * width, dev)
+    _ints("q_start", q_start, R + 1, dev)
+    _ints("kv_len", kv_len, R, dev)
+    if held is not None:
+        _ints("held", held, R, dev)
+    if offsets is not None:
+        _ints("offsets", offsets, R, dev)
+    m = marks.desc(cache, dev)
+    if workspace is None:
+        with _on_stream(stream):
+            workspace = new_workspace(key_weights_workspace_size(), Q.device, stream)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}, not on {workspace.device}")
+    _check(lib().gsi_key_weights(c, Q.data_ptr(), st[0], N, H, lse.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(),
+                                 None if held is None else held.data_ptr(), None if offsets is None else offsets.data_ptr(),
+                                 table.data_ptr(), width, R, N if max_q is None else max_q,
+                                 D ** -0.5 if scale is None else scale, 1 if causal else 0, m, workspace.data_ptr(),
+                                 workspace.numel(), _raw_stream(stream, Q)))
+    return marks
+
+
+def cache_evict_workspace_size(cache: PagedCache, n_requests: int, budget: int) -> int:
+    c = cache.desc()
+    n = int(lib().gsi_cache_evict_workspace_size(ctypes.byref(c), n_requests, budget))
+    if n == 0:
+        raise GsiError(1, lib().gsi_last_error().decode() or "no eviction of this shape")
+    return n
+
+
+def cache_evict(cache: PagedCache, kv_len: torch.Tensor, table: torch.Tensor, marks: KeyMarks, budget: int,
+                recent: int = 0, sinks: int = 0, offsets=None, kept=None, offsets_out=None, workspace=None, stream=None):
+    """Every request of more than `budget` keys keeps that many, for each head by
+    itself: those of the last `recent` positions, of the first `sinks`, and those
+    that gathered the most weight; the kept ones close the gaps (their order
+    changes).  Returns (kept, offsets_out): the lengths then, and offsets plus
+    the keys given up (the offsets of the next rotary_append, key_weights and
+    cache_evict).  paged_trim returns the pages: once for layers that share the
+    table."""
+    c = cache.desc()
+    dev = _device("the cache", cache.K)
+    R = kv_len.numel()
+    if table.dim() != 2 or table.shape[0] != R:
+        raise ValueError(f"table must be ({R}, pages), not {tuple(table.shape)}")
+    width = table.shape[1]
+    _ints("table", table, R * width, dev)
+    _ints("kv_len", kv_len, R, dev)
+    if offsets is not None:
+        _ints("offsets", offsets, R, dev)
+    m = marks.desc(cache, dev)
+    with _on_stream(stream):
+        if kept is None:
+            kept = torch.empty_like(kv_len)
+        if offsets_out is None:
+            offsets_out = torch.empty_like(kv_len)
+        if workspace is None:
+            workspace = torch.empty(cache_evict_workspace_size(cache, R, budget), dtype=torch.uint8, device=kv_len.device)
+    _ints("kept", kept, R, dev)
+    _ints("offsets_out", offsets_out, R, dev)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}, not on {workspace.device}")
+    _check(lib().gsi_cache_evict(c, kv_len.data_ptr(), table.data_ptr(), width, R, m, budget, recent, sinks,
+                                 None if offsets is None else offsets.data_ptr(), kept.data_ptr(), offsets_out.data_ptr(),
+                                 workspace.data_ptr(), workspace.numel(), _raw_stream(stream, kv_len)))
+    return kept, offsets_out
+
+
+@dataclass
+class Verdict:
+    """Of one step's drafts (device tensors): out (one a row: a request's next
+    tokens, then -1), accepted (requests) and kept (the requests' lengths, or None)."""
+    out: torch.Tensor
+    accepted: torch.Tensor
+    kept: torch.Tensor = None
+
+
+def verify_drafts(target: torch.Tensor, draft, tokens: torch.Tensor, uniforms: torch.Tensor, samples: torch.Tensor,
+                  q_start: torch.Tensor, kv_len=None, out=None, accepted=None, kept=None, stream=None) -> Verdict:
+    """Drafted tokens against the target's probabilities (N, vocab), row
+    q_start[r] being request r's last token and the rows behind it its drafts
+    (tokens, int32): row t's draft tokens[t + 1] stands if uniforms[t] draft <
+    target; the first that does not is replaced by a sample of what the draft
+    leaves of the target, behind drafts that all stand comes one of the target
+    (samples: a number within [0, 1) a request).  draft: (N, vocab)
+    probabilities, or None for drafts that are certain.  kv_len gives kept, the
+    lengths without the places of drafts that do not stand (for paged_trim)."""
+    dev = _device("target", target)
+    if target.dim() != 2 or (draft is not None and (draft.shape != target.shape or draft.get_device() != dev)):
+        raise ValueError("target and draft must be (tokens, vocabulary) tensors of one shape and device")
+    N, V = target.shape
+    ts, ds = target.stride(), (0, 1) if draft is None else draft.stride()
+    if N and V > 1 and (ts[1] != 1 or ds[1] != 1):
+        raise ValueError("the rows of target and draft must be contiguous")
+    R = q_start.numel() - 1
+    if R < 0:
+        raise ValueError("q_start must have one number more than there are requests")
+    _ints("tokens", tokens, N, dev)
+    _like("uniforms", uniforms, (N,), torch.float32, dev)
+    _like("samples", samples, (R,), torch.float32, dev)
+    _ints("q_start", q_start, R + 1, dev)
+    if kv_len is not None:
+        _ints("kv_len", kv_len, R, dev)
+    elif kept is not None:
+        raise ValueError("kept needs kv_len")
+    with _on_stream(stream):
+        if out is None:
+            out = torch.empty(N, dtype=_I32, device=target.device)
+        if accepted is None:
+            accepted = torch.empty(R, dtype=_I32, device=target.device)
+        if kept is None and kv_len is not None:
+            kept = torch.empty(R, dtype=_I32, device=target.device)
+    _ints("out", out, N, dev)
+    _ints("accepted", accepted, R, dev)
+    if kept is not None:
+        _ints("kept", kept, R, dev)
+    _check(lib().gsi_verify_drafts(target.data_ptr(), _float_code(target), ts[0], None if draft is None else draft.data_ptr(),
+                                   0 if draft is None else _float_code(draft), ds[0], N, V, tokens.data_ptr(),
+                                   uniforms.data_ptr(), samples.data_ptr(), q_start.data_ptr(),
+                                   None if kv_len is None else kv_len.data_ptr(), R, out.data_ptr(), accepted.data_ptr(),
+                                   None if kept is None else kept.data_ptr(), _raw_stream(stream, target)))
+    return Verdict(out, accepted, kept)
+
+
+def paged_trim(kv_len: torch.Tensor, kept: torch.Tensor, table: torch.Tensor, free_pages: torch.Tensor,
+               n_free: torch.Tensor, page_size: int, n_free_out=None, status=None, stream=None):
+    """The pages that requests of kv_len tokens no longer fill when they keep
+    kept[r] of them (0: the request is done), back on free_pages[n_free:]; a plan
+    that needs as many takes them in the same order again.  Returns (n_free_out,
+    status): the free pages then, and 0 or PLAN_ bits and nothing given back."""
+    dev = _device("kv_len", kv_len)
+    R, capacity = kv_len.numel(), free_pages.numel()
+    if table.dim() != 2 or table.shape[0] != R:
+        raise ValueError(f"table must be ({R}, pages), not {tuple(table.shape)}")
+    width = table.shape[1]
+    _ints("kv_len", kv_len, R, dev)
+    _ints("kept", kept, R, dev)
+    _ints("table", table, R * width, dev)
+    _ints("free_pages", free_pages, capacity, dev)
+    _ints("n_free", n_free, 1, dev)
+    with _on_stream(stream):
+        if n_free_out is None:
+            n_free_out = torch.empty_like(n_free)
+        if status is None:
+            status = torch.empty_like(n_free)
+    _ints("n_free_out", n_free_out, 1, dev)
+    _ints("status", status, 1, dev)
+    _check(lib().gsi_paged_trim(kv_len.data_ptr(), kept.data_ptr(), R, table.data_ptr(), width, free_pages.data_ptr(),
+                                capacity, n_free.data_ptr(), page_size, n_free_out.data_ptr(), status.data_ptr(),
+                                _raw_stream(stream, kv_len)))
+    return n_free_out, status

@@ -81,6 +81,7 @@ __global__ void __launch_bounds__(kPlainWarps * 32) attn_plain_kernel(AttnArgs a
     }
   }
   const float inv = l != 0.f ? 1.f / l : lim > 0 ? NAN : 0.f;  // as attn_inverse
+  if (a.LSE && lane == 0) a.LSE[tok * hq + head] = l == 0.f ? -INFINITY : m + logf(l);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int c = lane + 32 * i;

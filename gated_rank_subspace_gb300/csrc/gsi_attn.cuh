@@ -108,10 +108,18 @@ __device__ __forceinline__ float attn_inverse(const AttnArgs& a, const AttnReq& 
   return attn_lim(a, q, tok) > 0 ? NAN : 0.f;
 }
 
-// Writes CW columns from c of a finished row of token tok: o / l.
+// The logarithm of a finished row's sum, ln(l 2^m): of the weights as they entered the second product.  -inf where a row sees
+// no key or all its scores are -inf.
+__device__ __forceinline__ void attn_lse(const AttnArgs& a, int64_t row, float m, float l) {
+  if (a.LSE) a.LSE[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+// Writes CW columns from c of a finished row of token tok: o / l; its maximum m (in powers of two) is for the sum's logarithm.
 template <class T, int CW>
-__device__ __forceinline__ void attn_finish(const AttnArgs& a, const AttnReq& q, int tok, int64_t at, int c, float l,
+__device__ __forceinline__ void attn_finish(const AttnArgs& a, const AttnReq& q, int tok, int64_t row, int c, float m, float l,
                                             const float (&o)[CW]) {
+  const int64_t at = row * a.dim + c;
+  if (c == 0) attn_lse(a, row, m, l);
   const float inv = attn_inverse(a, q, tok, l);
   if constexpr (CW == 4) {
     static_assert(T::kBytes == 4, "pieces of four are float32's");
@@ -150,7 +158,7 @@ __device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnSeg& g, i
 #pragma unroll
     for (int i = 0; i < CW; ++i) o[i] = 0.f;
     attn_fold<kRowMajor, CW>(a, b0, b1, b0, tiles, tile, rows, row, c, m, l, o);
-    attn_finish<T, CW>(a, g.q, tok0 + row / a.group, attn_out_row(a, g, tok0, row) * a.dim + c, c, l, o);
+    attn_finish<T, CW>(a, g.q, tok0 + row / a.group, attn_out_row(a, g, tok0, row), c, m, l, o);
   }
 }
 

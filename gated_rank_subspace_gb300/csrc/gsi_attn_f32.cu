@@ -228,10 +228,12 @@ __global__ void __launch_bounds__(kF32Threads, BM == 16 || NC <= 2 ? 2 : 1) attn
         const int row = tr * RM + i;
         if (row >= n_rows) continue;
         const float inv = !whole ? 1.f : l[i] != 0.f ? 1.f / l[i] : lim[i] > 0 ? NAN : 0.f;  // as attn_inverse
+        const float ml = m[i] == -INFINITY ? m[i] : m[i] * c;  // in powers of two
         if (!whole && c0 == 0) {
-          part[row] = m[i] == -INFINITY ? m[i] : m[i] * c;
+          part[row] = ml;
           part[BM + row] = l[i];
         }
+        if (whole && c0 == 0) attn_lse(a, attn_out_row(a, g, tok0, row), ml, l[i]);
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
           const int col = c0 + n * cg;

@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(RowsCfg<NS>::kThreads, 1)
           v[x] = attn_nonfinite<BF16>(a, g, C::kKt, attn_lo(a, rl), rl, lo_max, lim_min, c + x, v[x]);
       }
       if (whole) {
-        attn_finish<BF16, 8>(a, g.q, tok0 + row / a.group, attn_out_row(a, g, tok0, row) * a.dim + c, c, sum, v);
+        attn_finish<BF16, 8>(a, g.q, tok0 + row / a.group, attn_out_row(a, g, tok0, row), c, mx, sum, v);
       } else {
         *attn_piece<true>(part, C::kRows, a.dim, row, c) = make_float4(v[0], v[1], v[2], v[3]);
         *attn_piece<true>(part, C::kRows, a.dim, row, c + 4) = make_float4(v[4], v[5], v[6], v[7]);

@@ -703,7 +703,7 @@ __global__ void __launch_bounds__(TilesCfg<NS>::kThreads, 1)
         }
       }
       float* part = attn_part(a, 2 * int(blockIdx.x) + (int(blockIdx.x) == b0), NQ, q, 128);
-      const int64_t out = row < n_rows ? attn_out_row(a, g, tok0, row) * a.dim : 0;
+      const int64_t out = row < n_rows ? attn_out_row(a, g, tok0, row) : 0;
 #pragma unroll 1
       for (int i = 0; i < NS; ++i) {
         uint32_t r[64];
@@ -725,7 +725,7 @@ __global__ void __launch_bounds__(TilesCfg<NS>::kThreads, 1)
           if (whole || fold) {
             float fm = ml, fl = l;
             if (fold) attn_fold<false, 64>(a, b0 + 1, b1, b0, NQ, q, 128, row, 64 * i, fm, fl, v);
-            attn_finish<BF16, 64>(a, g.q, my_tok, out + 64 * i, 64 * i, fl, v);
+            attn_finish<BF16, 64>(a, g.q, my_tok, out, 64 * i, fm, fl, v);
           } else {
 #pragma unroll
             for (int z = 0; z < 64; z += 4)

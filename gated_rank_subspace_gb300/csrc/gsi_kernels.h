@@ -299,6 +299,21 @@ struct PlanArgs {
 };
 cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t s);
 
+struct TrimArgs {
+  const int32_t* kv_len;
+  const int32_t* kept;
+  int n_req;
+  const int32_t* table;
+  int64_t width;
+  int32_t* free_pages;
+  int64_t capacity;
+  const int32_t* n_free;
+  int page_shift;
+  int32_t* n_free_out;
+  int32_t* status;
+};
+cudaError_t launch_paged_trim(const TrimArgs& a, cudaStream_t s);
+
 struct AppendArgs {
   const void* X;       // T x (hq + 2 hkv) * dim rows
   int64_t row_stride;
@@ -311,6 +326,23 @@ struct AppendArgs {
   void* Q;             // or null
 };
 cudaError_t launch_cache_append(const AppendArgs& a, gsi_dtype xdt, gsi_dtype cdt, cudaStream_t s);
+
+struct RotaryArgs {
+  AppendArgs to;
+  const int32_t* positions;
+  const int32_t* token_req;  // or null
+  const int32_t* offsets;    // or null
+  int n_req;
+  int turned;                // values of a head that are turned
+  int pairs;                 // neighbours are turned together (else value i and turned / 2 + i)
+  float scale;
+  const uint64_t* phases;    // turned / 2
+};
+// Rates of the pairs in radians a position and the factor of their cosines and sines; a rate in units of 2^-64 of a turn (host).
+void rotary_rates(int dim, double base, int scaling, double factor, double context, double fast, double slow, double* rates,
+                  float* scale);
+uint64_t rotary_phase(double rate);
+cudaError_t launch_rotary_append(const RotaryArgs& a, gsi_dtype xdt, gsi_dtype cdt, cudaStream_t s);
 
 struct AttnArgs {
   const void* K;
@@ -330,9 +362,76 @@ struct AttnArgs {
   float scale;
   int causal, window;
   void* work;
+  float* LSE;          // N x (hkv * group), or null
 };
 cudaError_t launch_paged_attention(const AttnArgs& a, gsi_dtype dt, int64_t max_q, cudaStream_t s);
 size_t attention_work_bytes(gsi_dtype dt, int dim, int group);
+
+struct KeyWeightArgs {
+  const void* K;
+  int64_t page_stride, head_stride, token_stride;
+  int64_t n_pages;
+  int page_shift, hkv, group, dim;
+  const void* Q;
+  int64_t q_stride;
+  const float* LSE;      // N x (hkv * group)
+  int N;
+  const int32_t* q_start;
+  const int32_t* kv_len;
+  const int32_t* held;     // or null
+  const int32_t* offsets;  // or null
+  const int32_t* table;
+  int64_t width;
+  int n_req;
+  float scale;
+  int causal;
+  float* weight;         // n_pages x hkv x page
+  int32_t* place;
+  void* work;
+};
+cudaError_t launch_key_weights(const KeyWeightArgs& a, gsi_dtype dt, int64_t max_q, cudaStream_t s);
+size_t key_weights_work_bytes();
+
+struct EvictArgs {
+  void* K;
+  void* V;
+  int64_t page_stride, head_stride, token_stride;  // elements
+  int64_t n_pages;
+  int page_shift, hkv, row_bytes, elem;
+  const int32_t* kv_len;
+  const int32_t* table;
+  int64_t width;
+  int n_req;
+  float* weight;
+  int32_t* place;
+  int budget, recent, sinks;
+  const int32_t* offsets;  // or null
+  int32_t* kept;
+  int32_t* offsets_out;
+  int32_t* moves;        // [n_req * hkv][2][budget]
+};
+// The lists lie behind the counters that the attention keeps in a workspace.
+constexpr size_t kEvictMovesAt = 4608;
+inline size_t evict_work_bytes(int64_t units, int64_t budget) { return kEvictMovesAt + (size_t(units) * budget * 8 + 255) / 256 * 256; }
+cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t s);
+
+struct VerifyArgs {
+  const void* target;
+  int64_t target_stride;
+  const void* draft;     // or null
+  int64_t draft_stride;
+  int N, vocab;
+  const int32_t* tokens;
+  const float* uniforms;
+  const float* samples;
+  const int32_t* q_start;
+  const int32_t* kv_len;  // or null
+  int n_req;
+  int32_t* out;
+  int32_t* accepted;
+  int32_t* kept;          // or null
+};
+cudaError_t launch_verify_drafts(const VerifyArgs& a, gsi_dtype tdt, gsi_dtype ddt, cudaStream_t s);
 
 struct NormArgs {
   const void* H;

@@ -1,7 +1,7 @@
-// Pages of the key/value cache: the plan of a step's pages and slots, and the
-// append of a qkv map's rows at those slots.
+// Pages of the key/value cache: the plan of a step's pages and slots, the
+// return of pages, and the append of a qkv map's rows at their slots.
 
-#include "gsi_common.cuh"
+#include "gsi_append.cuh"
 #include "gsi_kernels.h"
 
 namespace gsi {
@@ -213,33 +213,130 @@ cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, paged_plan_kernel, a);
 }
 
+// ------------------------------------------------------------------ trim
+// Request r filled ceil(l_r / P) pages and now fills ceil(k_r / P): the pages
+// between go back on the stack, F_r of them behind the B_r = sum_{i<r} F_i of
+// the requests before.  The i-th page given back (in the order of requests and
+// pages) lands at n_free + F - 1 - i, so a plan that needs them again takes
+// them in the same order.  As in the plan, every CTA forms the prefix sums
+// itself and writes its own slice of the pages, each finding its request by
+// bisection.  Latency bounds it.
+constexpr int kTrimPages = 1024;  // pages of a CTA, at least
+
+__device__ __forceinline__ PlanSums trim_request(const TrimArgs& a, int len, int kept) {
+  const long long round = (1ll << a.page_shift) - 1;
+  if (len < 0 || kept < 0 || kept > len) return PlanSums{0, 0, GSI_PLAN_BAD_LENGTH};
+  const long long held = (len + round) >> a.page_shift;
+  return PlanSums{0, held - ((kept + round) >> a.page_shift), held > a.width ? unsigned(GSI_PLAN_TABLE_FULL) : 0u};
+}
+
+__global__ void __launch_bounds__(kPlanThreads) paged_trim_kernel(const __grid_constant__ TrimArgs a) {
+  __shared__ PlanSums s_warp[kPlanThreads / 32];
+  __shared__ int s_back[kPlanChunk], s_first[kPlanChunk];  // B_r, and the first page that r gives back
+  pdl_launch_dependents();
+  pdl_wait();
+  const int tid = threadIdx.x, shift = a.page_shift, round = (1 << shift) - 1;
+  const int n_free = __ldcg(a.n_free);
+  const bool one_chunk = a.n_req <= kPlanChunk;
+  int len[kPlanItems], kept[kPlanItems];
+  auto load = [&](int c0) {
+#pragma unroll
+    for (int i = 0; i < kPlanItems; ++i) {
+      const int r = c0 + tid * kPlanItems + i;
+      len[i] = kept[i] = 0;
+      if (r < a.n_req) {
+        len[i] = __ldcg(a.kv_len + r);
+        kept[i] = __ldcg(a.kept + r);
+      }
+    }
+  };
+  auto sums = [&]() {
+    PlanSums s{0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < kPlanItems; ++i) {
+      const PlanSums q = trim_request(a, len[i], kept[i]);
+      s.pages += q.pages, s.bad |= q.bad;
+    }
+    return s;
+  };
+
+  // 1. the total and the checks, before anything is written
+  PlanSums all, at;
+  if (one_chunk) {
+    load(0);
+    at = plan_scan(sums(), s_warp, &all);
+  } else {
+    PlanSums mine{0, 0, 0};
+    for (int r = tid; r < a.n_req; r += kPlanThreads) {
+      const PlanSums q = trim_request(a, __ldcg(a.kv_len + r), __ldcg(a.kept + r));
+      mine.pages += q.pages, mine.bad |= q.bad;
+    }
+    plan_scan(mine, s_warp, &all);
+  }
+  unsigned bad = all.bad;
+  if (n_free < 0 || n_free > a.capacity || n_free + all.pages > a.capacity) bad |= GSI_PLAN_NO_PAGES;
+  if (blockIdx.x == 0 && tid == 0) {
+    *a.status = int(bad);
+    *a.n_free_out = bad ? n_free : int(n_free + all.pages);
+  }
+  if (bad) return;
+
+  // 2. the requests, a chunk at a time
+  const int total = int(all.pages);
+  const int i0 = int(all.pages * blockIdx.x / gridDim.x), i1 = int(all.pages * (blockIdx.x + 1) / gridDim.x);
+  int base = 0;
+  for (int c0 = 0; c0 < a.n_req; c0 += kPlanChunk) {
+    const int n = min(kPlanChunk, a.n_req - c0);
+    PlanSums chunk = all;
+    if (!one_chunk) {
+      load(c0);
+      at = plan_scan(sums(), s_warp, &chunk);
+    }
+    int b = base + int(at.pages);
+#pragma unroll
+    for (int i = 0; i < kPlanItems; ++i) {
+      const int r = tid * kPlanItems + i, first = int(((long long)kept[i] + round) >> shift);
+      if (r < n) {
+        s_back[r] = b;
+        s_first[r] = first;
+      }
+      b += int(((long long)len[i] + round) >> shift) - first;
+    }
+    __syncthreads();
+    const int end = base + int(chunk.pages);
+    for (int i = max(i0, base) + tid; i < min(i1, end); i += kPlanThreads) {
+      int lo = 0, hi = n;  // the last request whose pages begin at or before i
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_back[mid] <= i) lo = mid; else hi = mid;
+      }
+      a.free_pages[n_free + total - 1 - i] = __ldcg(a.table + int64_t(c0 + lo) * a.width + s_first[lo] + i - s_back[lo]);
+    }
+    base = end;
+    __syncthreads();  // before the next chunk's sums overwrite these
+  }
+}
+
+cudaError_t launch_paged_trim(const TrimArgs& a, cudaStream_t s) {
+  cudaLaunchConfig_t cfg{};
+  // (the pages given back are at most the stack's places)
+  cfg.gridDim = dim3(unsigned(max(int64_t(1), min(int64_t(sm_count()), a.capacity / kTrimPages))));
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_trim_kernel, a);
+}
+
 // ------------------------------------------------------------------ append
 // A copy: (hq + 2 hkv) * dim values a token are read, converted and written
 // once, so the bytes bound it (2048 tokens of 16 + 2 x 16 heads of 256: 24 us,
 // 6.3 TB/s; 16 tokens 1.9 us).  A CTA takes up to 512 16-byte output vectors of
 // one token; its slot is one broadcast load.
 constexpr int kAppendThreads = 256;
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-// One 16-byte vector of the cache's type from the row's values (float32 to
-// bf16 rounds to nearest even; bf16 to float32 is exact).
-template <class XT, class CT>
-__device__ __forceinline__ uint4 append_vec(const void* row, int64_t e) {
-  if constexpr (XT::kBytes == CT::kBytes) {
-    return ld_cg_v4(static_cast<const char*>(row) + e * XT::kBytes);
-  } else if constexpr (XT::kBytes == 4) {
-    const uint4 a = ld_cg_v4(static_cast<const char*>(row) + e * 4), b = ld_cg_v4(static_cast<const char*>(row) + e * 4 + 16);
-    return make_uint4(pack_bf16(__uint_as_float(a.x), __uint_as_float(a.y)), pack_bf16(__uint_as_float(a.z), __uint_as_float(a.w)),
-                      pack_bf16(__uint_as_float(b.x), __uint_as_float(b.y)), pack_bf16(__uint_as_float(b.z), __uint_as_float(b.w)));
-  } else {
-    const uint2 v = __ldcg(reinterpret_cast<const uint2*>(static_cast<const char*>(row) + e * 2));
-    return make_uint4(v.x << 16, v.x & 0xffff0000u, v.y << 16, v.y & 0xffff0000u);
-  }
-}
 
 template <class XT, class CT>
 __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(AppendArgs a) {

@@ -1,0 +1,177 @@
+// Verification of drafted tokens against the target's probabilities.
+
+#include "gsi_common.cuh"
+#include "gsi_kernels.h"
+
+namespace gsi {
+
+// A request's rows q_start[r] .. q_start[r + 1) hold its last token and its n
+// drafts; row t's probabilities p (target) and q (draft) are those of the token
+// behind it.  Draft d of row t stands if u_t q(d) < p(d); the first that does not
+// is replaced by a token of the distribution max(p - q, 0), and behind n standing
+// drafts comes one of p:  the smallest token x with
+//   sum_{y <= x} m(y) > v sum_y m(y).
+// Sums of 10^5 probabilities have to be right to far below one of them, whatever
+// their order: p and q become whole multiples of 2^-58 (exact from 2^-35 on), whose
+// differences and sums are exact in 64 bits; v times the total is formed in 128.
+//
+// A cluster takes a request.  Every CTA finds the row (the drafts' probabilities
+// are a few loads), then each sums a stretch of the row, a warp a stretch of that;
+// the one whose stretch holds the token looks through it again.  The bytes of the
+// one row of p and q bound it, for few requests the chain of loads and exchanges.
+constexpr int kVfThreads = 512, kVfWarps = kVfThreads / 32, kVfMost = 8;
+constexpr int kVfUnroll = 4;  // loads of each row in flight a lane
+
+// A probability in units of 2^-58: negative ones and NaN are 0, above 1 is 1.
+__device__ __forceinline__ unsigned long long vf_units(float p) {
+  return __float2ull_rz(fminf(fmaxf(p, 0.f), 1.f) * 288230376151711744.f);  // (fmaxf drops NaN)
+}
+
+struct VfShared {
+  unsigned long long total;           // of this CTA (read by the cluster)
+  unsigned long long warps[kVfWarps];
+  int fail;
+};
+
+template <class TT, class DT>
+__global__ void __launch_bounds__(kVfThreads, 2) verify_drafts_kernel(const __grid_constant__ VerifyArgs a) {
+  __shared__ VfShared sh;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = int(cluster.num_blocks()), c = int(cluster.block_rank());
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int r = blockIdx.x / C;
+  pdl_launch_dependents();
+  if (tid == 0) sh.fail = 0x7fffffff;
+  pdl_wait();
+  const int t0 = min(max(__ldcg(a.q_start + r), 0), a.N), t1 = min(max(__ldcg(a.q_start + r + 1), t0), a.N);
+  const int n = t1 - t0 - 1;  // drafts
+  if (n < 0) {
+    if (c == 0 && tid == 0) {
+      a.accepted[r] = 0;
+      if (a.kept) a.kept[r] = __ldcg(a.kv_len + r);
+    }
+    return;  // the whole cluster
+  }
+  __syncthreads();
+
+  // ---- the first draft that does not stand
+  auto p_at = [&](int t, int x) { return TT::load1_cg(a.target, t * a.target_stride + x); };
+  auto q_at = [&](int t, int x) { return a.draft ? DT::load1_cg(a.draft, t * a.draft_stride + x) : 1.f; };
+  for (int i = tid; i < n; i += kVfThreads) {
+    const int t = t0 + i, d = __ldcg(a.tokens + t + 1);
+    // (the product of two float32 is exact in 64 bits; a token outside the vocabulary has no probability)
+    const bool stands = d >= 0 && d < a.vocab && double(__ldcg(a.uniforms + t)) * double(q_at(t, d)) < double(p_at(t, d));
+    if (!stands) {
+      atomicMin(&sh.fail, i);
+      break;
+    }
+  }
+  __syncthreads();
+  const int taken = min(sh.fail, n);
+  const int t = t0 + taken;
+  const int gone = taken < n && !a.draft ? __ldcg(a.tokens + t + 1) : -1;  // a certain draft's whole mass
+
+  // ---- the distribution, a stretch a CTA and a warp
+  const int x0 = int(int64_t(a.vocab) * c / C), x1 = int(int64_t(a.vocab) * (c + 1) / C);
+  const int y0 = x0 + int(int64_t(x1 - x0) * warp / kVfWarps), y1 = x0 + int(int64_t(x1 - x0) * (warp + 1) / kVfWarps);
+  bool left = taken < n;  // what the draft leaves of the target, else the target itself
+  auto mass = [&](int x) -> unsigned long long {
+    const unsigned long long p = vf_units(p_at(t, x));
+    if (!left) return p;
+    if (!a.draft) return x == gone ? 0 : p;
+    const unsigned long long q = vf_units(q_at(t, x));
+    return p > q ? p - q : 0;
+  };
+  for (;;) {
+    unsigned long long sum = 0;
+    for (int x = y0 + lane; x < y1; x += 32 * kVfUnroll) {
+      unsigned long long m[kVfUnroll];
+#pragma unroll
+      for (int i = 0; i < kVfUnroll; ++i) m[i] = x + 32 * i < y1 ? mass(x + 32 * i) : 0;
+#pragma unroll
+      for (int i = 0; i < kVfUnroll; ++i) sum += m[i];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) sh.warps[warp] = sum;
+    __syncthreads();
+    if (tid == 0) {
+      unsigned long long s = 0;
+      for (int w = 0; w < kVfWarps; ++w) s += sh.warps[w];
+      sh.total = s;
+    }
+    cluster.sync();
+    unsigned long long total = 0, base = 0;
+    for (int b = 0; b < C; ++b) {
+      if (b == c) base = total;
+      total += *cluster.map_shared_rank(&sh.total, b);
+    }
+    cluster.sync();  // the totals have been read
+    if (total == 0) {
+      if (left) {  // a draft that leaves nothing: the target itself
+        left = false;
+        continue;
+      }
+      if (c == 0 && tid == 0) a.out[t] = -1;  // a row without any mass
+      break;
+    }
+    // the token's mass ends above floor(v total)
+    const float v = fminf(fmaxf(__ldcg(a.samples + r), 0.f), 0x1.fffffep-1f);
+    const unsigned long long at = __umul64hi(total, __float2ull_rz(v * 18446744073709551616.f));
+    for (int w = 0; w < warp; ++w) base += sh.warps[w];
+    if (base <= at && at < base + sum) {  // in this warp's stretch (one warp of the cluster)
+      for (int x = y0 + lane; x - lane < y1; x += 32) {
+        unsigned long long inc = x < y1 ? mass(x) : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const unsigned long long z = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += z;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, base + inc > at);
+        if (hit) {
+          if (lane == 0) a.out[t] = x + __ffs(hit) - 1;
+          break;
+        }
+        base += __shfl_sync(0xffffffffu, inc, 31);
+      }
+    }
+    break;
+  }
+
+  if (c != 0) return;
+  for (int i = tid; i <= n; i += kVfThreads) {
+    if (i < taken) a.out[t0 + i] = __ldcg(a.tokens + t0 + i + 1);
+    if (i > taken) a.out[t0 + i] = -1;
+  }
+  if (tid == 0) {
+    a.accepted[r] = taken;
+    if (a.kept) a.kept[r] = __ldcg(a.kv_len + r) - (n - taken);
+  }
+}
+
+template <class TT, class DT>
+static cudaError_t launch_vf(const VerifyArgs& a, cudaStream_t s) {
+  // as many CTAs a request as there are SMs for, of 4096 tokens at least
+  unsigned C = 1;
+  while (C < unsigned(kVfMost) && int64_t(a.n_req) * C * 2 <= 2 * sm_count() && a.vocab > int64_t(C) * 4096) C *= 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(unsigned(a.n_req) * C);
+  cfg.blockDim = dim3(kVfThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = C;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, verify_drafts_kernel<TT, DT>, a);
+}
+
+cudaError_t launch_verify_drafts(const VerifyArgs& a, gsi_dtype tdt, gsi_dtype ddt, cudaStream_t s) {
+  if (tdt == GSI_F32) return ddt == GSI_F32 ? launch_vf<F32, F32>(a, s) : launch_vf<F32, BF16>(a, s);
+  return ddt == GSI_F32 ? launch_vf<BF16, F32>(a, s) : launch_vf<BF16, BF16>(a, s);
+}
+
+}  // namespace gsi

@@ -1,0 +1,43 @@
+// Accumulated attention weights of cached keys: what their kernels share beside
+// the shares of their work -- the sums of a unit that is cut, and a key's sum.
+#pragma once
+
+#include "gsi_async.cuh"
+#include "gsi_weights_share.cuh"
+
+namespace gsi {
+
+// The parts of a unit that is cut: KT sums each, in the workspace.  The CTA
+// that finds itself the last to arrive adds them in the order of the line (so
+// the result does not depend on who came last) and sets the counter back to
+// zero.  Nobody waits.  At most two units of a share are cut: one that an
+// earlier CTA began (slot 2 b) and one that a later CTA ends (slot 2 b + 1).
+// (The counters lie where the attention's do, the parts behind them: one workspace serves both.)
+constexpr size_t kKwCounterBytes = 4096;
+static_assert(4 * kKwCtas <= int(kKwCounterBytes), "a counter a CTA");
+inline size_t kw_work_bytes() { return sizeof(Ctrl) + kKwCounterBytes + size_t(2) * kKwCtas * 128 * 4; }
+__device__ __forceinline__ unsigned* kw_counter(const KeyWeightArgs& a, int cta) {
+  return reinterpret_cast<unsigned*>(static_cast<char*>(a.work) + sizeof(Ctrl)) + cta;
+}
+__device__ __forceinline__ float* kw_part(const KeyWeightArgs& a, int slot) {
+  return reinterpret_cast<float*>(static_cast<char*>(a.work) + sizeof(Ctrl) + kKwCounterBytes) + size_t(slot) * 128;
+}
+__device__ __forceinline__ uint32_t* kw_err(const KeyWeightArgs& a) { return &static_cast<Ctrl*>(a.work)->err; }
+
+// Gives the sum of a unit's key to the key: added to what it has, or its first.
+__device__ __forceinline__ void kw_give(const KeyWeightArgs& a, const KwSeg& g, int key, float sum) {
+  if (key >= g.q.len || (g.q.q_len == 0 && key < g.q.held)) return;
+  const int pg = __ldcg(a.table + int64_t(g.r) * a.width + (key >> a.page_shift));
+  if (pg < 0 || pg >= a.n_pages) return;
+  const int64_t at = ((int64_t(pg) * a.hkv + g.h) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+  if (key < g.q.held) {
+    a.weight[at] = __ldcg(a.weight + at) + sum;
+  } else {
+    a.weight[at] = sum;
+    a.place[at] = key + (a.offsets ? __ldcg(a.offsets + g.r) : 0);
+  }
+}
+
+cudaError_t launch_key_weights_rows(const KeyWeightArgs& a, gsi_dtype dt, cudaStream_t s);
+
+}  // namespace gsi

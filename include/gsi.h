@@ -349,8 +349,11 @@ gsi_status gsi_linear_noalloc_status(uint32_t* code, void* stream);
  * its qkv and out maps, a paged key/value cache and the attention over it,
  * and between its blocks the norms, gate and residual.  A step of a server:
  *   gsi_paged_plan       pages and slots of the step's new tokens
- *   per layer: gsi_linear (qkv), gsi_cache_append, gsi_paged_attention,
- *              gsi_linear (out), gsi_norm_residual, gsi_linear (up) ...
+ *   per layer: gsi_linear (qkv), gsi_cache_append (gsi_rotary_append),
+ *              gsi_paged_attention, gsi_linear (out), gsi_norm_residual,
+ *              gsi_linear (up) ...
+ *   a cache of bounded length, per layer: gsi_key_weights, gsi_cache_evict
+ *   drafted tokens: gsi_verify_drafts;   shorter requests: gsi_paged_trim
  * The conventions above hold (asynchronous on `stream`, nothing allocated,
  * argument errors synchronous, no host synchronisation: lengths, tables and
  * slots stay on the device and calls may be captured into a CUDA graph).
@@ -407,6 +410,25 @@ gsi_status gsi_paged_plan(const int32_t* cached, const int32_t* fresh, int64_t n
                           int64_t page_size, int64_t n_tokens, int32_t* q_start, int32_t* kv_len, int64_t* slots,
                           int32_t* token_req, int32_t* positions, int32_t* n_free_out, int32_t* status, void* stream);
 
+/* The pages that requests no longer fill, back on the stack of free ones.
+ * Request r filled the pages table[r][0 .. ceil(kv_len[r] / page_size)) and
+ * keeps kept[r] <= kv_len[r] places (all of kv_len for none given back; 0 for
+ * a request that is done).  The pages beyond ceil(kept[r] / page_size) go to
+ * free_pages[*n_free ..), so that a gsi_paged_plan that takes as many gets
+ * them in the order of the requests and their pages again; *n_free_out is the
+ * number of free pages then.  The table is not written (its entries beyond a
+ * request's length mean nothing), its entries are given back as they are (a
+ * page belongs to one request), and the lengths may be one array.  Trimming
+ * that cannot be done is not done in part: *status receives GSI_PLAN_BAD_LENGTH
+ * (a negative length, or kept above kv_len), GSI_PLAN_TABLE_FULL (more pages
+ * than table_width) or GSI_PLAN_NO_PAGES (*n_free outside 0 .. capacity, or no
+ * room for the pages), *n_free_out receives *n_free, and free_pages stays.
+ * n_free_out must not be n_free (GSI_ERR_INVALID_ARG).  n_req <= 2^20,
+ * table_width * page_size < 2^31. */
+gsi_status gsi_paged_trim(const int32_t* kv_len, const int32_t* kept, int64_t n_req, const int32_t* table,
+                          int64_t table_width, int32_t* free_pages, int64_t capacity, const int32_t* n_free,
+                          int64_t page_size, int32_t* n_free_out, int32_t* status, void* stream);
+
 /* The rows of a qkv map (gsi_linear's Y, or any T x (n_q_heads + 2 n_heads) *
  * head_dim rows of type xdt, row_stride elements apart, a multiple of 16 bytes
  * where there are several): the first n_q_heads * head_dim values of a row are
@@ -417,6 +439,58 @@ gsi_status gsi_paged_plan(const int32_t* cached, const int32_t* fresh, int64_t n
  * the cache as it is; their queries are still written.  Slots are distinct. */
 gsi_status gsi_cache_append(const gsi_cache_desc* cache, const void* X, gsi_dtype xdt, int64_t row_stride,
                             const int64_t* slots, int64_t T, int64_t n_q_heads, void* Q, void* stream);
+
+/* Rotary positions.  The first dim values of a head (even, at most head_dim)
+ * are turned in dim / 2 pairs, the rest stay: pair i is the values 2 i and
+ * 2 i + 1 (GSI_ROTARY_PAIRS) or i and dim / 2 + i (GSI_ROTARY_HALF), and at
+ * position p becomes
+ *   a' = scale (a cos - b sin),  b' = scale (b cos + a sin),  angle p w_i.
+ * phases (DEVICE, dim / 2): w_i in units of 2^-64 of a turn, so that an
+ * angle's turns are taken off exactly at any position. */
+typedef enum gsi_rotary_layout { GSI_ROTARY_HALF = 0, GSI_ROTARY_PAIRS = 1 } gsi_rotary_layout;
+typedef struct gsi_rotary {
+  int64_t dim;
+  gsi_rotary_layout layout;
+  float scale;
+  const uint64_t* phases;
+} gsi_rotary;
+
+/* How the rates w_i = base^(-2 i / dim) are scaled for contexts longer than
+ * those of training:
+ *   NONE
+ *   LINEAR  w / factor (positions divided)
+ *   NTK     base factor^(dim / (dim - 2)) for the base (dim > 2): the first
+ *           pair as it was, the last one divided by factor
+ *   YARN    w (1 - g) + (w / factor) g, g rising from 0 at pair floor(at(fast))
+ *           to 1 at ceil(at(slow)) (within 0 .. dim - 1; a width of at least
+ *           0.001), at(x) = dim ln(context / (2 pi x)) / (2 ln base): pairs that
+ *           turn more than `fast` times in `context` positions keep their
+ *           rate; scale = 0.1 ln(factor) + 1
+ *   BANDS   w g + (w / factor) (1 - g), g = (context w / 2 pi - slow) /
+ *           (fast - slow) within 0 .. 1, by the turns in `context` positions. */
+typedef enum gsi_rotary_scaling {
+  GSI_ROTARY_NONE = 0, GSI_ROTARY_LINEAR = 1, GSI_ROTARY_NTK = 2, GSI_ROTARY_YARN = 3, GSI_ROTARY_BANDS = 4
+} gsi_rotary_scaling;
+
+/* On the HOST, without a GPU: the rates of dim / 2 pairs in radians a position
+ * (rates, double) and the factor of their cosines and sines (*scale), and
+ * rates as phases.  base > 1 and factor >= 1, finite; context, fast and slow
+ * are looked at by YARN and BANDS (context > 0, fast > slow > 0).  A rate
+ * that is not finite is refused. */
+gsi_status gsi_rotary_rates(int64_t dim, double base, gsi_rotary_scaling scaling, double factor, double context,
+                            double fast, double slow, double* rates, float* scale);
+gsi_status gsi_rotary_phases(const double* rates, int64_t n, uint64_t* phases);
+
+/* gsi_cache_append with the queries and keys turned by their positions on the
+ * way (values and what lies beyond rotary->dim are copied): token t stands at
+ * positions[t], plus offsets[token_req[t]] where offsets (n_req) is given: the
+ * places a request has given up by eviction (offsets[0] where token_req is
+ * NULL; a request outside 0 .. n_req adds nothing).  What is turned is formed
+ * in float32 and rounded once. */
+gsi_status gsi_rotary_append(const gsi_cache_desc* cache, const void* X, gsi_dtype xdt, int64_t row_stride,
+                             const int64_t* slots, const int32_t* positions, const int32_t* token_req,
+                             const int32_t* offsets, int64_t n_req, int64_t T, int64_t n_q_heads,
+                             const gsi_rotary* rotary, void* Q, void* stream);
 
 /* Attention of the new tokens of every request over its paged keys and
  * values.  Request r has the tokens q_start[r] .. q_start[r + 1) of Q (its
@@ -451,6 +525,106 @@ gsi_status gsi_paged_attention(const gsi_cache_desc* cache, const void* Q, int64
                                int64_t n_q_heads, const int32_t* q_start, const int32_t* kv_len,
                                const int32_t* table, int64_t table_width, int64_t n_req, int64_t max_q, float scale,
                                int causal, int64_t window, void* O, void* workspace, size_t ws_bytes, void* stream);
+
+/* The same, and where LSE (N x n_q_heads float32) is not NULL the natural
+ * logarithm of each row's sum of weights, ln sum_j exp(scale q . k_j): -inf
+ * for a row that sees no key or whose scores are all -inf.  For GSI_BF16 the
+ * sum is that of the weights as they entered the second product (off by 2^-8
+ * of it at most).  Rows outside every request are not written. */
+gsi_status gsi_paged_attention_lse(const gsi_cache_desc* cache, const void* Q, int64_t q_stride, int64_t N,
+                                   int64_t n_q_heads, const int32_t* q_start, const int32_t* kv_len,
+                                   const int32_t* table, int64_t table_width, int64_t n_req, int64_t max_q, float scale,
+                                   int causal, int64_t window, void* O, float* LSE, void* workspace, size_t ws_bytes,
+                                   void* stream);
+
+/* What eviction goes by, beside the cache: for every page, head and token of
+ * the cache (dense n_pages x n_heads x page_size) the attention weight that
+ * the key has received, and the position in its sequence where it came in. */
+typedef struct gsi_key_marks {
+  float* weight;
+  int32_t* place;
+} gsi_key_marks;
+
+/* The attention weight that each cached key receives from tokens of its
+ * request, gathered in marks.  Q (its rows, strides and requests), kv_len,
+ * table, scale and causal are those of gsi_paged_attention (without a window:
+ * it names keys by their place, and eviction moves them), LSE (N x n_q_heads)
+ * the logarithms that gsi_paged_attention_lse left for these rows.  For every
+ * key j of request r and every key/value head, over the request's tokens that
+ * see it and the head's query heads,
+ *   w = sum exp(scale q . k_j - LSE),
+ *   weight += w                                       for j < held[r],
+ *   weight  = w, place = j + offsets[r]               for the others:
+ * held (n_req; NULL: none) is the number of keys that had marks before (the
+ * plan's `cached`), offsets (n_req; NULL: zeros) what eviction has taken out.
+ * Q may be the last tokens only of those that came in (the last rows of a
+ * prompt), and q_len 0: keys from held on then begin at zero.  Sums are
+ * float32, in one order for given shapes.  A table entry outside the cache has
+ * no keys.  max_q bounds a request's tokens of Q (it chooses the kernel; a
+ * wrong one costs time, not results).
+ * workspace: zeroed once (gsi_workspace_init), one stream at a time, at least
+ * gsi_key_weights_workspace_size() bytes; it may be the attention's.  Limits as
+ * for gsi_paged_attention. */
+size_t gsi_key_weights_workspace_size(void);
+gsi_status gsi_key_weights(const gsi_cache_desc* cache, const void* Q, int64_t q_stride, int64_t N, int64_t n_q_heads,
+                           const float* LSE, const int32_t* q_start, const int32_t* kv_len, const int32_t* held,
+                           const int32_t* offsets, const int32_t* table, int64_t table_width, int64_t n_req,
+                           int64_t max_q, float scale, int causal, const gsi_key_marks* marks, void* workspace,
+                           size_t ws_bytes, void* stream);
+
+/* Eviction: every request of more than `budget` keys keeps `budget` of them,
+ * chosen for each key/value head by itself: those that came in at the last
+ * `recent` positions (place >= kv_len + offsets - recent), then those of the
+ * first `sinks` (place < sinks), then those of the largest weight, ties to the
+ * lowest index; a NaN counts as the lowest weight, a key whose table entry
+ * lies outside the cache goes first.  recent + sinks <= budget, budget >= 1.
+ * The kept keys among 0 .. budget - 1 stay, the others move, K, V and marks, in
+ * their order into the places given up, in theirs; what lies behind `budget`
+ * is left as it is.  (So the order of cached keys changes: attention without a
+ * window does not depend on it, and turned keys keep their positions.)
+ * kept (n_req): the lengths then; offsets_out (n_req, or NULL): offsets (NULL:
+ * zeros) plus the keys given up, the difference between a request's positions
+ * and its places.  Neither may be kv_len or offsets (GSI_ERR_INVALID_ARG).
+ * Pages are returned by gsi_paged_trim (once, where layers share the table:
+ * every layer keeps the same number of keys).  A page belongs to one request.
+ * workspace: gsi_cache_evict_workspace_size bytes (0, and a message, where the
+ * cache is refused), zeroed or not, one stream at a time; it may be the
+ * attention's.  table_width * page_size <= 2^31 - 512, n_req * n_heads <= 2^27. */
+size_t gsi_cache_evict_workspace_size(const gsi_cache_desc* cache, int64_t n_req, int64_t budget);
+gsi_status gsi_cache_evict(const gsi_cache_desc* cache, const int32_t* kv_len, const int32_t* table,
+                           int64_t table_width, int64_t n_req, const gsi_key_marks* marks, int64_t budget,
+                           int64_t recent, int64_t sinks, const int32_t* offsets, int32_t* kept, int32_t* offsets_out,
+                           void* workspace, size_t ws_bytes, void* stream);
+
+/* Drafted tokens against the target's probabilities.  The rows q_start[r] ..
+ * q_start[r + 1) of a step are request r's last token and its n drafts:
+ * tokens[t] is row t's token, target (N x vocab, float32 or bf16, rows
+ * target_stride apart) row t's probabilities for the token behind it, draft the
+ * probabilities that token was drawn from (a request's last row is not read),
+ * or NULL for drafts that are certain.  In the order of the rows, draft d =
+ * tokens[t + 1] stands if uniforms[t] draft[t][d] < target[t][d] (draft 1 where
+ * NULL); a token outside the vocabulary does not.  At the first that does not,
+ * a token is sampled from max(target - draft, 0) (NULL: target without d), or
+ * from target where that leaves nothing; behind n standing drafts from target:
+ * the first token x whose running sum is above samples[r] times the whole.
+ * Negative probabilities and NaN count as 0, above 1 as 1; sums are exact to
+ * 2^-58 a token.  A row without any mass gives -1; samples are taken within
+ * [0, 1).
+ *   out (N)       row q_start[r] + i: the request's i-th token from here on:
+ *                 the drafts that stand, the sampled token, then -1; rows
+ *                 outside every request are not written
+ *   accepted (n_req)  the drafts that stand
+ *   kept (n_req, or NULL with kv_len NULL)  kv_len[r] less the rows of the
+ *                 drafts that do not: what gsi_paged_trim and the next plan
+ *                 take for the request's length.
+ * A request without rows accepts 0 and keeps kv_len.  out must not be tokens
+ * (GSI_ERR_INVALID_ARG); kept may be kv_len.  Probabilities need only their
+ * natural alignment.  N <= 2^24, n_req <= 2^20, vocab <= 2^24. */
+gsi_status gsi_verify_drafts(const void* target, gsi_dtype tdt, int64_t target_stride, const void* draft, gsi_dtype ddt,
+                             int64_t draft_stride, int64_t N, int64_t vocab, const int32_t* tokens,
+                             const float* uniforms, const float* samples, const int32_t* q_start,
+                             const int32_t* kv_len, int64_t n_req, int32_t* out, int32_t* accepted, int32_t* kept,
+                             void* stream);
 
 typedef enum gsi_norm_kind { GSI_NORM_NONE = 0, GSI_NORM_RMS = 1, GSI_NORM_LAYER = 2 } gsi_norm_kind;
 
