@@ -1,6 +1,8 @@
 // Accumulated attention weights of cached keys: dispatch, and the kernel on the
 // CUDA cores.
 
+#include <algorithm>
+
 #include "gsi_weights.cuh"
 
 namespace gsi {
@@ -155,7 +157,10 @@ static cudaError_t launch_kw(const KeyWeightArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_key_weights(const KeyWeightArgs& a, gsi_dtype dt, int64_t max_q, cudaStream_t s) {
-  return dt == GSI_BF16 ? launch_kw<BF16>(a, s) : launch_kw<F32>(a, s);
+  if (dt == GSI_F32) return launch_kw<F32>(a, s);
+  if (a.N == 0) return launch_kw<BF16>(a, s);  // keys to begin at zero, without a row
+  // (the hint is the caller's: a step of 16 rows has to hold a token's heads)
+  return launch_key_weights_tiles(a, std::clamp<int64_t>(max_q, 1, a.N) * a.group <= 16, s);
 }
 
 }  // namespace gsi

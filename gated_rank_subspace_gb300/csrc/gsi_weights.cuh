@@ -38,6 +38,7 @@ __device__ __forceinline__ void kw_give(const KeyWeightArgs& a, const KwSeg& g, 
   }
 }
 
-cudaError_t launch_key_weights_rows(const KeyWeightArgs& a, gsi_dtype dt, cudaStream_t s);
+// A bf16 cache, on the tensor cores; few: steps of 16 query rows (else 128).  There is a row of Q.
+cudaError_t launch_key_weights_tiles(const KeyWeightArgs& a, bool few, cudaStream_t s);
 
 }  // namespace gsi
