@@ -939,7 +939,7 @@ def cache_evict(cache: PagedCache, kv_len: torch.Tensor, table: torch.Tensor, ma
         if offsets_out is None:
             offsets_out = torch.empty_like(kv_len)
         if workspace is None:
-            workspace = torch.empty(cache_evict_workspace_size(cache, R, budget), dtype=torch.uint8, device=kv_len.device)
+            workspace = new_workspace(cache_evict_workspace_size(cache, R, budget), kv_len.device, stream)
     _ints("kept", kept, R, dev)
     _ints("offsets_out", offsets_out, R, dev)
     if workspace.get_device() != dev or not workspace.is_contiguous():

@@ -1,6 +1,6 @@
 // Eviction from a paged cache by accumulated weight.
 
-#include "gsi_common.cuh"
+#include "gsi_async.cuh"
 #include "gsi_kernels.h"
 
 namespace gsi {
@@ -14,26 +14,36 @@ namespace gsi {
 // A cluster takes one (request, head), a CTA of it a stretch of the keys, a warp a
 // stretch of that:
 //   1. each key's rank as a 32-bit whole number, kept in shared memory;
-//   2. the B-th largest: three histograms over 11, 11 and 10 bits, added over the
-//      cluster, each narrowing the number to one bin of the last;
+//   2. the B-th largest: four histograms of 8 bits, added over the cluster, each
+//      narrowing the number to one bin of the last (wider ones cost more to add
+//      than the pass they save: three of 11, 11 and 10 bits 28 us where four take
+//      25, 80 heads of up to 8003 keys, nothing to move), until a bin stays whole;
 //   3. per warp: how many equal it, then how many gaps and movers there are; the
 //      warps' first numbers are sums over the warps and CTAs before;
 //   4. the lists of gaps and movers (workspace), and the moves, dealt out to all
-//      warps of the cluster: a pair a lane for addresses, weights and places, whole
-//      rows by the warp.
+//      warps of the cluster.
+// Few keys given up (a decode step's one) are found without histograms, as the
+// lowest ranks one after the other, by one CTA.
 // Bound by the bytes where much moves (a row of K and V read and written, 8 bytes
 // a key), by the chain of steps at a decode step's one key.
 constexpr int kEvThreads = 512, kEvWarps = kEvThreads / 32;
 constexpr int kEvHeld = 16384;   // ranks in shared memory; more are formed again in every pass
-constexpr int kEvBins = 2048, kEvMost = 8;
-constexpr size_t kEvSmem = size_t(kEvHeld) * 4;
+constexpr int kEvBins = 256, kEvMost = 8;
+constexpr int kEvBuf = 6144;     // bytes of a warp's rows in flight
+constexpr int kEvFew = 8;        // keys given up that are found one by one
+constexpr size_t kEvSmem = size_t(kEvHeld) * 4 > size_t(kEvWarps) * kEvBuf ? size_t(kEvHeld) * 4 : size_t(kEvWarps) * kEvBuf;
+static_assert(kEvBuf >= 2 * 1024 && kEvBuf % 16 == 0, "two rows of 256 float32 values");
 
 struct EvShared {
-  int hist[kEvBins];             // read by the cluster
+  int hist[2][kEvBins];          // of a pass and the next one (read by the cluster)
   int warps[3][kEvWarps];        // equal, gaps, movers
   int count[3];                  // of this CTA (read by the cluster)
-  int found[2];                  // digit, rank within it
+  int found[3];                  // digit, rank within it, how many there are
   int scan[kEvWarps];
+  unsigned long long low[kEvWarps];
+  uint64_t bar[kEvWarps];        // a warp's rows in flight
+  int gone[kEvFew], gap[kEvFew], mover[kEvFew];
+  int n_moves;
 };
 
 // Whole numbers in the order of weights: NaN lowest, then -inf .. inf.
@@ -44,7 +54,7 @@ __device__ __forceinline__ uint32_t ev_rank(float w) {
 }
 
 __global__ void __launch_bounds__(kEvThreads, 2) cache_evict_kernel(const __grid_constant__ EvictArgs a) {
-  extern __shared__ uint32_t ev_smem[];
+  extern __shared__ __align__(128) uint32_t ev_smem[];
   __shared__ EvShared sh;
   uint32_t* s_rank = ev_smem;
   cg::cluster_group cluster = cg::this_cluster();
@@ -52,6 +62,8 @@ __global__ void __launch_bounds__(kEvThreads, 2) cache_evict_kernel(const __grid
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int unit = blockIdx.x / C, r = unit / a.hkv, h = unit - r * a.hkv;
   pdl_launch_dependents();
+  if (tid < kEvWarps) bar_init(&sh.bar[tid], 1);
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   pdl_wait();
   const int n = int(min(int64_t(max(__ldcg(a.kv_len + r), 0)), a.width << a.page_shift));
   const int B = min(n, a.budget);
@@ -65,53 +77,144 @@ __global__ void __launch_bounds__(kEvThreads, 2) cache_evict_kernel(const __grid
   const int page = 1 << a.page_shift;
   const int32_t* table = a.table + int64_t(r) * a.width;
   auto mark = [&](int pg, int j) { return ((int64_t(pg) * a.hkv + h) << a.page_shift) + (j & (page - 1)); };
-  const int64_t newest = int64_t(n) + gone - a.recent;
-  auto rank_of = [&](int j) -> uint32_t {
-    const int pg = __ldcg(table + (j >> a.page_shift));
-    if (pg < 0 || pg >= a.n_pages) return 0;  // (no key: a place outside the cache goes first)
-    const int64_t at = mark(pg, j);
-    const float w = __ldcg(a.weight + at);
-    const int place = __ldcg(a.place + at);
-    return place >= newest ? 0xffffffffu : place < a.sinks ? 0xfffffffeu : ev_rank(w);
+  const int vec = a.row_bytes / 16;
+  const int64_t head = h * a.head_stride;
+  auto row_of = [&](int pg, int j) { return (pg * a.page_stride + head + int64_t(j & (page - 1)) * a.token_stride) * a.elem; };
+  // one key, by a warp
+  auto move = [&](int dj, int sj) {
+    const int dp = __ldcg(table + (dj >> a.page_shift)), sp = __ldcg(table + (sj >> a.page_shift));
+    if (dp < 0 || dp >= a.n_pages || sp < 0 || sp >= a.n_pages) return;
+    const int64_t from = row_of(sp, sj), to = row_of(dp, dj), s = mark(sp, sj), d = mark(dp, dj);
+    for (int e = lane; e < 2 * vec; e += 32) {
+      char* base = static_cast<char*>(e < vec ? a.K : a.V) + (e < vec ? e : e - vec) * 16;
+      *reinterpret_cast<uint4*>(base + to) = ld_cg_v4(base + from);
+    }
+    if (lane == 0) a.weight[d] = __ldcg(a.weight + s);
+    if (lane == 1) a.place[d] = __ldcg(a.place + s);
   };
+  const int64_t newest = int64_t(n) + gone - a.recent;
+  // ranks of the N keys from j on, `step` apart, those below `end`: their table entries, then their marks, in flight together
+  auto ranks_of = [&](auto& out, int j, int step, int end) {
+    constexpr int N = sizeof(out) / sizeof(out[0]);
+    int pg[N], place[N];
+    float w[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) pg[i] = j + i * step < end ? __ldcg(table + ((j + i * step) >> a.page_shift)) : -1;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const bool there = pg[i] >= 0 && pg[i] < a.n_pages;
+      const int64_t at = there ? mark(pg[i], j + i * step) : 0;
+      w[i] = there ? __ldcg(a.weight + at) : 0.f;
+      place[i] = there ? __ldcg(a.place + at) : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)  // (no key: a place outside the cache goes first)
+      out[i] = pg[i] < 0 || pg[i] >= a.n_pages ? 0
+               : place[i] >= newest            ? 0xffffffffu
+               : place[i] < a.sinks            ? 0xfffffffeu
+                                               : ev_rank(w[i]);
+  };
+  auto hold = [&](int from, int end) {  // the ranks of keys [from, end), which this CTA keeps
+    for (int j = from + tid; j < end; j += 8 * kEvThreads) {
+      uint32_t x[8];
+      ranks_of(x, j, kEvThreads, end);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (j + i * kEvThreads < end) s_rank[j - from + i * kEvThreads] = x[i];
+    }
+  };
+
+  if (n - B <= kEvFew && n <= kEvHeld) {
+    if (c != 0) return;
+    hold(0, n);
+    // the keys given up, from the lowest rank on; of equal ones the last first.  (A thread looks at the ranks it wrote.)
+    unsigned long long last = 0;  // above the one found before
+    for (int e = 0; e < n - B; ++e) {
+      unsigned long long low = ~0ull;
+      for (int j = tid; j < n; j += kEvThreads) {
+        const unsigned long long x = (unsigned long long)s_rank[j] << 32 | (0xffffffffu - unsigned(j));
+        if ((e == 0 || x > last) && x < low) low = x;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const unsigned long long x = __shfl_xor_sync(0xffffffffu, low, o);
+        if (x < low) low = x;
+      }
+      __syncthreads();  // the warps' lowest before have been read
+      if (lane == 0) sh.low[warp] = low;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kEvWarps; ++w) {
+        const unsigned long long x = sh.low[w];
+        if (x < low) low = x;
+      }
+      last = low;
+      if (tid == 0) sh.gone[e] = int(0xffffffffu - unsigned(low));
+    }
+    __syncthreads();
+    if (warp == 0) {
+      const int mine = lane < n - B ? sh.gone[lane] : 0x7fffffff;  // a key given up
+      const int next = B + lane;                                  // a key behind the new length
+      int before = 0;
+      bool stays = lane < n - B;
+      for (int e = 0; e < n - B; ++e) {
+        const int x = __shfl_sync(0xffffffffu, mine, e);
+        before += x < mine;
+        stays = stays && x != next;
+      }
+      if (mine < B) sh.gap[before] = mine;
+      const unsigned b = __ballot_sync(0xffffffffu, stays);
+      if (stays) sh.mover[__popc(b & ((1u << lane) - 1u))] = next;
+      if (lane == 0) sh.n_moves = __popc(b);
+    }
+    __syncthreads();
+    if (warp < sh.n_moves) move(sh.gap[warp], sh.mover[warp]);
+    return;
+  }
+
   // this CTA's keys [j0, j1), this warp's [k0, k1)
   const int j0 = int(int64_t(n) * c / C), j1 = int(int64_t(n) * (c + 1) / C);
   const int k0 = j0 + int(int64_t(j1 - j0) * warp / kEvWarps), k1 = j0 + int(int64_t(j1 - j0) * (warp + 1) / kEvWarps);
   const bool held = j1 - j0 <= kEvHeld;
-  auto rank = [&](int j) { return held ? s_rank[j - j0] : rank_of(j); };
-  for (int e = tid; e < kEvBins; e += kEvThreads) sh.hist[e] = 0;
-  if (held) {
-#pragma unroll 4
-    for (int j = j0 + tid; j < j1; j += kEvThreads) s_rank[j - j0] = rank_of(j);
-  }
+  auto rank = [&](int j) {
+    if (held) return s_rank[j - j0];
+    uint32_t x[1];
+    ranks_of(x, j, 1, k1);
+    return x[0];
+  };
+  for (int e = tid; e < 2 * kEvBins; e += kEvThreads) (&sh.hist[0][0])[e] = 0;
+  if (held) hold(j0, j1);
   __syncthreads();
 
   // ---- the B-th largest rank: `value`, of which the first `ties` stay
   uint32_t value = 0, mask = 0;
   int ties = B;
+  bool all = false;  // every key of the bin stays: all ranks from `value` on
 #pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
+  for (int shift = 24, buf = 0; shift >= 0; shift -= 8, buf ^= 1) {
     for (int j = k0 + lane; j - lane < k1; j += 32) {
       const uint32_t x = j < k1 ? rank(j) : 0;
       const bool in = j < k1 && (x & mask) == value;
-      const int bin = in ? int(x >> shift) & (bins - 1) : -1;
-      const unsigned same = __match_any_sync(0xffffffffu, bin);  // one addition for all lanes of a bin
-      if (in && lane == __ffs(same) - 1) atomicAdd(&sh.hist[bin], __popc(same));
+      const int bin = int(x >> shift) & (kEvBins - 1);
+      const unsigned some = __ballot_sync(0xffffffffu, in);
+      if (some == 0) continue;
+      // one addition where all lanes have one bin (weights that are alike), else one each
+      const int first = __ffs(some) - 1, theirs = __shfl_sync(0xffffffffu, bin, first);
+      if (__all_sync(0xffffffffu, !in || bin == theirs)) {
+        if (lane == first) atomicAdd(&sh.hist[buf][bin], __popc(some));
+      } else if (in) {
+        atomicAdd(&sh.hist[buf][bin], 1);
+      }
     }
     cluster.sync();
-    // a thread adds its neighbouring bins, from the top: bins 4 t .. 4 t + 3 of the reversed order
-    int mine[4], sum = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int bin = bins - 1 - (tid * 4 + i);
-      int v = 0;
-      if (bin >= 0)
-        for (int b = 0; b < C; ++b) v += cluster.map_shared_rank(sh.hist, b)[bin];
-      mine[i] = v;
-      sum += v;
+    // bins from the top, a thread each
+    const int bin = kEvBins - 1 - tid;
+    int count = 0;
+    if (bin >= 0) {
+      for (int b = 0; b < C; ++b) count += cluster.map_shared_rank(sh.hist[buf], b)[bin];
+      sh.hist[buf ^ 1][bin] = 0;  // (of the pass before: every CTA has read it)
     }
-    int inc = sum;
+    int inc = count;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, inc, o);
@@ -119,51 +222,55 @@ __global__ void __launch_bounds__(kEvThreads, 2) cache_evict_kernel(const __grid
     }
     if (lane == 31) sh.scan[warp] = inc;
     __syncthreads();
-    int above = inc - sum;
+    int above = inc - count;
     for (int w = 0; w < warp; ++w) above += sh.scan[w];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (above < ties && ties <= above + mine[i]) {
-        sh.found[0] = bins - 1 - (tid * 4 + i);
-        sh.found[1] = ties - above;
-      }
-      above += mine[i];
+    if (above < ties && ties <= above + count) {  // one thread (those past the bins have no count)
+      sh.found[0] = bin;
+      sh.found[1] = ties - above;
+      sh.found[2] = count;
     }
-    cluster.sync();  // the histograms have been read
-    value |= uint32_t(sh.found[0]) << shift;
-    mask |= uint32_t(bins - 1) << shift;
-    ties = sh.found[1];
-    for (int e = tid; e < kEvBins; e += kEvThreads) sh.hist[e] = 0;
     __syncthreads();
+    value |= uint32_t(sh.found[0]) << shift;
+    mask |= uint32_t(kEvBins - 1) << shift;
+    ties = sh.found[1];
+    all = sh.found[2] == ties;
+    if (all) break;
   }
 
   // ---- numbers of the warps' first equal key, gap and mover
-  auto before = [&](int which) {  // of this warp: over the CTAs and warps before it; all warps have written theirs
+  // sums over the CTAs and warps before this one, of the counts from `which` on; all warps have written theirs
+  auto before = [&](int which, int n_counts, int* out) {
     __syncthreads();
-    if (tid == 0) {
+    if (tid < n_counts) {
       int s = 0;
-      for (int w = 0; w < kEvWarps; ++w) s += sh.warps[which][w];
-      sh.count[which] = s;
+#pragma unroll
+      for (int w = 0; w < kEvWarps; ++w) s += sh.warps[which + tid][w];
+      sh.count[which + tid] = s;
     }
     cluster.sync();
-    int s = 0;
-    for (int b = 0; b < c; ++b) s += cluster.map_shared_rank(sh.count, b)[which];
-    for (int w = 0; w < warp; ++w) s += sh.warps[which][w];
-    return s;
+    for (int i = 0; i < n_counts; ++i) {
+      int s = 0;
+      for (int b = 0; b < c; ++b) s += cluster.map_shared_rank(sh.count, b)[which + i];
+      for (int w = 0; w < warp; ++w) s += sh.warps[which + i][w];
+      out[i] = s;
+    }
   };
-  int eq = 0;
-  for (int j = k0 + lane; j - lane < k1; j += 32) eq += __popc(__ballot_sync(0xffffffffu, j < k1 && rank(j) == value));
-  if (lane == 0) sh.warps[0][warp] = eq;
-  const int eq0 = before(0);
+  int eq0 = 0;
+  if (!all) {
+    int eq = 0;
+    for (int j = k0 + lane; j - lane < k1; j += 32) eq += __popc(__ballot_sync(0xffffffffu, j < k1 && rank(j) == value));
+    if (lane == 0) sh.warps[0][warp] = eq;
+    before(0, 1, &eq0);
+  }
   // walks this warp's keys: f(j, there, stays)
   auto walk = [&](auto f) {
     int seen = eq0;
     for (int j = k0 + lane; j - lane < k1; j += 32) {
       const bool there = j < k1;
       const uint32_t x = there ? rank(j) : 0;
-      const bool same = there && x == value;
+      const bool same = there && !all && x == value;
       const unsigned b = __ballot_sync(0xffffffffu, same);
-      const bool stays = there && (x > value || (same && seen + __popc(b & ((1u << lane) - 1u)) < ties));
+      const bool stays = there && (same ? seen + __popc(b & ((1u << lane) - 1u)) < ties : x >= value);
       seen += __popc(b);
       f(j, there, stays);
     }
@@ -177,7 +284,9 @@ __global__ void __launch_bounds__(kEvThreads, 2) cache_evict_kernel(const __grid
     sh.warps[1][warp] = gaps;
     sh.warps[2][warp] = movers;
   }
-  int gap0 = before(1), mover0 = before(2);
+  int at[2];
+  before(1, 2, at);
+  int gap0 = at[0], mover0 = at[1];
   int32_t* list = a.moves + int64_t(unit) * 2 * a.budget;
   walk([&](int j, bool there, bool stays) {
     const bool gap = there && j < B && !stays, mover = there && j >= B && stays;
@@ -191,48 +300,51 @@ __global__ void __launch_bounds__(kEvThreads, 2) cache_evict_kernel(const __grid
   int total = 0;
   for (int b = 0; b < C; ++b) total += cluster.map_shared_rank(sh.count, b)[1];
   __threadfence();
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the ranks' memory becomes the rows'
   cluster.sync();  // the lists are there, and no CTA's shared memory is read from here on
 
-  // ---- the moves
-  const int vec = a.row_bytes / 16;
-  const int64_t head = h * a.head_stride;
-  for (int i0 = (c * kEvWarps + warp) * 32; i0 < total; i0 += C * kEvThreads) {
-    const int i = i0 + lane;
-    long long from = -1, to = -1;
-    if (i < total) {
+  // ---- the moves: a warp's rows pass through its part of shared memory by bulk copies, a lane a row of K or V
+  uint8_t* buf = reinterpret_cast<uint8_t*>(ev_smem) + warp * kEvBuf;
+  const int pairs = min(32, kEvBuf / a.row_bytes) / 2, stride = C * kEvWarps * pairs;
+  char* base = static_cast<char*>(lane & 1 ? a.V : a.K);
+  struct Row {
+    int64_t from, to, s, d;  // bytes of the row, marks; none: -1
+  };
+  auto row_at = [&](int i0) {
+    const int i = i0 + (lane >> 1);
+    if (lane < 2 * pairs && i < total) {
       const int dj = __ldcg(list + i), sj = __ldcg(list + a.budget + i);
       const int dp = __ldcg(table + (dj >> a.page_shift)), sp = __ldcg(table + (sj >> a.page_shift));
-      if (dp >= 0 && dp < a.n_pages && sp >= 0 && sp < a.n_pages) {
-        from = (sp * a.page_stride + head + int64_t(sj & (page - 1)) * a.token_stride) * a.elem;
-        to = (dp * a.page_stride + head + int64_t(dj & (page - 1)) * a.token_stride) * a.elem;
-        const int64_t s = mark(sp, sj), d = mark(dp, dj);
-        const float w = __ldcg(a.weight + s);
-        const int p = __ldcg(a.place + s);
-        a.weight[d] = w;
-        a.place[d] = p;
-      }
+      if (dp >= 0 && dp < a.n_pages && sp >= 0 && sp < a.n_pages) return Row{row_of(sp, sj), row_of(dp, dj), mark(sp, sj), mark(dp, dj)};
     }
-    const int m = min(32, total - i0);
-    // four pairs' rows in flight
-    for (int p = 0; p < m; p += 4) {
-      long long f[4], t[4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        f[x] = __shfl_sync(0xffffffffu, from, p + x);
-        t[x] = __shfl_sync(0xffffffffu, to, p + x);
-      }
-      for (int e = lane; e < 2 * vec; e += 32) {
-        char* base = static_cast<char*>(e < vec ? a.K : a.V) + (e < vec ? e : e - vec) * 16;
-        uint4 v[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          if (f[x] >= 0) v[x] = ld_cg_v4(base + f[x]);
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          if (f[x] >= 0) *reinterpret_cast<uint4*>(base + t[x]) = v[x];
-      }
+    return Row{-1, -1, -1, -1};
+  };
+  int i0 = (c * kEvWarps + warp) * pairs;
+  Row now = row_at(i0);
+  bool ok = true;
+  for (uint32_t phase = 0; ok && i0 < total; i0 += stride, phase ^= 1) {
+    const bool there = now.from >= 0;
+    const int rows = __popc(__ballot_sync(0xffffffffu, there));
+    if (lane == 0) bar_expect_tx(&sh.bar[warp], uint32_t(rows * a.row_bytes));
+    __syncwarp();
+    if (there) bulk_g2s(buf + lane * a.row_bytes, base + now.from, uint32_t(a.row_bytes), &sh.bar[warp]);
+    const Row next = row_at(i0 + stride);
+    if (there) {
+      if (lane & 1)
+        a.place[now.d] = __ldcg(a.place + now.s);
+      else
+        a.weight[now.d] = __ldcg(a.weight + now.s);
     }
+    ok = __all_sync(0xffffffffu, bar_wait(&sh.bar[warp], phase, a.err));
+    if (ok && there)
+      asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(base + now.to), "r"(sa(buf + lane * a.row_bytes)),
+                   "r"(uint32_t(a.row_bytes))
+                   : "memory");
+    asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();  // every lane's row has been read: the buffer may be filled again
+    now = next;
   }
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t s) {
@@ -241,8 +353,10 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t s) {
       ready([] { return cudaFuncSetAttribute(cache_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kEvSmem)); });
   if (e != cudaSuccess) return e;
   const int64_t units = int64_t(a.n_req) * a.hkv, most = a.width << a.page_shift;
-  unsigned C = 1;  // as many CTAs a unit as there are SMs for, of 512 keys at least
-  while (C < unsigned(kEvMost) && units * C * 2 <= 2 * sm_count() && most > int64_t(C) * 512) C *= 2;
+  // As many CTAs a unit as the SMs hold, of 512 keys at least.  80 heads of up to 8003 keys to 2048, us: 1 CTA each 80, 2 62, 4
+  // (a few of them left over for a second turn) 60, 8 75.
+  unsigned C = 1;
+  while (C < unsigned(kEvMost) && units * C * 2 <= 3 * sm_count() && most > int64_t(C) * 512) C *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(unsigned(units * C));
   cfg.blockDim = dim3(kEvThreads);

@@ -409,6 +409,7 @@ struct EvictArgs {
   int32_t* kept;
   int32_t* offsets_out;
   int32_t* moves;        // [n_req * hkv][2][budget]
+  uint32_t* err;         // the workspace's error word
 };
 // The lists lie behind the counters that the attention keeps in a workspace.
 constexpr size_t kEvictMovesAt = 4608;

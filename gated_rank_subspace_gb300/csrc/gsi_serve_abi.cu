@@ -518,6 +518,7 @@ gsi_status gsi_cache_evict(const gsi_cache_desc* cache, const int32_t* kv_len, c
   a.kept = kept;
   a.offsets_out = offsets_out;
   a.moves = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + kEvictMovesAt);
+  a.err = &static_cast<Ctrl*>(workspace)->err;
   return launched(launch_cache_evict(a, static_cast<cudaStream_t>(stream)), "cache eviction launch");
 }
 

@@ -12,19 +12,24 @@ namespace gsi {
 // drafts comes one of p:  the smallest token x with
 //   sum_{y <= x} m(y) > v sum_y m(y).
 // Sums of 10^5 probabilities have to be right to far below one of them, whatever
-// their order: p and q become whole multiples of 2^-58 (exact from 2^-35 on), whose
+// their order: p and q become whole multiples of 2^-46 (exact from 2^-23 on), whose
 // differences and sums are exact in 64 bits; v times the total is formed in 128.
 //
 // A cluster takes a request.  Every CTA finds the row (the drafts' probabilities
 // are a few loads), then each sums a stretch of the row, a warp a stretch of that;
-// the one whose stretch holds the token looks through it again.  The bytes of the
-// one row of p and q bound it, for few requests the chain of loads and exchanges.
+// the CTA whose stretch holds the token looks through the warp's part of it again,
+// all its threads four tokens each.  The bytes of the one row of p and q bound it,
+// for few requests the chain of loads and exchanges.
 constexpr int kVfThreads = 512, kVfWarps = kVfThreads / 32, kVfMost = 8;
-constexpr int kVfUnroll = 4;  // loads of each row in flight a lane
+constexpr int kVfUnroll = 8;  // loads of each row in flight a lane
 
-// A probability in units of 2^-58: negative ones and NaN are 0, above 1 is 1.
-__device__ __forceinline__ unsigned long long vf_units(float p) {
-  return __float2ull_rz(fminf(fmaxf(p, 0.f), 1.f) * 288230376151711744.f);  // (fmaxf drops NaN)
+// A probability within 0 .. 1 (NaN: 0) as hi 2^-23 + lo 2^-46, both rounded to nearest: adding 1 leaves x's multiple of
+// 2^-23 in the sum's lower bits, and the rest, which is exact, added to 1.5 2^-23 its multiple of 2^-46.  (Conversions to
+// 64-bit numbers run at a fraction of the rate: 88 us with them where this takes %%US%%, 64 rows of 100003.)
+__device__ __forceinline__ int2 vf_split(float x) {
+  x = __saturatef(x);
+  const float h = __fadd_rn(x, 1.f), l = __fadd_rn(__fsub_rn(x, __fsub_rn(h, 1.f)), 0x1.8p-23f);
+  return make_int2(__float_as_int(h) - __float_as_int(1.f), __float_as_int(l) - __float_as_int(0x1.8p-23f));
 }
 
 struct VfShared {
@@ -75,21 +80,27 @@ __global__ void __launch_bounds__(kVfThreads, 2) verify_drafts_kernel(const __gr
   const int x0 = int(int64_t(a.vocab) * c / C), x1 = int(int64_t(a.vocab) * (c + 1) / C);
   const int y0 = x0 + int(int64_t(x1 - x0) * warp / kVfWarps), y1 = x0 + int(int64_t(x1 - x0) * (warp + 1) / kVfWarps);
   bool left = taken < n;  // what the draft leaves of the target, else the target itself
-  auto mass = [&](int x) -> unsigned long long {
-    const unsigned long long p = vf_units(p_at(t, x));
-    if (!left) return p;
-    if (!a.draft) return x == gone ? 0 : p;
-    const unsigned long long q = vf_units(q_at(t, x));
-    return p > q ? p - q : 0;
+  // the mass of a token with probabilities p and q, in units of 2^-46
+  auto mass = [&](float p, float q, int x) -> long long {
+    const int2 u = vf_split(p);
+    if (!left) return (long long)u.x * (1 << 23) + u.y;
+    if (!a.draft) return x == gone ? 0 : (long long)u.x * (1 << 23) + u.y;
+    const int2 w = vf_split(q);
+    // (the split is monotone; NaN compares as 0)
+    const long long m = (long long)(u.x - w.x) * (1 << 23) + (u.y - w.y);
+    return m > 0 ? m : 0;
   };
+  const bool both = a.draft != nullptr;
   for (;;) {
     unsigned long long sum = 0;
     for (int x = y0 + lane; x < y1; x += 32 * kVfUnroll) {
-      unsigned long long m[kVfUnroll];
+      float p[kVfUnroll], q[kVfUnroll];
 #pragma unroll
-      for (int i = 0; i < kVfUnroll; ++i) m[i] = x + 32 * i < y1 ? mass(x + 32 * i) : 0;
+      for (int i = 0; i < kVfUnroll; ++i) p[i] = x + 32 * i < y1 ? p_at(t, x + 32 * i) : 0.f;
 #pragma unroll
-      for (int i = 0; i < kVfUnroll; ++i) sum += m[i];
+      for (int i = 0; i < kVfUnroll; ++i) q[i] = both && left && x + 32 * i < y1 ? q_at(t, x + 32 * i) : 0.f;
+#pragma unroll
+      for (int i = 0; i < kVfUnroll; ++i) sum += mass(p[i], q[i], x + 32 * i);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -118,22 +129,43 @@ __global__ void __launch_bounds__(kVfThreads, 2) verify_drafts_kernel(const __gr
     // the token's mass ends above floor(v total)
     const float v = fminf(fmaxf(__ldcg(a.samples + r), 0.f), 0x1.fffffep-1f);
     const unsigned long long at = __umul64hi(total, __float2ull_rz(v * 18446744073709551616.f));
-    for (int w = 0; w < warp; ++w) base += sh.warps[w];
-    if (base <= at && at < base + sum) {  // in this warp's stretch (one warp of the cluster)
-      for (int x = y0 + lane; x - lane < y1; x += 32) {
-        unsigned long long inc = x < y1 ? mass(x) : 0;
+    if (at < base || at >= base + sh.total) break;  // in another CTA's stretch
+    int w = 0;
+    for (; at >= base + sh.warps[w]; ++w) base += sh.warps[w];
+    const int z0 = x0 + int(int64_t(x1 - x0) * w / kVfWarps), z1 = x0 + int(int64_t(x1 - x0) * (w + 1) / kVfWarps);
+    for (int z = z0; z < z1; z += 4 * kVfThreads) {
+      long long m[4];
+      float p[4], q[4];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const unsigned long long z = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += z;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, base + inc > at);
-        if (hit) {
-          if (lane == 0) a.out[t] = x + __ffs(hit) - 1;
-          break;
-        }
-        base += __shfl_sync(0xffffffffu, inc, 31);
+      for (int i = 0; i < 4; ++i) {
+        const int x = z + 4 * tid + i;
+        p[i] = x < z1 ? p_at(t, x) : 0.f;
+        q[i] = both && left && x < z1 ? q_at(t, x) : 0.f;
       }
+      unsigned long long mine = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mine += m[i] = mass(p[i], q[i], z + 4 * tid + i);
+      unsigned long long inc = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      __syncthreads();  // the sums before have been read
+      if (lane == 31) sh.warps[warp] = inc;
+      __syncthreads();
+      unsigned long long from = base + inc - mine, all = 0;
+      for (int i = 0; i < kVfWarps; ++i) {
+        if (i < warp) from += sh.warps[i];
+        all += sh.warps[i];
+      }
+      if (from <= at && at < from + mine) {  // one thread
+        int i = 0;
+        for (; i < 3 && at >= from + m[i]; ++i) from += m[i];
+        a.out[t] = z + 4 * tid + i;
+      }
+      base += all;
+      if (at < base) break;
     }
     break;
   }

@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kKwThreads, 1) key_weights_kernel(const __grid
 #pragma unroll
       for (int w = 0; w < kKwThreads / 32; ++w) sum += s_sum[w][tid];
     if (g.a == 0 && g.b == g.n) {
-      if (tid < kKwKeys) kw_give(a, g, key0 + tid, sum);
+      if (tid < kKwKeys) kw_give(a, g, key0 + tid, kw_mark(a, g, key0 + tid), sum);
     } else {
       int b0, b1;
       walk.parts(g, b0, b1);
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kKwThreads, 1) key_weights_kernel(const __grid
         __threadfence();
         sum = 0.f;
         for (int b = b0; b <= b1; ++b) sum += __ldcg(kw_part(a, 2 * b + (b == b0)) + tid);
-        kw_give(a, g, key0 + tid, sum);
+        kw_give(a, g, key0 + tid, kw_mark(a, g, key0 + tid), sum);
       }
     }
     __syncthreads();  // before the next part writes the shared rows

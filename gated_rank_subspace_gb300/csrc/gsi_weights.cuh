@@ -24,17 +24,31 @@ __device__ __forceinline__ float* kw_part(const KeyWeightArgs& a, int slot) {
 }
 __device__ __forceinline__ uint32_t* kw_err(const KeyWeightArgs& a) { return &static_cast<Ctrl*>(a.work)->err; }
 
-// Gives the sum of a unit's key to the key: added to what it has, or its first.
-__device__ __forceinline__ void kw_give(const KeyWeightArgs& a, const KwSeg& g, int key, float sum) {
-  if (key >= g.q.len || (g.q.q_len == 0 && key < g.q.held)) return;
+// Where a unit's key has its marks, and what it has gathered: two loads, one behind the other, that are issued before the sum
+// is needed.
+struct KwMark {
+  int64_t at;  // none: -1
+  float old;
+  int shift;   // the request's offset
+};
+__device__ __forceinline__ KwMark kw_mark(const KeyWeightArgs& a, const KwSeg& g, int key) {
+  KwMark m{-1, 0.f, 0};
+  if (key >= g.q.len || (g.q.q_len == 0 && key < g.q.held)) return m;
   const int pg = __ldcg(a.table + int64_t(g.r) * a.width + (key >> a.page_shift));
-  if (pg < 0 || pg >= a.n_pages) return;
-  const int64_t at = ((int64_t(pg) * a.hkv + g.h) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+  if (key >= g.q.held && a.offsets) m.shift = __ldcg(a.offsets + g.r);
+  if (pg < 0 || pg >= a.n_pages) return m;
+  m.at = ((int64_t(pg) * a.hkv + g.h) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+  if (key < g.q.held) m.old = __ldcg(a.weight + m.at);
+  return m;
+}
+// Gives the sum of a unit's key to the key: added to what it has, or its first.
+__device__ __forceinline__ void kw_give(const KeyWeightArgs& a, const KwSeg& g, int key, const KwMark& m, float sum) {
+  if (m.at < 0) return;
   if (key < g.q.held) {
-    a.weight[at] = __ldcg(a.weight + at) + sum;
+    a.weight[m.at] = m.old + sum;
   } else {
-    a.weight[at] = sum;
-    a.place[at] = key + (a.offsets ? __ldcg(a.offsets + g.r) : 0);
+    a.weight[m.at] = sum;
+    a.place[m.at] = key + m.shift;
   }
 }
 

@@ -211,6 +211,9 @@ __global__ void __launch_bounds__(KtCfg<NS, NR>::kThreads, 1)
       const int key = g.t * kKtKeys + row;
       const int n_steps = g.q.q_len > 0 ? g.b - g.a : 0;
       const int ends = n_steps > 0 ? (step + n_steps - 1) & 1 : 0;  // the warpgroup that ends the part
+      const bool whole = g.a == 0 && g.b == g.n;
+      KwMark mark{-1, 0.f, 0};
+      if (whole && wg == ends) mark = kw_mark(a, g, key);  // ahead of the wait for the scores
       unsigned long long acc[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
       for (int i = 0; i < n_steps; ++i, ++step) {
         if ((step & 1) != wg) continue;
@@ -274,8 +277,8 @@ __global__ void __launch_bounds__(KtCfg<NS, NR>::kThreads, 1)
         if (wg == ends) sum += half[row];
       }
       if (wg != ends) continue;
-      if (g.a == 0 && g.b == g.n) {
-        kw_give(a, g, key, sum);
+      if (whole) {
+        kw_give(a, g, key, mark, sum);
         continue;
       }
       int b0, b1;
@@ -293,7 +296,7 @@ __global__ void __launch_bounds__(KtCfg<NS, NR>::kThreads, 1)
         __threadfence();
         sum = 0.f;
         for (int b = b0; b <= b1; ++b) sum += __ldcg(kw_part(a, 2 * b + (b == b0)) + row);
-        kw_give(a, g, key, sum);
+        kw_give(a, g, key, kw_mark(a, g, key), sum);
       }
       wg_sync();  // before the flag is written again
     }

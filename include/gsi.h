@@ -587,9 +587,9 @@ gsi_status gsi_key_weights(const gsi_cache_desc* cache, const void* Q, int64_t q
  * and its places.  Neither may be kv_len or offsets (GSI_ERR_INVALID_ARG).
  * Pages are returned by gsi_paged_trim (once, where layers share the table:
  * every layer keeps the same number of keys).  A page belongs to one request.
- * workspace: gsi_cache_evict_workspace_size bytes (0, and a message, where the
- * cache is refused), zeroed or not, one stream at a time; it may be the
- * attention's.  table_width * page_size <= 2^31 - 512, n_req * n_heads <= 2^27. */
+ * workspace: zeroed once (gsi_workspace_init), one stream at a time, at least
+ * gsi_cache_evict_workspace_size bytes (0, and a message, where the cache is
+ * refused); it may be the attention's.  table_width * page_size <= 2^31 - 512, n_req * n_heads <= 2^27. */
 size_t gsi_cache_evict_workspace_size(const gsi_cache_desc* cache, int64_t n_req, int64_t budget);
 gsi_status gsi_cache_evict(const gsi_cache_desc* cache, const int32_t* kv_len, const int32_t* table,
                            int64_t table_width, int64_t n_req, const gsi_key_marks* marks, int64_t budget,
@@ -608,7 +608,7 @@ gsi_status gsi_cache_evict(const gsi_cache_desc* cache, const int32_t* kv_len, c
  * from target where that leaves nothing; behind n standing drafts from target:
  * the first token x whose running sum is above samples[r] times the whole.
  * Negative probabilities and NaN count as 0, above 1 as 1; sums are exact to
- * 2^-58 a token.  A row without any mass gives -1; samples are taken within
+ * 2^-47 a token.  A row without any mass gives -1; samples are taken within
  * [0, 1).
  *   out (N)       row q_start[r] + i: the request's i-th token from here on:
  *                 the drafts that stand, the sampled token, then -1; rows

@@ -409,7 +409,7 @@ def test_evict_on_another_stream_and_in_a_graph(gsi):
     kept, out = gsi.cache_evict(cache, lens, tab, marks, 64)
     ref = [t.clone() for t in (cache.K, cache.V, marks.weight, marks.place, kept, out)]
     s = torch.cuda.Stream()
-    work = torch.empty(gsi.cache_evict_workspace_size(cache, 2, 64), dtype=torch.uint8, device="cuda")
+    work = gsi.new_workspace(gsi.cache_evict_workspace_size(cache, 2, 64))
 
     def reset():
         cache.K.copy_(K), cache.V.copy_(V), marks.weight.copy_(W), marks.place.copy_(P), kept.zero_(), out.zero_()
