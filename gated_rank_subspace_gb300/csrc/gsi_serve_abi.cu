@@ -382,8 +382,8 @@ static gsi_status check_marks(const gsi_cache_desc* c, const gsi_key_marks* m) {
   if (c->n_pages == 0) return GSI_OK;
   const float* weight = m->weight;
   const int32_t* place = m->place;
-  GSI_NEED(weight, 4);
-  GSI_NEED(place, 4);
+  GSI_NEED(weight, 16);
+  GSI_NEED(place, 16);
   return GSI_OK;
 }
 

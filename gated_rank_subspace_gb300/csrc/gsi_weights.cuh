@@ -15,12 +15,13 @@ namespace gsi {
 // (The counters lie where the attention's do, the parts behind them: one workspace serves both.)
 constexpr size_t kKwCounterBytes = 4096;
 static_assert(4 * kKwCtas <= int(kKwCounterBytes), "a counter a CTA");
-inline size_t kw_work_bytes() { return sizeof(Ctrl) + kKwCounterBytes + size_t(2) * kKwCtas * 128 * 4; }
+constexpr int kKwPart = 128;  // sums of a part, at most
+inline size_t kw_work_bytes() { return sizeof(Ctrl) + kKwCounterBytes + size_t(2) * kKwCtas * kKwPart * 4; }
 __device__ __forceinline__ unsigned* kw_counter(const KeyWeightArgs& a, int cta) {
   return reinterpret_cast<unsigned*>(static_cast<char*>(a.work) + sizeof(Ctrl)) + cta;
 }
 __device__ __forceinline__ float* kw_part(const KeyWeightArgs& a, int slot) {
-  return reinterpret_cast<float*>(static_cast<char*>(a.work) + sizeof(Ctrl) + kKwCounterBytes) + size_t(slot) * 128;
+  return reinterpret_cast<float*>(static_cast<char*>(a.work) + sizeof(Ctrl) + kKwCounterBytes) + size_t(slot) * kKwPart;
 }
 __device__ __forceinline__ uint32_t* kw_err(const KeyWeightArgs& a) { return &static_cast<Ctrl*>(a.work)->err; }
 
@@ -52,7 +53,8 @@ __device__ __forceinline__ void kw_give(const KeyWeightArgs& a, const KwSeg& g, 
   }
 }
 
-// A bf16 cache, on the tensor cores; few: steps of 16 query rows (else 128).  There is a row of Q.
+// A bf16 cache, on the tensor cores; few: steps of 16 query rows (else 128).  There is a row of Q, and a step holds a token's
+// heads.
 cudaError_t launch_key_weights_tiles(const KeyWeightArgs& a, bool few, cudaStream_t s);
 
 }  // namespace gsi

@@ -19,7 +19,8 @@ namespace gsi {
 //
 // tpt is a power of two that divides KT, so the row tiles that tile t loses to
 // the causal mask are t k - c, with k = KT / tpt and c = ceil((len - q_len) /
-// tpt): the steps of the first x tiles are an arithmetic series.
+// tpt): the steps of the first x tiles are an arithmetic series.  (A unit that no
+// row sees counts as one step: its keys may have to begin at zero.)
 constexpr int kKwCtas = 304;  // CTAs of a launch, at most: two an SM
 
 struct KwReq {
@@ -56,12 +57,6 @@ struct KwShape {
   __device__ __forceinline__ long long skip(const KeyWeightArgs& a, const KwReq& q) const {
     return a.causal ? -(-(long long)(q.len - q.q_len) >> shift) : (1ll << 40);
   }
-  // first row tile that sees a key of tile t, and how many do (one step at least)
-  __device__ __forceinline__ void steps(const KeyWeightArgs& a, const KwReq& q, int t, int& u0, int& n) const {
-    const long long u = (long long)t * (KT >> shift) - skip(a, q);
-    u0 = u > 0 ? int(u) : 0;
-    n = max(1, row_tiles(q) - u0);
-  }
   // steps of the tiles before x
   __device__ __forceinline__ long long prefix(const KeyWeightArgs& a, const KwReq& q, int x) const {
     const int t0 = first_tile(q);
@@ -75,28 +70,39 @@ struct KwShape {
   }
 };
 
-// A CTA's share, walked part by part; every role of a CTA walks it alike.
+// A CTA's share, walked part by part; every role of a CTA walks it alike, and few of its steps are more than additions.
 template <int KT>
 struct KwWalk {
   KwShape<KT> shape;
   KwReq q;
-  int r, h, t;
+  int r, h, t;                // request, head, tile
+  int first, tiles, row_tiles;
+  long long u;                // first row tile that sees the tile, where positive
   long long off;              // steps of the tile at t that lie before this place
   long long total, pos, end;  // steps of the line, and this CTA's
   int grid;                   // CTAs that have a share
 
+  __device__ __forceinline__ void enter(const KeyWeightArgs& a, const KwReq& q_, int t_) {  // tile t of a request
+    q = q_;
+    first = shape.first_tile(q);
+    tiles = shape.tiles(q);
+    row_tiles = shape.row_tiles(q);
+    t = t_ < 0 ? first : t_;
+    u = (long long)t * (KT >> shape.shift) - shape.skip(a, q);
+  }
   __device__ __forceinline__ bool next(const KeyWeightArgs& a, KwSeg& g) {
     if (pos >= end) return false;
-    while (t >= shape.tiles(q)) {  // the next head or request with a step (there is one)
-      if (q.len > shape.first_tile(q) * KT && h + 1 < a.hkv) {
+    while (t >= tiles) {  // the next head or request with a step (there is one)
+      if (tiles > first && h + 1 < a.hkv) {
         ++h;
+        enter(a, q, -1);
       } else {
-        q = shape.request(a, ++r);
         h = 0;
+        enter(a, shape.request(a, ++r), -1);
       }
-      t = shape.first_tile(q);
     }
-    shape.steps(a, q, t, g.u0, g.n);
+    g.u0 = u > 0 ? int(u) : 0;
+    g.n = max(1, row_tiles - g.u0);
     g.q = q;
     g.r = r;
     g.h = h;
@@ -108,6 +114,7 @@ struct KwWalk {
     pos += g.b - g.a;
     off = 0;
     ++t;
+    u += KT >> shape.shift;
     return true;
   }
   // The CTAs that hold parts of a unit.
@@ -117,19 +124,29 @@ struct KwWalk {
   }
 };
 
+// Whole quotient of a by b > 0 (in 32 bits, a fifth of the time, where they suffice).
+__device__ __forceinline__ long long kw_div(long long a, long long b) {
+  if (((a | b) >> 31) == 0) return int(a) / int(b);
+  return a / b;
+}
+
 // The share of CTA blockIdx.x; all NT threads of the block.
 template <int KT, int NT>
 __device__ __forceinline__ void kw_share(const KeyWeightArgs& a, int tpt, KwWalk<KT>& w) {
-  __shared__ long long s_sum[NT / 32];
-  __shared__ KwWalk<KT> s_walk;
+  __shared__ long long s_sum[NT / 32], s_at;
+  __shared__ KwReq s_req;
+  __shared__ int s_r;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  KwShape<KT> shape;
-  shape.tpt = tpt;
-  shape.shift = __ffs(tpt) - 1;
+  w.shape.tpt = tpt;
+  w.shape.shift = __ffs(tpt) - 1;
   const int r0 = int((long long)a.n_req * tid / NT), r1 = int((long long)a.n_req * (tid + 1) / NT);
   long long mine = 0;
+  KwReq q{};  // of request r0
 #pragma unroll 1
-  for (int r = r0; r < r1; ++r) mine += shape.head_steps(a, shape.request(a, r)) * a.hkv;
+  for (int r = r1 - 1; r >= r0; --r) {
+    q = w.shape.request(a, r);
+    mine += w.shape.head_steps(a, q) * a.hkv;
+  }
   long long inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -144,41 +161,44 @@ __device__ __forceinline__ void kw_share(const KeyWeightArgs& a, int tpt, KwWalk
     if (i < warp) before += s_sum[i];
     total += s_sum[i];
   }
-  const int grid = int(total < (long long)gridDim.x ? total : (long long)gridDim.x);
-  const bool some = int(blockIdx.x) < grid;
-  const long long pos = some ? total * blockIdx.x / grid : 0, end = some ? total * (blockIdx.x + 1) / grid : 0;
-  if (!some && tid == 0) {
-    s_walk.pos = s_walk.end = 0;
-  } else if (some && before <= pos && pos < before + mine) {
-    KwWalk<KT> p;
-    p.shape = shape;
-    p.total = total;
-    p.pos = pos;
-    p.end = end;
-    p.grid = grid;
-    long long at = pos - before, per;
-    p.r = r0;
+  w.total = total;
+  w.grid = int(total < (long long)gridDim.x ? total : (long long)gridDim.x);
+  const bool some = int(blockIdx.x) < w.grid;
+  w.pos = some ? kw_div(total * blockIdx.x, w.grid) : 0;
+  w.end = some ? kw_div(total * (blockIdx.x + 1), w.grid) : 0;
+  if (some && before <= w.pos && w.pos < before + mine) {  // the request, by the thread that counted it
+    long long at = w.pos - before;
+    int r = r0;
 #pragma unroll 1
-    for (;; ++p.r) {
-      p.q = shape.request(a, p.r);
-      per = shape.head_steps(a, p.q);
-      if (at < per * a.hkv) break;
-      at -= per * a.hkv;
+    for (;;) {
+      const long long n = w.shape.head_steps(a, q) * a.hkv;
+      if (at < n) break;
+      at -= n;
+      q = w.shape.request(a, ++r);
     }
-    p.h = int(at / per);
-    at -= p.h * per;
-    int lo = shape.first_tile(p.q), hi = shape.tiles(p.q);  // the last tile that begins at or before `at`
-#pragma unroll 1
-    while (hi - lo > 1) {
-      const int mid = lo + (hi - lo) / 2;
-      if (shape.prefix(a, p.q, mid) <= at) lo = mid; else hi = mid;
-    }
-    p.t = lo;
-    p.off = at - shape.prefix(a, p.q, lo);
-    s_walk = p;
+    s_at = at;
+    s_req = q;
+    s_r = r;
   }
   __syncthreads();
-  w = s_walk;
+  if (!some) return;
+  // the head, and the last tile that begins at or before the place: a warp tries 32 at a time (each warp for itself)
+  const KwReq mine_q = s_req;
+  const long long per = w.shape.head_steps(a, mine_q);
+  w.r = s_r;
+  w.h = int(kw_div(s_at, per));
+  const long long at = s_at - w.h * per;
+  int lo = w.shape.first_tile(mine_q), hi = w.shape.tiles(mine_q);
+#pragma unroll 1
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const long long mid = lo + (long long)(lane + 1) * step;
+    const bool reached = mid < hi && w.shape.prefix(a, mine_q, int(mid)) <= at;
+    lo += __popc(__ballot_sync(0xffffffffu, reached)) * step;
+    hi = min(hi, lo + step);
+  }
+  w.enter(a, mine_q, lo);
+  w.off = at - w.shape.prefix(a, mine_q, lo);
 }
 
 }  // namespace gsi

@@ -539,7 +539,8 @@ gsi_status gsi_paged_attention_lse(const gsi_cache_desc* cache, const void* Q, i
 
 /* What eviction goes by, beside the cache: for every page, head and token of
  * the cache (dense n_pages x n_heads x page_size) the attention weight that
- * the key has received, and the position in its sequence where it came in. */
+ * the key has received, and the position in its sequence where it came in.
+ * Both 16-byte aligned. */
 typedef struct gsi_key_marks {
   float* weight;
   int32_t* place;

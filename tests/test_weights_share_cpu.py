@@ -23,9 +23,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 
 def cases():
     rng = random.Random(5)
-    out = [(kt, 3, 16, 1, 1, 4, 9, [], []) for kt in (64, 128)]
+    out = [(kt, 3, 16, 1, 1, 4, 9, [], []) for kt in (64, 128, 256)]
     for i in range(260):
-        kt = rng.choice([64, 128])
+        kt = rng.choice([64, 128, 256])
         tpt = rng.choice([t for t in (1, 2, 4, 8, 16, 32, 64, 128) if t <= kt])
         n_req = rng.choice([1, 1, 2, 3, 9, 40, 500])
         most_q, most_k = rng.choice([(1, 900), (3, 60), (40, 700), (700, 2000), (300, 100)])

@@ -34,7 +34,7 @@ struct Index {
 };
 static Index threadIdx, blockIdx, gridDim;
 
-constexpr int kMaxThreads = 384;
+constexpr int kMaxThreads = 448;
 static ucontext_t g_main, g_fiber[kMaxThreads];
 static bool g_done[kMaxThreads];
 static std::vector<char> g_stacks(size_t(kMaxThreads) * 65536);
@@ -75,6 +75,13 @@ static T __shfl_up_sync(unsigned, T v, int o) {
   const int lane = threadIdx.x % 32;
   return lane >= o ? T(all[lane - o]) : v;
 }
+static unsigned __ballot_sync(unsigned, bool p) {
+  const long long* all = warp_meet(p);
+  unsigned bits = 0;
+  for (int i = 0; i < 32; ++i) bits |= unsigned(all[i]) << i;
+  return bits;
+}
+static int __popc(unsigned x) { return __builtin_popcount(x); }
 static void __syncthreads() { g_block.meet(threadIdx.x, 0); }
 static int __ffs(int x) { return __builtin_ffs(x); }
 
@@ -176,7 +183,7 @@ int main() {
     a.kv_len = len.data();
     a.held = held.data();
     gridDim.x = grid;
-    if (kt == 64) run<64, 256>(a, grid); else run<128, 384>(a, grid);
+    if (kt == 64) run<64, 256>(a, grid); else if (kt == 128) run<128, 448>(a, grid); else run<256, 448>(a, grid);
   }
   return 0;
 }
