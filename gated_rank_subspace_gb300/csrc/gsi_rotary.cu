@@ -34,22 +34,35 @@ __device__ __forceinline__ float2 rotary_turn(unsigned long long rate, int64_t p
   return quarter == 0 ? make_float2(c, s) : quarter == 1 ? make_float2(-s, c) : quarter == 2 ? make_float2(-c, -s) : make_float2(s, -c);
 }
 
-// N values of a row from element e on, as float32.
+// N values of a row from element e on: as they are, and as float32.
 template <class XT, int N>
-__device__ __forceinline__ void rotary_load(const char* row, int64_t e, float (&f)[N]) {
+struct RotaryValues {
+  static constexpr int kBytes = N * XT::kBytes;
+  uint4 v[(kBytes + 15) / 16];
+  __device__ __forceinline__ void load(const char* row, int64_t e) {
+    if constexpr (kBytes == 8) {  // four bf16 values for a float32 vector
+      const uint2 u = __ldcg(reinterpret_cast<const uint2*>(row + e * XT::kBytes));
+      v[0] = make_uint4(u.x, u.y, 0, 0);
+    } else {
 #pragma unroll
-  for (int i = 0; i < N * XT::kBytes / 16; ++i) {
-    float v[XT::kPerVec];
-    XT::unpack(ld_cg_v4(row + e * XT::kBytes + 16 * i), v);
+      for (int i = 0; i < kBytes / 16; ++i) v[i] = ld_cg_v4(row + e * XT::kBytes + 16 * i);
+    }
+  }
+  __device__ __forceinline__ void floats(float (&f)[N]) const {
+    if constexpr (kBytes == 8) {
+      BF16::unpack2(v[0].x, f[0], f[1]);
+      BF16::unpack2(v[0].y, f[2], f[3]);
+    } else {
 #pragma unroll
-    for (int x = 0; x < XT::kPerVec; ++x) f[i * XT::kPerVec + x] = v[x];
+      for (int i = 0; i < kBytes / 16; ++i) {
+        float w[XT::kPerVec];
+        XT::unpack(v[i], w);
+#pragma unroll
+        for (int x = 0; x < XT::kPerVec; ++x) f[i * XT::kPerVec + x] = w[x];
+      }
+    }
   }
-  if constexpr (N * XT::kBytes == 8) {  // four bf16 values for a float32 vector
-    const uint2 u = __ldcg(reinterpret_cast<const uint2*>(row + e * XT::kBytes));
-    BF16::unpack2(u.x, f[0], f[1]);
-    BF16::unpack2(u.y, f[2], f[3]);
-  }
-}
+};
 template <class CT, int N>
 __device__ __forceinline__ void rotary_store(char* dst, const float (&f)[N]) {
   if constexpr (CT::kBytes == 2)
@@ -83,10 +96,9 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_append_kernel(const __g
   const char* row = static_cast<const char*>(a.X) + t * a.row_stride * XT::kBytes;
   const bool whole = half % N == 0;  // a vector's partners are a vector
   __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int v = (blockIdx.y * 2 + i) * kRotaryThreads + threadIdx.x;
-    if (v >= n_vec) return;
+  const int stride = gridDim.y * kRotaryThreads;
+#pragma unroll 2
+  for (int v = blockIdx.y * kRotaryThreads + threadIdx.x; v < n_vec; v += stride) {
     int head = v / per_head;
     const int e = (v - head * per_head) * N;
     const int64_t first = int64_t(head) * a.dim;  // of the head's values in the row
@@ -96,19 +108,26 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_append_kernel(const __g
       if (!a.Q) continue;
       dst = static_cast<char*>(a.Q) + ((t * a.hq + head) * a.dim + e) * CT::kBytes;
     } else {
-      if (!there) return;
+      if (!there) break;
       head -= a.hq;
       const bool val = head >= a.hkv;
       if (val) head -= a.hkv;
       dst = static_cast<char*>(val ? a.V : a.K) + (pg * a.page_stride + head * a.head_stride + off * a.token_stride + e) * CT::kBytes;
     }
-    if (!turns) {
-      *reinterpret_cast<uint4*>(dst) = append_vec<XT, CT>(row, first + e);
-      continue;
-    }
+    // every lane's loads first: a warp's lanes turn and copy side by side
+    const bool halves = turns && !r.pairs && whole;
+    if (halves && e >= half) continue;  // made with its partner
+    RotaryValues<XT, N> own, partner;
+    own.load(row, first + e);
+    if (halves) partner.load(row, first + half + e);
     float x[N], y[N];
-    if (r.pairs) {
-      rotary_load<XT, N>(row, first + e, x);
+    own.floats(x);
+    if (!turns) {
+      if constexpr (XT::kBytes == CT::kBytes)
+        *reinterpret_cast<uint4*>(dst) = own.v[0];
+      else
+        rotary_store<CT, N>(dst, x);
+    } else if (r.pairs) {
 #pragma unroll
       for (int z = 0; z < N; z += 2) {
         const bool in = e + z < r.turned;
@@ -117,11 +136,9 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_append_kernel(const __g
         y[z + 1] = in ? fmaf(x[z + 1], cs.x, x[z] * cs.y) : x[z + 1];
       }
       rotary_store<CT, N>(dst, y);
-    } else if (whole) {
-      if (e >= half) continue;  // made with its partner
+    } else if (halves) {
       float p[N], q[N];
-      rotary_load<XT, N>(row, first + e, x);
-      rotary_load<XT, N>(row, first + half + e, p);
+      partner.floats(p);
 #pragma unroll
       for (int z = 0; z < N; ++z) {
         const float2 cs = s_turn[e + z];
@@ -131,7 +148,6 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_append_kernel(const __g
       rotary_store<CT, N>(dst, y);
       rotary_store<CT, N>(dst + half * CT::kBytes, q);
     } else {
-      rotary_load<XT, N>(row, first + e, x);
 #pragma unroll
       for (int z = 0; z < N; ++z) {
         const int el = e + z;
@@ -152,7 +168,10 @@ cudaError_t launch_rotary_append(const RotaryArgs& r, gsi_dtype xdt, gsi_dtype c
   const AppendArgs& a = r.to;
   const int n_vec = (a.hq + 2 * a.hkv) * (a.dim / (cdt == GSI_BF16 ? 8 : 4));
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(a.T, (n_vec + 2 * kRotaryThreads - 1) / (2 * kRotaryThreads));
+  // many tokens: a CTA each, which forms its angles once (three CTAs a token of 48 heads of 256 took 32 us for 2048 tokens, one
+  // %%ONE%%); few: spread over the SMs
+  const int parts = (n_vec + 2 * kRotaryThreads - 1) / (2 * kRotaryThreads);
+  cfg.gridDim = dim3(a.T, a.T >= 2 * sm_count() ? 1 : parts);
   cfg.blockDim = dim3(kRotaryThreads);
   cfg.stream = s;
   cudaLaunchAttribute at[1];

@@ -25,7 +25,7 @@ constexpr int kVfUnroll = 8;  // loads of each row in flight a lane
 
 // A probability within 0 .. 1 (NaN: 0) as hi 2^-23 + lo 2^-46, both rounded to nearest: adding 1 leaves x's multiple of
 // 2^-23 in the sum's lower bits, and the rest, which is exact, added to 1.5 2^-23 its multiple of 2^-46.  (Conversions to
-// 64-bit numbers run at a fraction of the rate: 88 us with them where this takes %%US%%, 64 rows of 100003.)
+// 64-bit numbers run at a fraction of the rate: 88 us with them where this takes 20, 64 rows of 100003.)
 __device__ __forceinline__ int2 vf_split(float x) {
   x = __saturatef(x);
   const float h = __fadd_rn(x, 1.f), l = __fadd_rn(__fsub_rn(x, __fsub_rn(h, 1.f)), 0x1.8p-23f);
