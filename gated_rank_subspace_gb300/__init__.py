@@ -933,13 +933,12 @@ def cache_evict(cache: PagedCache, kv_len: torch.Tensor, table: torch.Tensor, ma
     if offsets is not None:
         _ints("offsets", offsets, R, dev)
     m = marks.desc(cache, dev)
-    with _on_stream(stream):
-        if kept is None:
-            kept = torch.empty_like(kv_len)
-        if offsets_out is None:
-            offsets_out = torch.empty_like(kv_len)
-        if workspace is None:
-            workspace = new_workspace(cache_evict_workspace_size(cache, R, budget), kv_len.device, stream)
+    if kept is None or offsets_out is None or workspace is None:
+        with _on_stream(stream):
+            kept = torch.empty_like(kv_len) if kept is None else kept
+            offsets_out = torch.empty_like(kv_len) if offsets_out is None else offsets_out
+            if workspace is None:
+                workspace = new_workspace(cache_evict_workspace_size(cache, R, budget), kv_len.device, stream)
     _ints("kept", kept, R, dev)
     _ints("offsets_out", offsets_out, R, dev)
     if workspace.get_device() != dev or not workspace.is_contiguous():
@@ -987,13 +986,12 @@ def verify_drafts(target: torch.Tensor, draft, tokens: torch.Tensor, uniforms: t
         _ints("kv_len", kv_len, R, dev)
     elif kept is not None:
         raise ValueError("kept needs kv_len")
-    with _on_stream(stream):
-        if out is None:
-            out = torch.empty(N, dtype=_I32, device=target.device)
-        if accepted is None:
-            accepted = torch.empty(R, dtype=_I32, device=target.device)
-        if kept is None and kv_len is not None:
-            kept = torch.empty(R, dtype=_I32, device=target.device)
+    if out is None or accepted is None or (kept is None and kv_len is not None):
+        with _on_stream(stream):
+            out = torch.empty(N, dtype=_I32, device=target.device) if out is None else out
+            accepted = torch.empty(R, dtype=_I32, device=target.device) if accepted is None else accepted
+            if kept is None and kv_len is not None:
+                kept = torch.empty(R, dtype=_I32, device=target.device)
     _ints("out", out, N, dev)
     _ints("accepted", accepted, R, dev)
     if kept is not None:
@@ -1022,11 +1020,10 @@ def paged_trim(kv_len: torch.Tensor, kept: torch.Tensor, table: torch.Tensor, fr
     _ints("table", table, R * width, dev)
     _ints("free_pages", free_pages, capacity, dev)
     _ints("n_free", n_free, 1, dev)
-    with _on_stream(stream):
-        if n_free_out is None:
-            n_free_out = torch.empty_like(n_free)
-        if status is None:
-            status = torch.empty_like(n_free)
+    if n_free_out is None or status is None:
+        with _on_stream(stream):
+            n_free_out = torch.empty_like(n_free) if n_free_out is None else n_free_out
+            status = torch.empty_like(n_free) if status is None else status
     _ints("n_free_out", n_free_out, 1, dev)
     _ints("status", status, 1, dev)
     _check(lib().gsi_paged_trim(kv_len.data_ptr(), kept.data_ptr(), R, table.data_ptr(), width, free_pages.data_ptr(),

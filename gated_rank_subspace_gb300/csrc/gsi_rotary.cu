@@ -169,7 +169,7 @@ cudaError_t launch_rotary_append(const RotaryArgs& r, gsi_dtype xdt, gsi_dtype c
   const int n_vec = (a.hq + 2 * a.hkv) * (a.dim / (cdt == GSI_BF16 ? 8 : 4));
   cudaLaunchConfig_t cfg{};
   // many tokens: a CTA each, which forms its angles once (three CTAs a token of 48 heads of 256 took 32 us for 2048 tokens, one
-  // %%ONE%%); few: spread over the SMs
+  // 29); few: spread over the SMs
   const int parts = (n_vec + 2 * kRotaryThreads - 1) / (2 * kRotaryThreads);
   cfg.gridDim = dim3(a.T, a.T >= 2 * sm_count() ? 1 : parts);
   cfg.blockDim = dim3(kRotaryThreads);

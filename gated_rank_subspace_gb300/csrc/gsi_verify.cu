@@ -20,8 +20,8 @@ namespace gsi {
 // the CTA whose stretch holds the token looks through the warp's part of it again,
 // all its threads four tokens each.  The bytes of the one row of p and q bound it,
 // for few requests the chain of loads and exchanges.
-constexpr int kVfThreads = 512, kVfWarps = kVfThreads / 32, kVfMost = 8;
-constexpr int kVfUnroll = 8;  // loads of each row in flight a lane
+constexpr int kVfThreads = 256, kVfWarps = kVfThreads / 32, kVfMost = 8;
+constexpr int kVfUnroll = 2;  // groups of 8 tokens of each row in flight a lane
 
 // A probability within 0 .. 1 (NaN: 0) as hi 2^-23 + lo 2^-46, both rounded to nearest: adding 1 leaves x's multiple of
 // 2^-23 in the sum's lower bits, and the rest, which is exact, added to 1.5 2^-23 its multiple of 2^-46.  (Conversions to
@@ -32,6 +32,18 @@ __device__ __forceinline__ int2 vf_split(float x) {
   return make_int2(__float_as_int(h) - __float_as_int(1.f), __float_as_int(l) - __float_as_int(0x1.8p-23f));
 }
 
+// Eight values from element e on (a multiple of 16 bytes), or zeros.
+template <class T>
+__device__ __forceinline__ void vf_load8(const void* base, int64_t e, bool there, float (&f)[8]) {
+  const char* at = static_cast<const char*>(base) + e * T::kBytes;
+#pragma unroll
+  for (int i = 0; i < 8; i += T::kPerVec) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (there) v = ld_cg_v4(at + i * T::kBytes);
+    T::unpack(v, f + i);
+  }
+}
+
 struct VfShared {
   unsigned long long total;           // of this CTA (read by the cluster)
   unsigned long long warps[kVfWarps];
@@ -39,7 +51,7 @@ struct VfShared {
 };
 
 template <class TT, class DT>
-__global__ void __launch_bounds__(kVfThreads, 2) verify_drafts_kernel(const __grid_constant__ VerifyArgs a) {
+__global__ void __launch_bounds__(kVfThreads, 4) verify_drafts_kernel(const __grid_constant__ VerifyArgs a) {
   __shared__ VfShared sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int C = int(cluster.num_blocks()), c = int(cluster.block_rank());
@@ -93,14 +105,35 @@ __global__ void __launch_bounds__(kVfThreads, 2) verify_drafts_kernel(const __gr
   const bool both = a.draft != nullptr;
   for (;;) {
     unsigned long long sum = 0;
-    for (int x = y0 + lane; x < y1; x += 32 * kVfUnroll) {
-      float p[kVfUnroll], q[kVfUnroll];
+    // 16 bytes at a time where the rows' addresses allow it (an odd vocabulary's do from some token on, both rows alike where
+    // their types are), one by one before and behind
+    const bool two = both && left;
+    const int64_t pr = t * a.target_stride, qr = two ? t * a.draft_stride : 0;
+    auto one = [&](int x) { sum += mass(TT::load1_cg(a.target, pr + x), two ? DT::load1_cg(a.draft, qr + x) : 0.f, x); };
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(a.target) + (pr + y0) * TT::kBytes;
+    int z0 = y0 + int((16 - (pa & 15)) & 15) / TT::kBytes, z1 = z0;
+    if (z0 < y1 && (!two || ((reinterpret_cast<uintptr_t>(a.draft) + (qr + z0) * DT::kBytes) & 15) == 0)) z1 = z0 + (y1 - z0) / 8 * 8;
+    z0 = min(z0, z1 = min(z1, y1));
+    for (int x = y0 + lane; x < z0; x += 32) one(x);
+    for (int x = z0 + 8 * lane; x < z1; x += 256 * kVfUnroll) {
+      float p[kVfUnroll][8], q[kVfUnroll][8];
 #pragma unroll
-      for (int i = 0; i < kVfUnroll; ++i) p[i] = x + 32 * i < y1 ? p_at(t, x + 32 * i) : 0.f;
+      for (int i = 0; i < kVfUnroll; ++i) vf_load8<TT>(a.target, pr + x + 256 * i, x + 256 * i < z1, p[i]);
 #pragma unroll
-      for (int i = 0; i < kVfUnroll; ++i) q[i] = both && left && x + 32 * i < y1 ? q_at(t, x + 32 * i) : 0.f;
+      for (int i = 0; i < kVfUnroll; ++i) vf_load8<DT>(a.draft, qr + x + 256 * i, two && x + 256 * i < z1, q[i]);
 #pragma unroll
-      for (int i = 0; i < kVfUnroll; ++i) sum += mass(p[i], q[i], x + 32 * i);
+      for (int i = 0; i < kVfUnroll; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum += mass(p[i][e], q[i][e], x + 256 * i + e);
+    }
+    for (int x = z1 + lane; x < y1; x += 32 * 8) {
+      float p[8], q[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[i] = x + 32 * i < y1 ? TT::load1_cg(a.target, pr + x + 32 * i) : 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[i] = two && x + 32 * i < y1 ? DT::load1_cg(a.draft, qr + x + 32 * i) : 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += mass(p[i], q[i], x + 32 * i);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -132,15 +165,15 @@ __global__ void __launch_bounds__(kVfThreads, 2) verify_drafts_kernel(const __gr
     if (at < base || at >= base + sh.total) break;  // in another CTA's stretch
     int w = 0;
     for (; at >= base + sh.warps[w]; ++w) base += sh.warps[w];
-    const int z0 = x0 + int(int64_t(x1 - x0) * w / kVfWarps), z1 = x0 + int(int64_t(x1 - x0) * (w + 1) / kVfWarps);
-    for (int z = z0; z < z1; z += 4 * kVfThreads) {
+    const int f0 = x0 + int(int64_t(x1 - x0) * w / kVfWarps), f1 = x0 + int(int64_t(x1 - x0) * (w + 1) / kVfWarps);
+    for (int z = f0; z < f1; z += 4 * kVfThreads) {
       long long m[4];
       float p[4], q[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int x = z + 4 * tid + i;
-        p[i] = x < z1 ? p_at(t, x) : 0.f;
-        q[i] = both && left && x < z1 ? q_at(t, x) : 0.f;
+        p[i] = x < f1 ? p_at(t, x) : 0.f;
+        q[i] = both && left && x < f1 ? q_at(t, x) : 0.f;
       }
       unsigned long long mine = 0;
 #pragma unroll
@@ -185,7 +218,7 @@ template <class TT, class DT>
 static cudaError_t launch_vf(const VerifyArgs& a, cudaStream_t s) {
   // as many CTAs a request as there are SMs for, of 4096 tokens at least
   unsigned C = 1;
-  while (C < unsigned(kVfMost) && int64_t(a.n_req) * C * 2 <= 2 * sm_count() && a.vocab > int64_t(C) * 4096) C *= 2;
+  while (C < unsigned(kVfMost) && int64_t(a.n_req) * C * 2 <= 4 * sm_count() && a.vocab > int64_t(C) * 2048) C *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(unsigned(a.n_req) * C);
   cfg.blockDim = dim3(kVfThreads);

@@ -18,7 +18,7 @@ namespace gsi {
 //            of K bound it: a ring of 200 KB keeps them coming, page numbers are
 //            loaded several units ahead, and a warp brings what the keys have
 //            gathered (a unit's ~700 ns do not hold the two loads, one behind the
-//            other, that this takes a thread: 161 us with them, %%FEW%% without,
+//            other, that this takes a thread: 160 us with them, 139 without,
 //            16 requests of 8191 keys, 40 x 128);
 //   NR = 128: many.  K stays while the rows pass; the exponentials bound it (one
 //            a pair), above 128 columns the products.  (256 keys over 64 rows a
