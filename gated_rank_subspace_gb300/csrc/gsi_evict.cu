@@ -336,6 +336,7 @@ __global__ void __launch_bounds__(kEvThreads, 2) cache_evict_kernel(const __grid
         a.weight[now.d] = __ldcg(a.weight + now.s);
     }
     ok = __all_sync(0xffffffffu, bar_wait(&sh.bar[warp], phase, a.err));
+    if (!ok) bar_wait(&sh.bar[warp], phase, a.err, kSpinCyclesAfterError);  // the copies in flight land before the CTA leaves
     if (ok && there)
       asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(base + now.to), "r"(sa(buf + lane * a.row_bytes)),
                    "r"(uint32_t(a.row_bytes))

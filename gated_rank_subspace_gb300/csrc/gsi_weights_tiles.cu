@@ -18,7 +18,7 @@ namespace gsi {
 //            of K bound it: a ring of 200 KB keeps them coming, page numbers are
 //            loaded several units ahead, and a warp brings what the keys have
 //            gathered (a unit's ~700 ns do not hold the two loads, one behind the
-//            other, that this takes a thread: 160 us with them, 139 without,
+//            other, that this takes a thread: 160 us with them, 143 without,
 //            16 requests of 8191 keys, 40 x 128);
 //   NR = 128: many.  K stays while the rows pass; the exponentials bound it (one
 //            a pair), above 128 columns the products.  (256 keys over 64 rows a
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(KtCfg<NS, NR>::kThreads, 1)
     }
     for (int i = 0; i < C::kMarks; ++i) {
       bar_init(&bars.mark_full[i], 33);
-      bar_init(&bars.mark_empty[i], 4);
+      bar_init(&bars.mark_empty[i], 8);
     }
     bar_init(&bars.done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -427,8 +427,9 @@ __global__ void __launch_bounds__(KtCfg<NS, NR>::kThreads, 1)
         asm volatile("bar.sync 3, 256;" ::: "memory");
         if (ends) sum += theirs[row];
       }
-      if (!ends) continue;
       if (loaded) {
+        // Both warpgroups wait for the marks and give their place in the ring back: the next unit there may be the other one's,
+        // and a parity tells a phase from its neighbours only.
         ok = ok && __all_sync(0xffffffffu, bar_wait(&bars.mark_full[mb], mp, err));
         if (!ok) continue;
         mark.old = s_old[mb * 128 + row];
@@ -437,6 +438,7 @@ __global__ void __launch_bounds__(KtCfg<NS, NR>::kThreads, 1)
         if (lane == 0) bar_arrive(&bars.mark_empty[mb]);
         if (pg >= 0 && key < g.q.len) mark.at = ((int64_t(pg) * a.hkv + g.h) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
       }
+      if (!ends) continue;
       if (whole) {
         kw_give(a, g, key, mark, sum);
         continue;

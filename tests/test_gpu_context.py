@@ -196,6 +196,23 @@ def test_key_weights(gsi, lens, dt, hq, hkv, D, page):
     Weights(gsi, dt, hq, hkv, D, page, lens).check(max_q=max(1, max(q for q, _ in lens)))
 
 
+@pytest.mark.parametrize("dt,D", [(BF, 8), (BF, 16), (BF, 40), (BF, 136), (F, 4), (F, 100), (F, 252)])
+@pytest.mark.parametrize("lens", [[(1, 77), (1, 3)], [(3, 200), (1, 1)], [(70, 300)]], ids=str)
+def test_key_weights_odd_head_sizes(gsi, dt, D, lens):
+    Weights(gsi, dt, 4, 2, D, 32, lens).check(max(q for q, _ in lens))
+
+
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 32), (256, 16)])
+def test_key_weights_of_units_of_one_and_more_steps(gsi, D, page):
+    # a few-row kernel's units of one, two and five steps in turn: the warpgroups change places, and whose turn a place in the
+    # rings is
+    lens = [(1, 500), (20, 400), (1, 900), (33, 300), (1, 130), (70, 200)] * 4
+    w = Weights(gsi, BF, 2, 2, D, page, lens, held=[max(0, n - q) for q, n in lens])
+    ref = w.check(1)
+    for _ in range(3):
+        assert torch.equal(w.run(1).weight, ref.weight)
+
+
 @pytest.mark.parametrize("dt", [BF, F])
 @pytest.mark.parametrize("lens", [[(1, 77), (1, 3)], [(20, 300), (0, 200), (1, 130)], [(130, 260)]], ids=str)
 def test_key_weights_gathered_over_steps(gsi, dt, lens):
@@ -257,7 +274,7 @@ def test_key_weights_rows_without_a_sum(gsi, dt):
     w.check()
 
 
-@pytest.mark.parametrize("dt,D,hq,hkv,lens", [(BF, 128, 8, 8, [(1, 3000), (1, 9000)]), (BF, 64, 8, 1, [(600, 600)]), (BF, 256, 4, 4, [(500, 1200)]),
+@pytest.mark.parametrize("dt,D,hq,hkv,lens", [(BF, 128, 8, 8, [(1, 3000), (1, 9000)]), (BF, 128, 32, 32, [(1, 8000)] * 6), (BF, 256, 16, 16, [(1, 6000)] * 4), (BF, 64, 8, 1, [(600, 600)]), (BF, 256, 4, 4, [(500, 1200)]),
                                               (F, 64, 4, 4, [(300, 700), (1, 2000)])])
 def test_key_weights_long(gsi, dt, D, hq, hkv, lens):
     g = gen(D)
@@ -275,7 +292,7 @@ def test_key_weights_long(gsi, dt, D, hq, hkv, lens):
     work = gsi.new_workspace(gsi.key_weights_workspace_size())
     gsi.key_weights(cache, Q, lse, qs, kv, tab, marks, max_q=max(q for q, _ in lens), workspace=work)
     gsi.key_weights(cache, Q, lse, qs, kv, tab, again, max_q=max(q for q, _ in lens), workspace=work)
-    assert torch.equal(marks.weight, again.weight)
+    assert torch.equal(marks.weight, again.weight) and gsi.workspace_status(work) == 0
     assert not work.any() or not work[256:256 + 4096].any()  # the counters are back at zero
     a = 0
     for r, (q, n) in enumerate(lens):
@@ -293,6 +310,59 @@ def test_key_weights_long(gsi, dt, D, hq, hkv, lens):
             # what all rows give is one each, but for the rounding of the weights that were summed
             assert abs(want.sum().item() - q * (hq // hkv)) <= 2**-8 * q * (hq // hkv)
         a += q
+
+
+@pytest.mark.parametrize("dt,hq,hkv", [(BF, 2, 1), (F, 2, 1)])
+def test_key_weights_of_many_requests(gsi, dt, hq, hkv):
+    rng = np.random.default_rng(3)
+    lens = [(int(q), int(q + n)) for q, n in zip(rng.integers(0, 3, 700), rng.integers(0, 40, 700))]
+    Weights(gsi, dt, hq, hkv, 32, 16, lens, held=[max(0, n - q) for q, n in lens], offsets=rng.integers(0, 9, 700).tolist()).check(2)
+
+
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("lens", [[(1, 700), (1, 20)], [(40, 300), (200, 260)]], ids=str)
+def test_key_weights_on_another_stream_and_in_graphs(gsi, dt, lens):
+    """One workspace for the attention, the weights and the eviction, in two graphs of a stream, replayed in turn."""
+    w = Weights(gsi, dt, 4, 2, 64, 16, lens)
+    ref = w.run().weight
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = w.run(stream=s)
+    s.synchronize()
+    assert torch.equal(got.weight, ref)
+    N, hq = w.Q.shape[:2]
+    ws = gsi.new_workspace(max(gsi.paged_attention_workspace_size(w.cache, hq), gsi.key_weights_workspace_size(),
+                               gsi.cache_evict_workspace_size(w.cache, len(lens), 16)))
+    args = (i32(w.q_start), i32(w.kv_len), i32(w.table))
+    out, lse = torch.empty_like(w.Q), torch.empty(N, hq, device="cuda")
+    a, b = (gsi.KeyMarks(w.marks.weight.clone(), w.marks.place.clone()) for _ in range(2))
+    kept, gone = torch.empty_like(args[1]), torch.empty_like(args[1])
+    want = gsi.paged_attention(w.cache, w.Q, *args)
+    torch.cuda.synchronize()
+    first, second = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(first):
+        gsi.paged_attention(w.cache, w.Q, *args, out=out, lse=lse, workspace=ws)
+        gsi.key_weights(w.cache, w.Q, w.lse, *args, a, workspace=ws)
+    scratch = gsi.PagedCache(w.cache.K.clone(), w.cache.V.clone())
+    with torch.cuda.graph(second):
+        gsi.key_weights(w.cache, w.Q, w.lse, *args, b, workspace=ws)
+        gsi.cache_evict(scratch, args[1], args[2], gsi.KeyMarks(b.weight, b.place), 16, kept=kept, offsets_out=gone, workspace=ws)
+    keep = None
+    for _ in range(3):
+        a.weight.zero_(), b.weight.zero_(), out.zero_()
+        scratch.K.copy_(w.cache.K), scratch.V.copy_(w.cache.V)
+        first.replay(), second.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        table, valid = args[2].long(), [n for _, n in lens]
+        for r, n in enumerate(valid):
+            pg = table[r, torch.arange(n, device="cuda") // 16]
+            assert torch.equal(a.weight[pg, :, torch.arange(n, device="cuda") % 16], ref[pg, :, torch.arange(n, device="cuda") % 16])
+        assert kept.tolist() == [min(16, n) for n in valid]
+        now = (scratch.K.clone(), b.weight.clone(), b.place.clone())
+        assert keep is None or all(torch.equal(x, y) for x, y in zip(keep, now))
+        keep = now
+    assert gsi.workspace_status(ws) == 0
 
 
 # ------------------------------------------------------------------ the attention's logarithms
@@ -390,6 +460,20 @@ def test_evict_with_table_entries_outside_the_cache(gsi):
     evict_case(gsi, BF, 2, 16, 16, [200, 100], 40, 5, 2, edit=edit)
 
 
+def test_evict_in_a_permuted_cache(gsi):
+    lens, hkv, D, page = [200, 90, 30], 3, 40, 16
+    table, pages = paged(lens, page, 1, gen(1))
+    K, V = (torch.randn(pages, hkv, page, D, device="cuda", generator=gen(2)).to(BF) for _ in range(2))
+    W, P = torch.randn(pages, hkv, page, device="cuda", generator=gen(3)), torch.arange(pages * hkv * page, device="cuda").int().view(pages, hkv, page)
+    got = []
+    for layout in (lambda t: t.clone(), lambda t: t.transpose(1, 2).contiguous().transpose(1, 2)):
+        for budget in (50, 199):
+            cache, marks = gsi.PagedCache(layout(K), layout(V)), gsi.KeyMarks(W.clone(), P.clone())
+            gsi.cache_evict(cache, i32(lens), i32(table), marks, budget)
+            got.append((cache.K, cache.V, marks.weight, marks.place))
+    assert all(torch.equal(a, b) for i in (0, 1) for a, b in zip(got[i], got[i + 2]))
+
+
 def test_evict_keeps_the_last_and_first_positions(gsi):
     n, budget = 300, 60
     cache, marks = evict_case(gsi, BF, 3, 16, 16, [n], budget, recent=20, sinks=4, offsets=[50], weights=lambda w: -w.abs())
@@ -429,6 +513,51 @@ def test_evict_on_another_stream_and_in_a_graph(gsi):
         assert all(torch.equal(a, b) for a, b in zip(ref, (cache.K, cache.V, marks.weight, marks.place, kept, out)))
 
 
+def test_offsets_beyond_32_bits(gsi):
+    # a cache of more than 2^31 elements, the request's pages at its far end and at its beginning
+    hkv, D, page, k, hq = 8, 128, 64, 300, 16
+    n_pages = 2**31 // (hkv * D * page) + 40
+    big = gsi.PagedCache(*(torch.empty(n_pages, hkv, page, D, dtype=BF, device="cuda") for _ in range(2)))
+    table, order = i32([[n_pages - 1, 0, n_pages - 7, n_pages - 2, 3]]), i32([[0, 1, 2, 3, 4]])
+    small = gsi.PagedCache(*(torch.randn(5, hkv, page, D, device="cuda", generator=gen(6)).to(BF) for _ in range(2)))
+    at = table[0].long()
+    big.K[at], big.V[at] = small.K, small.V
+    bm, sm = gsi.KeyMarks.empty(big), gsi.KeyMarks.empty(small)
+    for q in (1, 130):
+        Q = torch.randn(q, hq, D, device="cuda", generator=gen(q)).to(BF)
+        lse = torch.empty(q, hq, device="cuda")
+        gsi.paged_attention(small, Q, i32([0, q]), i32([k]), order, lse=lse)
+        gsi.key_weights(big, Q, lse, i32([0, q]), i32([k]), table, bm)
+        gsi.key_weights(small, Q, lse, i32([0, q]), i32([k]), order, sm)
+        seen = torch.arange(5 * page, device="cuda").view(5, 1, page).expand(5, hkv, page) < k
+        assert torch.equal(bm.weight[at][seen], sm.weight[seen]) and torch.equal(bm.place[at][seen], sm.place[seen])
+    for budget in (299, 77):
+        kept, _ = gsi.cache_evict(big, i32([k]), table, bm, budget, 10, 2)
+        gsi.cache_evict(small, i32([k]), order, sm, budget, 10, 2)
+        seen = torch.arange(5 * page, device="cuda").view(5, 1, page).expand(5, hkv, page) < k
+        assert kept.item() == budget and torch.equal(big.K[at], small.K) and torch.equal(big.V[at], small.V)
+        assert torch.equal(bm.weight[at][seen], sm.weight[seen]) and torch.equal(bm.place[at][seen], sm.place[seen])
+        k = budget
+    rows = torch.randn(1, (hq + 2 * hkv) * D, device="cuda", generator=gen(1))
+    gsi.rotary_append(big, rows, torch.tensor([n_pages * page - 1], device="cuda"), i32([9]), hq, gsi.Rotary.make(D))
+    gsi.rotary_append(small, rows, torch.tensor([7], device="cuda"), i32([9]), hq, gsi.Rotary.make(D))
+    assert torch.equal(big.K[-1, :, -1], small.K[0, :, 7]) and torch.equal(big.V[-1, :, -1], small.V[0, :, 7])
+
+
+def test_wide_probability_rows_beyond_32_bits(gsi):
+    # rows more than 2^31 elements into the probabilities
+    N, V = 4, 3000
+    stride = 2**30
+    wide = torch.empty((N - 1) * stride + V, dtype=BF, device="cuda")
+    target = wide.as_strided((N, V), (stride, 1))
+    p = torch.softmax(3 * torch.randn(N, V, device="cuda", generator=gen(2)), -1).to(BF)
+    target.copy_(p)
+    tokens, u, v = i32([0, 5, int(p[1].argmax()), 7]), torch.tensor([0.0, 0.0, 0.999, 0.5], device="cuda"), torch.tensor([0.3], device="cuda")
+    tokens[1] = p[0].argmax().int()
+    a, b = (gsi.verify_drafts(t, None, tokens, u, v, i32([0, 4])) for t in (target, p))
+    assert torch.equal(a.out, b.out) and a.accepted.tolist() == b.accepted.tolist() == [2]
+
+
 # ------------------------------------------------------------------ drafts
 def verify_case(gsi, n, V, tdt=F, ddt=F, seed=0, near=1.0, edit=None, stride=0, kv=True):
     g = gen(seed)
@@ -466,6 +595,16 @@ def test_verify_many_drafts_and_blocks(gsi):
     assert verify_case(gsi, [700, 3, 600], 64, near=0.0).accepted.tolist() == [700, 3, 600]  # equal probabilities: all stand
     verify_case(gsi, [2] * 200, 9000, seed=2)
     verify_case(gsi, [2], 300_001, seed=3)
+
+
+def test_verify_leaves_rows_of_no_request(gsi):
+    target = torch.softmax(torch.randn(9, 50, device="cuda", generator=gen(8)), -1)
+    tokens, u, v = i32(range(9)), torch.full((9,), 2.0, device="cuda"), torch.tensor([0.5, 0.5], device="cuda")
+    out = torch.full((9,), -7, dtype=torch.int32, device="cuda")
+    got = gsi.verify_drafts(target, None, tokens, u, v, i32([2, 4, 7]), out=out)
+    assert got.accepted.tolist() == [0, 0] and out[[0, 1, 7, 8]].tolist() == [-7] * 4 and out[[3, 5, 6]].tolist() == [-1] * 3
+    none = gsi.verify_drafts(target[:0], None, tokens[:0], u[:0], v, i32([0, 0, 0]), kv_len=i32([5, 6]))
+    assert none.accepted.tolist() == [0, 0] and none.kept.tolist() == [5, 6]
 
 
 def test_verify_borders(gsi):
@@ -648,6 +787,30 @@ def test_drafted_steps_in_one_graph(gsi):
         assert out.tolist() == want[0] and acc.tolist() == want[1] and kept.tolist() == want[2]
         w = co.trim(kv.tolist(), want[2], table.cpu().numpy(), [-1] * 20, 0, page)
         assert free.tolist() == w[0] and left.item() == w[1] and status.item() == 0
+
+
+def test_rotary_verify_and_trim_on_another_stream(gsi):
+    s = torch.cuda.Stream()
+    rows, slots, pos = torch.randn(9, 6 * 64, device="cuda", generator=gen(3)), torch.randperm(32, device="cuda", generator=gen(4))[:9], i32(range(50, 59))
+    a, b = (gsi.PagedCache(*(torch.zeros(2, 2, 16, 64, dtype=BF, device="cuda") for _ in range(2))) for _ in range(2))
+    turn = gsi.Rotary.make(64)
+    target, tokens = torch.softmax(torch.randn(6, 500, device="cuda", generator=gen(5)), -1), i32([0, 3, 9, 1, 4, 400])
+    u, v, qs, kv = torch.rand(6, device="cuda"), torch.rand(2, device="cuda"), i32([0, 4, 6]), i32([40, 60])
+    table, free = i32([[1, 2, 3, 9], [4, 5, 6, 8]]), [i32([-1] * 8) for _ in range(2)]
+    torch.cuda.synchronize()
+    q = gsi.rotary_append(a, rows, slots, pos, 2, turn)
+    r = gsi.verify_drafts(target, None, tokens, u, v, qs, kv_len=kv)
+    n = gsi.paged_trim(kv, i32([3, 0]), table, free[0], i32([0]), 16)
+    kept = i32([3, 0])
+    zero = i32([0])
+    torch.cuda.synchronize()
+    q2 = gsi.rotary_append(b, rows, slots, pos, 2, turn, stream=s)
+    r2 = gsi.verify_drafts(target, None, tokens, u, v, qs, kv_len=kv, stream=s)
+    n2 = gsi.paged_trim(kv, kept, table, free[1], zero, 16, stream=s)
+    s.synchronize()
+    assert torch.equal(q, q2) and torch.equal(a.K, b.K) and torch.equal(a.V, b.V)
+    assert torch.equal(r.out, r2.out) and torch.equal(r.accepted, r2.accepted) and torch.equal(r.kept, r2.kept)
+    assert torch.equal(free[0], free[1]) and n[0].item() == n2[0].item() == 6
 
 
 def test_tensors_elsewhere_are_refused(gsi):
