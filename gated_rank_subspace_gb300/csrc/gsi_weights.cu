@@ -7,19 +7,25 @@
 
 namespace gsi {
 
-// A unit is 64 keys, a step up to 64 query rows at a time: scores as register
-// tiles of 4 x 4 over 256 threads, keys and rows in shared memory as float32; a
-// thread adds its rows' weights to its four keys' sums, and the sixteen row
-// groups are added when the part of the unit ends, in one order.  The score, its
+// A unit is 64 keys, a step up to 64 query rows at a time (few rows: 16): scores
+// as register tiles of 4 x 4 (4 x 1) over 256 threads, keys and rows in shared
+// memory as float32; a thread adds its rows' weights to its four keys' sums, and
+// the sixteen row groups are added when the part of the unit ends, in one order.
+// Up to four CTAs an SM, so that one's loads pass under another's products
+// (few rows, where that is what bounds them: one token of 16 requests of 2048
+// keys, 16 x 128, 395 us with one CTA, all of its rows formed whether there or not,
+// 109 with three, 88 with four and a spill of 68 bytes; 1.8 TB/s).  The score, its
 // scaling and the row's logarithm meet in one fused product, exact up to its
 // result, so a weight's error is that of its score.
-constexpr int kKwKeys = 64, kKwRows = 64, kKwThreads = 256;
+constexpr int kKwKeys = 64, kKwThreads = 256;
 
-template <class T>
-__global__ void __launch_bounds__(kKwThreads, 1) key_weights_kernel(const __grid_constant__ KeyWeightArgs a, int tpt) {
+template <class T, int RM>
+__global__ void __launch_bounds__(kKwThreads, RM == 1 ? 4 : 2) key_weights_kernel(const __grid_constant__ KeyWeightArgs a, int tpt) {
+  constexpr int kKwRows = 16 * RM;
   extern __shared__ __align__(16) float kw_smem[];
   __shared__ float s_sum[kKwThreads / 32][kKwKeys];
   __shared__ float s_lse[kKwRows];
+  __shared__ float s_part[RM == 1 ? 16 : 1][kKwKeys];
   __shared__ int s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tk = tid % 16, tr = tid / 16;
@@ -70,24 +76,37 @@ __global__ void __launch_bounds__(kKwThreads, 1) key_weights_kernel(const __grid
           s_lse[tid] = __ldcg(a.LSE + int64_t(g.q.q0 + tok0 + tok) * a.hkv * a.group + head);
         }
         __syncthreads();
-        float s[4][4] = {};
+        // few rows: the row groups that are left over take a part of the columns each (a row's products in 16 / R parts, R the
+        // power of two from its rows on)
+        const int rows2 = RM > 1 || n_rows > 8 ? 16 : n_rows > 4 ? 8 : n_rows > 2 ? 4 : n_rows;
+        const int parts = RM > 1 ? 1 : 16 / rows2, mine = RM > 1 ? tr : tr % rows2, part = RM > 1 ? 0 : tr / rows2;
+        float s[RM][4] = {};
 #pragma unroll 4
-        for (int x = 0; x < d4; ++x) {
-          float4 q[4], k[4];
+        for (int x = d4 * part / parts; x < d4 * (part + 1) / parts; ++x) {
+          float4 q[RM], k[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const float4*>(sq + (tr * 4 + i) * DP + 4 * x);
+          for (int i = 0; i < RM; ++i) q[i] = *reinterpret_cast<const float4*>(sq + (mine * RM + i) * DP + 4 * x);
 #pragma unroll
           for (int n = 0; n < 4; ++n) k[n] = *reinterpret_cast<const float4*>(sk + (tk + 16 * n) * DP + 4 * x);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < RM; ++i)
 #pragma unroll
             for (int n = 0; n < 4; ++n)
               s[i][n] = fmaf(q[i].w, k[n].w, fmaf(q[i].z, k[n].z, fmaf(q[i].y, k[n].y, fmaf(q[i].x, k[n].x, s[i][n]))));
         }
+        if (parts > 1) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = tr * 4 + i;
-          if (row >= n_rows) break;
+          for (int n = 0; n < 4; ++n) s_part[tr][tk + 16 * n] = s[0][n];
+          __syncthreads();
+          if (part == 0)
+            for (int z = 1; z < parts; ++z)
+#pragma unroll
+              for (int n = 0; n < 4; ++n) s[0][n] += s_part[mine + z * rows2][tk + 16 * n];
+        }
+#pragma unroll
+        for (int i = 0; i < RM; ++i) {
+          const int row = mine * RM + i;
+          if (row >= n_rows || part > 0) break;
           const int lim = a.causal ? g.q.len - g.q.q_len + tok0 + (row0 + row) / a.group + 1 : g.q.len;
           const float lse = s_lse[row];
 #pragma unroll
@@ -134,33 +153,41 @@ __global__ void __launch_bounds__(kKwThreads, 1) key_weights_kernel(const __grid
 
 size_t key_weights_work_bytes() { return (kw_work_bytes() + 255) / 256 * 256; }
 
-template <class T>
+template <class T, int RM>
 static cudaError_t launch_kw(const KeyWeightArgs& a, cudaStream_t s) {
+  constexpr int kRows = 16 * RM;
   static OnEveryDevice ready;
   const cudaError_t e = ready([] {
-    return cudaFuncSetAttribute(key_weights_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (kKwKeys + kKwRows) * 260 * 4);
+    return cudaFuncSetAttribute(key_weights_kernel<T, RM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (kKwKeys + kRows) * 260 * 4);
   });
   if (e != cudaSuccess) return e;
   int tpt = 1;
-  while (2 * tpt * a.group <= kKwRows) tpt *= 2;
+  while (2 * tpt * a.group <= kRows) tpt *= 2;
+  const size_t smem = size_t(kKwKeys + kRows) * (a.dim + 4) * 4;
+  // One CTA an SM where that gives each two steps at most: units are cut less (64 tokens over 600 keys, 3 requests of 4 x 64:
+  // 10.2 us, with two an SM 12.3; but 256 over 2048, 4 requests, 57 and 44).  `steps` is what they would be if rows filled
+  // them and every request had the table's length.
+  const int64_t steps = std::max<int64_t>(int64_t(a.N) * a.group / kRows + 1, a.n_req) * a.hkv * ((a.width << a.page_shift) / kKwKeys + 1);
+  const int per_sm = steps <= 2 * sm_count() ? 1 : min(RM == 1 ? 4 : 2, int(233472 / (smem + 6144)));
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(min(sm_count(), kKwCtas));
+  cfg.gridDim = dim3(min(per_sm * sm_count(), kKwCtas));
   cfg.blockDim = dim3(kKwThreads);
-  cfg.dynamicSmemBytes = size_t(kKwKeys + kKwRows) * (a.dim + 4) * 4;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, key_weights_kernel<T>, a, tpt);
+  return cudaLaunchKernelEx(&cfg, key_weights_kernel<T, RM>, a, tpt);
 }
 
 cudaError_t launch_key_weights(const KeyWeightArgs& a, gsi_dtype dt, int64_t max_q, cudaStream_t s) {
-  if (dt == GSI_F32) return launch_kw<F32>(a, s);
-  if (a.N == 0) return launch_kw<BF16>(a, s);  // keys to begin at zero, without a row
+  if (a.N == 0) return dt == GSI_F32 ? launch_kw<F32, 1>(a, s) : launch_kw<BF16, 1>(a, s);  // keys to begin at zero, without a row
   // (the hint is the caller's: a step of 16 rows has to hold a token's heads)
-  return launch_key_weights_tiles(a, std::clamp<int64_t>(max_q, 1, a.N) * a.group <= 16, s);
+  const bool few = std::clamp<int64_t>(max_q, 1, a.N) * a.group <= 16;
+  if (dt == GSI_F32) return few ? launch_kw<F32, 1>(a, s) : launch_kw<F32, 4>(a, s);
+  return launch_key_weights_tiles(a, few, s);
 }
 
 }  // namespace gsi

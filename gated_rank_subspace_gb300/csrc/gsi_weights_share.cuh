@@ -21,7 +21,7 @@ namespace gsi {
 // the causal mask are t k - c, with k = KT / tpt and c = ceil((len - q_len) /
 // tpt): the steps of the first x tiles are an arithmetic series.  (A unit that no
 // row sees counts as one step: its keys may have to begin at zero.)
-constexpr int kKwCtas = 304;  // CTAs of a launch, at most: two an SM
+constexpr int kKwCtas = 608;  // CTAs of a launch, at most: four an SM
 
 struct KwReq {
   int q0, q_len, len, held;
