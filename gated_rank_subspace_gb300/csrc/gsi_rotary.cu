@@ -17,9 +17,10 @@ namespace gsi {
 // one integer product.  Its nearest quarter turn is taken off, and what is left
 // (under an eighth) becomes a float32 with all its bits.
 //
-// A copy otherwise: the bytes bound it.  A CTA takes up to 512 16-byte output
-// vectors of a token and forms the token's sines and cosines once, in shared
-// memory.  With values i and turned / 2 + i, one thread makes both output
+// A copy otherwise: the bytes bound it, and a CTA's chain position, angle, barrier
+// (2048 tokens of 16 + 2 x 16 heads of 256 29 us, 5.2 TB/s; the plain append 24).  A
+// CTA takes a token, or 512 16-byte output vectors of it where tokens are few, and
+// forms the token's sines and cosines once, in shared memory.  With values i and turned / 2 + i, one thread makes both output
 // vectors where they are aligned, so that each row is read once.
 constexpr int kRotaryThreads = 256;
 

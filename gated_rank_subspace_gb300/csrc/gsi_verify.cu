@@ -19,7 +19,8 @@ namespace gsi {
 // are a few loads), then each sums a stretch of the row, a warp a stretch of that;
 // the CTA whose stretch holds the token looks through the warp's part of it again,
 // all its threads four tokens each.  The bytes of the one row of p and q bound it,
-// for few requests the chain of loads and exchanges.
+// for few requests the chain of loads and exchanges (one row of 50257 7 us, 64 of
+// 100003 20, 16 of 250002 bf16 probabilities 18, which take 25 one value at a time).
 constexpr int kVfThreads = 256, kVfWarps = kVfThreads / 32, kVfMost = 8;
 constexpr int kVfUnroll = 2;  // groups of 8 tokens of each row in flight a lane
 
