@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kEvThreads, 2) cache_evict_kernel(const __grid
       place[i] = there ? __ldcg(a.place + at) : 0;
     }
 #pragma unroll
-    for (int i = 0; i < N; ++i)  // (no key: a place outside the cache goes first)
+    for (int i = 0; i < N; ++i)  // (a place outside the cache has no key: the lowest)
       out[i] = pg[i] < 0 || pg[i] >= a.n_pages ? 0
                : place[i] >= newest            ? 0xffffffffu
                : place[i] < a.sinks            ? 0xfffffffeu

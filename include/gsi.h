@@ -577,8 +577,8 @@ gsi_status gsi_key_weights(const gsi_cache_desc* cache, const void* Q, int64_t q
  * chosen for each key/value head by itself: those that came in at the last
  * `recent` positions (place >= kv_len + offsets - recent), then those of the
  * first `sinks` (place < sinks), then those of the largest weight, ties to the
- * lowest index; a NaN counts as the lowest weight, a key whose table entry
- * lies outside the cache goes first.  recent + sinks <= budget, budget >= 1.
+ * lowest index; NaN, and any key whose table entry lies outside the cache,
+ * counts as the lowest weight.  recent + sinks <= budget, budget >= 1.
  * The kept keys among 0 .. budget - 1 stay, the others move, K, V and marks, in
  * their order into the places given up, in theirs; what lies behind `budget`
  * is left as it is.  (So the order of cached keys changes: attention without a
