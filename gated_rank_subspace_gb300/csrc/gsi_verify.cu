@@ -99,13 +99,13 @@ __global__ void __launch_bounds__(kVfThreads, 4) verify_drafts_kernel(const __gr
   }
   __syncthreads();
 
-  // ---- the first draft that does not stand
+  // ---- the first draft that does not stand, by what its probabilities count as (NaN and what is negative 0, above 1 as 1)
   auto p_at = [&](int t, int x) { return TT::load1_cg(a.target, t * a.target_stride + x); };
   auto q_at = [&](int t, int x) { return a.draft ? DT::load1_cg(a.draft, t * a.draft_stride + x) : 1.f; };
   for (int i = tid; i < n; i += kVfThreads) {
     const int t = t0 + i, d = __ldcg(a.tokens + t + 1);
     // (the product of two float32 is exact in 64 bits; a token outside the vocabulary has no probability)
-    const bool stands = d >= 0 && d < a.vocab && double(__ldcg(a.uniforms + t)) * double(q_at(t, d)) < double(p_at(t, d));
+    const bool stands = d >= 0 && d < a.vocab && double(__ldcg(a.uniforms + t)) * double(__saturatef(q_at(t, d))) < double(__saturatef(p_at(t, d)));
     if (!stands) {
       atomicMin(&sh.fail, i);
       break;

@@ -608,9 +608,9 @@ gsi_status gsi_cache_evict(const gsi_cache_desc* cache, const int32_t* kv_len, c
  * a token is sampled from max(target - draft, 0) (NULL: target without d), or
  * from target where that leaves nothing; behind n standing drafts from target:
  * the first token x whose running sum is above samples[r] times the whole.
- * Negative probabilities and NaN count as 0, above 1 as 1; sums are exact to
- * 2^-47 a token.  A row without any mass gives -1; samples are taken within
- * [0, 1).
+ * Negative probabilities and NaN count as 0, above 1 as 1, for drafts and for
+ * samples; sums are exact to 2^-47 a token, whatever a row adds up to.  A row
+ * without any mass gives -1; samples are taken within [0, 1).
  *   out (N)       row q_start[r] + i: the request's i-th token from here on:
  *                 the drafts that stand, the sampled token, then -1; rows
  *                 outside every request are not written

@@ -164,8 +164,8 @@ def verify(target, draft, tokens, uniforms, samples, q_start, kv_len=None):
             d = int(tokens[t + 1])
             if not 0 <= d < V:
                 break
-            q = 1.0 if draft is None else float(draft[t, d])
-            if not float(uniforms[t]) * q < float(target[t, d]):
+            q = 1.0 if draft is None else float(clean(draft[t, d]))
+            if not float(uniforms[t]) * q < float(clean(target[t, d])):
                 break
             out[t] = d
             t += 1

@@ -5,7 +5,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_context import BF, F, gsi, i32, verify_case  # noqa: F401
+from oracle import context_oracle as co
+from test_gpu_context import BF, F, f64, gsi, i32, verify_case  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +38,27 @@ def test_verify_the_widest_row(gsi, R):  # noqa: F811
         got = gsi.verify_drafts(target, None, i32([0]), torch.zeros(1, device="cuda"), samples, i32(q_start))
         # the k-th of equal tokens is the first whose running sum, k + 1, is above v times their number
         assert got.out.tolist() == [skip + int(float(samples[0]) * (V - skip))], v
+
+
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.mark.parametrize("p,q,u,stands", [
+    (0.5, NAN, 0.9, True), (0.0, NAN, 0.9, False),     # NaN counts as 0: 0 < p
+    (0.5, -0.1, 1.0, True), (0.0, -0.1, 0.5, False),   # so does what is negative
+    (-0.1, -0.5, 0.5, False), (NAN, 0.5, 0.0, False), (-0.2, 0.5, 0.0, False),
+    (0.95, 2.0, 0.9, True), (0.85, 2.0, 0.9, False),   # above 1 counts as 1
+    (INF, 2.0, 0.9, True), (3.0, 2.0, 1.0, False), (3.0, INF, 0.99, True), (1.0, INF, 1.0, False)])
+@pytest.mark.parametrize("dt", [F, BF])
+def test_verify_takes_a_draft_by_what_its_probabilities_count_as(gsi, p, q, u, stands, dt):  # noqa: F811
+    target = torch.tensor([[0.25, p, 0.25, 0.25], [1.0, 0.0, 0.0, 0.0]], device="cuda").to(dt)
+    draft = torch.tensor([[0.0, q, 0.0, 0.0], [0.0] * 4], device="cuda").to(dt)
+    us, v = torch.tensor([u, 0.0], device="cuda"), torch.tensor([0.999], device="cuda")
+    got = gsi.verify_drafts(target, draft, i32([0, 1]), us, v, i32([0, 2]))
+    assert got.accepted.tolist() == [int(stands)]
+    want = co.verify(f64(target), f64(draft), [0, 1], us.tolist(), v.tolist(), [0, 2])
+    assert got.out.tolist() == want[0] and want[1] == [int(stands)]
+    if dt is F:  # a certain draft: its 1 against what the target's probability counts as
+        got = gsi.verify_drafts(target, None, i32([0, 1]), us, v, i32([0, 2]))
+        count = min(max(p, 0.0), 1.0) if p == p else 0.0
+        assert got.accepted.tolist() == [int(float(us[0]) < count)]
