@@ -772,7 +772,7 @@ class Rotary:
 
     @classmethod
     def from_rates(cls, rates, layout: str = "half", scale: float = 1.0, device="cuda"):
-        """From the w_i in radians a position (numbers, kept in 64 bits)."""
+        """From the w_i in radians a position (numbers of up to 2^40, kept in 64 bits)."""
         n = len(rates)
         w, out = (ctypes.c_double * n)(*[float(r) for r in rates]), (ctypes.c_uint64 * n)()
         _check(lib().gsi_rotary_phases(w, n, out))

@@ -211,13 +211,14 @@ void rotary_rates(int dim, double base, int scaling, double factor, double conte
 }
 
 uint64_t rotary_phase(double rate) {
-  // the rate over 2 pi as a sum of two doubles: hi, and what its rounding and that of 1 / (2 pi) leave
+  // the rate (2^40 at most) over 2 pi as a sum of two doubles: hi, and what its rounding and that of 1 / (2 pi) leave (below
+  // 2^-14 of a turn, known to 2^-66)
   constexpr double kInv = 0.15915494309189535, kInvLow = -9.839338337591243e-18;  // 1 / (2 pi)
   const double hi = rate * kInv, lo = std::fma(rate, kInv, -hi) + rate * kInvLow;
   // 2^64 (hi - its nearest whole + lo): the difference is exact, and unsigned sums wrap as turns do
   const double a = std::ldexp(hi - std::rint(hi), 64), b = std::rint(std::ldexp(lo, 64));
   const uint64_t ua = a >= 9223372036854775808.0 ? uint64_t(1) << 63 : uint64_t(int64_t(a));
-  return ua + uint64_t(int64_t(std::fmod(b, 9223372036854775808.0)));
+  return ua + uint64_t(int64_t(b));
 }
 
 }  // namespace gsi

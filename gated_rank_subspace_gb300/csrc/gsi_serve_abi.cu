@@ -260,7 +260,8 @@ gsi_status gsi_rotary_phases(const double* rates, int64_t n, uint64_t* phases) {
   GSI_NEED(rates, 8);
   GSI_NEED(phases, 8);
   for (int64_t i = 0; i < n; ++i)
-    if (!std::isfinite(rates[i])) return refuse(GSI_ERR_INVALID_ARG, "rate %lld is not finite", (long long)i);
+    if (!(std::fabs(rates[i]) <= 1099511627776.0))
+      return refuse(GSI_ERR_INVALID_ARG, "rate %lld is not finite, or above 2^40 in magnitude", (long long)i);
   for (int64_t i = 0; i < n; ++i) phases[i] = rotary_phase(rates[i]);
   return record_error(GSI_OK, "");
 }

@@ -476,7 +476,8 @@ typedef enum gsi_rotary_scaling {
  * (rates, double) and the factor of their cosines and sines (*scale), and
  * rates as phases.  base > 1 and factor >= 1, finite; context, fast and slow
  * are looked at by YARN and BANDS (context > 0, fast > slow > 0).  A rate
- * that is not finite is refused. */
+ * that is not finite or above 2^40 in magnitude has no phase (GSI_ERR_INVALID_ARG):
+ * up to there a phase is right to 2 units. */
 gsi_status gsi_rotary_rates(int64_t dim, double base, gsi_rotary_scaling scaling, double factor, double context,
                             double fast, double slow, double* rates, float* scale);
 gsi_status gsi_rotary_phases(const double* rates, int64_t n, uint64_t* phases);
