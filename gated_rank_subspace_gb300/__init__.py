@@ -869,7 +869,9 @@ def key_weights(cache: PagedCache, Q: torch.Tensor, lse: torch.Tensor, q_start: 
     scale and causal): added to the marks of the first held[r] keys of request r
     (a plan's cached lengths), the beginning of the others', which get the
     position place + offsets[r] (cache_evict's offsets_out).  held None: no key
-    has marks yet.  Q may be the last tokens only of those that came in."""
+    has marks yet.  Q may be the last tokens only of those that came in.  No page
+    may belong to two requests (a shared beginning): their sums would overwrite
+    each other."""
     c = cache.desc()
     dev = _device("the cache", cache.K)
     shape, st = Q.shape, Q.stride()
@@ -921,7 +923,7 @@ def cache_evict(cache: PagedCache, kv_len: torch.Tensor, table: torch.Tensor, ma
     changes).  Returns (kept, offsets_out): the lengths then, and offsets plus
     the keys given up (the offsets of the next rotary_append, key_weights and
     cache_evict).  paged_trim returns the pages: once for layers that share the
-    table."""
+    table.  No page may belong to two requests."""
     c = cache.desc()
     dev = _device("the cache", cache.K)
     R = kv_len.numel()

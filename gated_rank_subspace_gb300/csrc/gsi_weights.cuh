@@ -42,7 +42,8 @@ __device__ __forceinline__ KwMark kw_mark(const KeyWeightArgs& a, const KwSeg& g
   if (key < g.q.held) m.old = __ldcg(a.weight + m.at);
   return m;
 }
-// Gives the sum of a unit's key to the key: added to what it has, or its first.
+// Gives the sum of a unit's key to the key: added to what it has, or its first.  (The key has no other writer: a page belongs
+// to one request.)
 __device__ __forceinline__ void kw_give(const KeyWeightArgs& a, const KwSeg& g, int key, const KwMark& m, float sum) {
   if (m.at < 0) return;
   if (key < g.q.held) {

@@ -423,8 +423,8 @@ gsi_status gsi_paged_plan(const int32_t* cached, const int32_t* fresh, int64_t n
  * (a negative length, or kept above kv_len), GSI_PLAN_TABLE_FULL (more pages
  * than table_width) or GSI_PLAN_NO_PAGES (*n_free outside 0 .. capacity, or no
  * room for the pages), *n_free_out receives *n_free, and free_pages stays.
- * n_free_out must not be n_free (GSI_ERR_INVALID_ARG).  n_req <= 2^20,
- * table_width * page_size < 2^31. */
+ * n_free_out must not be n_free (GSI_ERR_INVALID_ARG), and status neither of
+ * them.  n_req <= 2^20, table_width * page_size < 2^31. */
 gsi_status gsi_paged_trim(const int32_t* kv_len, const int32_t* kept, int64_t n_req, const int32_t* table,
                           int64_t table_width, int32_t* free_pages, int64_t capacity, const int32_t* n_free,
                           int64_t page_size, int32_t* n_free_out, int32_t* status, void* stream);
@@ -562,8 +562,11 @@ typedef struct gsi_key_marks {
  * Q may be the last tokens only of those that came in (the last rows of a
  * prompt), and q_len 0: keys from held on then begin at zero.  Sums are
  * float32, in one order for given shapes.  A table entry outside the cache has
- * no keys.  max_q bounds a request's tokens of Q (it chooses the kernel; a
- * wrong one costs time, not results).
+ * no keys.  A page belongs to one request and stands in its table once: marks
+ * are read, added to and written by the key's request alone, and pages that
+ * requests share (gsi_paged_attention takes them) would lose sums.
+ * max_q bounds a request's tokens of Q (it chooses the kernel; a wrong one
+ * costs time, not results).
  * workspace: zeroed once (gsi_workspace_init), one stream at a time, at least
  * gsi_key_weights_workspace_size() bytes; it may be the attention's.  Limits as
  * for gsi_paged_attention. */
