@@ -6,9 +6,73 @@ import pytest
 import torch
 
 from oracle import context_oracle as co
-from test_gpu_context import BF, F, f64, gsi, i32, verify_case  # noqa: F401
+from test_gpu_context import BF, F, f64, gen, gsi, i32, rotary_case, verify_case  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ rotary
+@pytest.mark.parametrize("xdt,cdt", [(F, BF), (BF, BF), (F, F), (BF, F)])
+@pytest.mark.parametrize("layout", ["half", "pairs"])
+@pytest.mark.parametrize("T,hq,hkv,D,page,n", [(5, 3, 3, 80, 32, 20), (37, 4, 1, 64, 16, 2), (9, 4, 4, 256, 256, 64), (4, 2, 2, 96, 16, 48), (3, 1, 1, 8, 16, 6)])
+def test_rotary_copies_what_a_key_has_beside_its_turned_values(gsi, xdt, cdt, layout, T, hq, hkv, D, page, n):  # noqa: F811
+    g = gen(T + n)
+    rows = torch.randn(T, (hq + 2 * hkv) * D, device="cuda", generator=g).to(xdt)
+    cache = gsi.PagedCache(*(torch.zeros(T // page + 1, hkv, page, D, dtype=cdt, device="cuda") for _ in range(2)))
+    slots = torch.randperm((T // page + 1) * page, device="cuda", generator=g)[:T]
+    slots[T // 2] = -1  # a token that the cache does not get
+    gsi.rotary_append(cache, rows, slots, i32(range(1000, 1000 + T)), hq, gsi.Rotary.make(n, 10000.0, layout))
+    there = slots >= 0
+    got = cache.K[(slots // page).clamp(min=0), :, slots % page][there]
+    key = rows.view(T, -1, D)[there, hq:hq + hkv]
+    assert torch.equal(got[..., n:], key[..., n:].to(cdt))  # bit for bit
+    assert not torch.equal(got[..., :n], key[..., :n].to(cdt))
+
+
+@pytest.mark.parametrize("xdt,cdt", [(F, BF), (BF, BF), (BF, F)])
+@pytest.mark.parametrize("layout", ["half", "pairs"])
+@pytest.mark.parametrize("T,hq,hkv,D,page,n", [(331, 8, 4, 64, 16, 64), (305, 3, 1, 80, 32, 20), (640, 12, 2, 128, 64, 32)])
+def test_rotary_of_a_prompt(gsi, xdt, cdt, layout, T, hq, hkv, D, page, n):  # noqa: F811
+    # (from twice the SMs on a token has one CTA, whose threads may have several vectors or none)
+    rotary_case(gsi, xdt, cdt, T, hq, hkv, D, page, n, layout, list(range(7, 7 + T)))
+
+
+# ------------------------------------------------------------------ eviction
+@pytest.mark.parametrize("R,hkv,lens,budget,recent,sinks", [
+    (30, 8, (16_385, 19_001), 9000, 500, 4),     # 240 heads: a CTA each
+    (30, 8, (16_400, 16_393), 16_384, 0, 0),     # few keys given up, more than are looked through one by one
+    (15, 8, (32_800, 34_001), 12_345, 64, 64)])  # 120 heads: two CTAs each
+def test_evict_more_keys_than_shared_memory_holds_under_many_heads(gsi, R, hkv, lens, budget, recent, sinks):  # noqa: F811
+    g = gen(R + budget)
+    D, page = 8, 256
+    n = [lens[r % 2] - r for r in range(R)]
+    width = -(-max(n) // page)
+    cache = gsi.PagedCache.empty(R * width, hkv, page, D, BF)
+    cache.K.normal_(generator=g), cache.V.normal_(generator=g)
+    table = torch.randperm(R * width, device="cuda", generator=g).int().view(R, width)
+    # rounded weights: ties, at the border too
+    marks = gsi.KeyMarks((torch.randn(R * width, hkv, page, device="cuda", generator=g) * 300).round(),
+                         torch.zeros(R * width, hkv, page, dtype=torch.int32, device="cuda"))
+    for r in range(R):
+        marks.place[table[r].long()] = torch.stack([torch.randperm(width * page, device="cuda", generator=g) for _ in range(hkv)]).int().view(hkv, width, page).transpose(0, 1)
+    flat = lambda t: torch.stack([t[table[r].long()].transpose(0, 1).flatten(1, 2) for r in range(R)])  # noqa: E731  (R, hkv, places)
+    want = [flat(t).clone() for t in (cache.K, cache.V, marks.weight, marks.place)]
+    kept, out = gsi.cache_evict(cache, i32(n), table, marks, budget, recent, sinks)
+    assert kept.tolist() == [min(budget, m) for m in n] and out.tolist() == [max(0, m - budget) for m in n]
+    for r in range(R):
+        if n[r] <= budget:
+            continue
+        for h in range(hkv):
+            w, p = want[2][r, h, :n[r]].clone(), want[3][r, h, :n[r]]
+            w[p < sinks] = 1e30
+            w[p >= n[r] - recent] = float("inf")
+            stay = torch.zeros(n[r], dtype=torch.bool, device="cuda")
+            stay[torch.sort(w, descending=True, stable=True).indices[:budget]] = True
+            gaps, movers = (~stay[:budget]).nonzero()[:, 0], stay[budget:].nonzero()[:, 0] + budget
+            for a in want:
+                a[r, h, gaps] = a[r, h, movers]
+    for a, b in zip(want, (cache.K, cache.V, marks.weight, marks.place)):
+        assert torch.equal(a, flat(b))
 
 
 # ------------------------------------------------------------------ drafts
