@@ -29,7 +29,9 @@ namespace gsi {
 // moves at 5.3 TB/s), by the chain of steps at a decode step's one key (128 heads of 1025
 // keys 6 us).
 constexpr int kEvThreads = 512, kEvWarps = kEvThreads / 32;
-constexpr int kEvHeld = 16384;   // ranks in shared memory; more are formed again in every pass
+// Ranks in a CTA's shared memory: 131,072 a head up to 57 heads (eight CTAs each), 16,384 from 229 on (one).  More are formed again
+// in every pass (256 heads of 16,385 to 16,640 keys to 8192 304 us, of 16,384 228; one key of 16,385 99, of 16,384 23).
+constexpr int kEvHeld = 16384;
 constexpr int kEvBins = 256, kEvMost = 8;
 constexpr int kEvBuf = 6144;     // bytes of a warp's rows in flight
 constexpr int kEvFew = 8;        // keys given up that are found one by one
@@ -356,7 +358,7 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t s) {
       ready([] { return cudaFuncSetAttribute(cache_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kEvSmem)); });
   if (e != cudaSuccess) return e;
   const int64_t units = int64_t(a.n_req) * a.hkv, most = a.width << a.page_shift;
-  // As many CTAs a unit as the SMs hold, of 512 keys at least.  80 heads of up to 8003 keys to 2048, us: 1 CTA each 80, 2 62, 4
+  // As many CTAs a unit as the SMs hold, where several of more than 256 places of the table each (a request may fill fewer).  80 heads of up to 8003 keys to 2048, us: 1 CTA each 80, 2 62, 4
   // (a few of them left over for a second turn) 60, 8 75.
   unsigned C = 1;
   while (C < unsigned(kEvMost) && units * C * 2 <= 3 * sm_count() && most > int64_t(C) * 512) C *= 2;

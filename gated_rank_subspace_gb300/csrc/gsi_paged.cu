@@ -221,7 +221,7 @@ cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t s) {
 // them in the same order.  As in the plan, every CTA forms the prefix sums
 // itself and writes its own slice of the pages, each finding its request by
 // bisection.  Latency bounds it: 2.9 us for 16 requests, 5.2 for 4093.
-constexpr int kTrimPages = 1024;  // pages of a CTA, at least
+constexpr int kTrimPages = 1024;  // places of the stack a CTA, at least (what is given back may be less)
 
 __device__ __forceinline__ PlanSums trim_request(const TrimArgs& a, int len, int kept) {
   const long long round = (1ll << a.page_shift) - 1;

@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kVfThreads, 4) verify_drafts_kernel(const __gr
 
 template <class TT, class DT, class Sum>
 static cudaError_t launch_vf_sum(const VerifyArgs& a, cudaStream_t s) {
-  // as many CTAs a request as there are SMs for, of 4096 tokens at least
+  // as many CTAs a request as there are SMs for (four an SM), where several of more than 1024 tokens each
   unsigned C = 1;
   while (C < unsigned(kVfMost) && int64_t(a.n_req) * C * 2 <= 4 * sm_count() && a.vocab > int64_t(C) * 2048) C *= 2;
   cudaLaunchConfig_t cfg{};

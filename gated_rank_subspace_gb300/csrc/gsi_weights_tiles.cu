@@ -20,13 +20,15 @@ namespace gsi {
 //            gathered (a unit's ~700 ns do not hold the two loads, one behind the
 //            other, that this takes a thread: 160 us with them, 143 without,
 //            16 requests of 8191 keys, 40 x 128);
-//   NR = 128: many.  K stays while the rows pass; up to 128 columns the chain of a
-//            step's sums bounds it (~1300 cycles of exponentials, loads from TMEM
-//            and waits), above the products: 8192 tokens of 32/8 x 128 284 us, of
-//            16 x 256 197 (1.40 PFLOP/s), of 32 x 64 292.  (256 keys over 64 rows a step, which
+//   NR = 128: many.  K stays while the rows pass: 8192 tokens of 32/8 x 128 284 us,
+//            of 32 x 64 292, of 16 x 256 197 (1.40 PFLOP/s).  A step takes ~1250 cycles at
+//            64 and at 128 columns, ~1750 at 256; its exponentials take 512, its
+//            products 4 a column: neither bounds it below 256 columns, nor do the
+//            sums by themselves (~1400 a step and warpgroup, which has every
+//            second step).  What does has not been found.  (256 keys over 64 rows a step, which
 //            halves the reads of Q, was no faster while the rows' logarithms
 //            bounded both: 27.0 against 24.3 us for 2048 tokens of 16 x 256, 235
-//            against 229 for 8192.)
+//            against 229 for 8192; not tried again since they do not.)
 constexpr int kKtSlab = 16384;                 // 64 columns of 128 keys
 
 template <int NS, int NR>
